@@ -226,6 +226,145 @@ int moe_prefill_run_layer(moe_prefill_t* h, const moe_layer_io_t* io, void* stre
  */
 int moe_prefill_run_layer_noalloc(const moe_prefill_params_t* p, const moe_layer_io_t* io, void* stream);
 
+/* ---------------------------------------------------- element types --- */
+
+/* Types of the activations that the few-token layer and the MXFP4 operators
+ * take and return. */
+enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 };
+
+/* -------------------------------------------------- a few tokens' layer --- */
+/*
+ * The MoE FFN layer for a few tokens: the steps after a prompt (page #663,
+ * "What", runs the prompt through the same layer), on the same weight blob and
+ * handle as moe_prefill_run_layer.
+ *
+ *   - Routing: as there (top-k by logit, ties to the lower expert, softmax over
+ *     the k).  A logit of -inf marks an expert that is not available to the
+ *     token: it gets weight 0, its slot's expert index is -1, and no weights
+ *     are read for it.  A token with no expert available (an empty slot of a
+ *     padded batch) gets y = 0.
+ *   - Activations are not quantised: x and the SwiGLU output enter the products
+ *     as 24-bit integers per block of 32 (error at most 2^-23 of the block's
+ *     largest magnitude) and all sums are fp32, so y is the layer of the 4-bit
+ *     weights to about fp32 rounding.  moe_prefill_run_layer's y differs from
+ *     it by that path's Q8 rounding of x and h.
+ *   - A block of 32 values of x that holds an infinity or a NaN makes the
+ *     token's y NaN; so does an h that leaves the fp32 range.
+ *   - Deterministic: the same bits on every run.
+ */
+typedef struct moe_decode_io {
+    uint32_t struct_size;
+    int32_t layer;             /* as moe_layer_io_t: >= 0 from the stream pool, -1 weights_dev */
+    const void* weights_dev;   /* device: a resident layer blob (layer == -1) */
+    int32_t n_tokens;          /* T >= 0 (0 is a no-op); T * top_k <= MOE_DECODE_MAX_PAIRS.
+                                  Not bounded by the handle's max_tokens */
+    int32_t dtype;             /* MOE_F32 / MOE_BF16 / MOE_F16: the type of x and y */
+    const void* x;             /* device [T, d], rows x_stride elements apart; rows 16-byte aligned */
+    int64_t x_stride;          /* >= d */
+    const float* logits;       /* device [T, E] fp32, finite or -inf; rows logits_stride apart */
+    int64_t logits_stride;     /* >= E */
+    void* y;                   /* device [T, d], rows y_stride apart, 16-byte aligned;
+                                  overwritten, and nothing between the rows; may be x */
+    int64_t y_stride;          /* >= d */
+    void* workspace;           /* device scratch, 256-byte aligned, for this call alone until it
+                                  has finished; its contents need not be kept or cleared.  Calls
+                                  that may overlap (two streams, two captured graphs) need one each */
+    uint64_t workspace_bytes;  /* >= moe_decode_workspace_size() for these T */
+    int32_t* eidx;             /* optional export [T, k]: expert of slot j, -1: none available */
+    float* weights;            /* optional export [T, k]: router weight of that slot */
+} moe_decode_io_t;
+
+#define MOE_DECODE_MAX_PAIRS 1024
+
+/* Device bytes of moe_decode_io_t::workspace for the dimensions in p, with
+ * max_tokens = the largest n_tokens.  Host only.  MOE_EINVAL on bad dimensions
+ * or max_tokens * top_k > MOE_DECODE_MAX_PAIRS. */
+int moe_decode_workspace_size(const moe_prefill_params_t* p, uint64_t* bytes);
+
+/* Enqueues the layer on `stream`.  Allocates nothing and never waits on the
+ * host, so it can be captured in a HIP graph where moe_prefill_run_layer can
+ * (layer == -1; a pool layer queues copies as there).  layer >= 0 takes the
+ * weights from the pool and queues prefetches as moe_prefill_run_layer does,
+ * an active_only pool loads the experts with rows only.
+ * Errors: MOE_EINVAL, MOE_ESTATE, MOE_EHIP, as there; nothing is enqueued on
+ * MOE_EINVAL. */
+int moe_decode_run_layer(moe_prefill_t* h, const moe_decode_io_t* io, void* stream);
+
+/* ---------------------------------------------------------------- MXFP4 --- */
+/*
+ * Matrices in MXFP4 (OCP Microscaling Formats v1.0): [M, K], K a multiple of 32,
+ * as
+ *   codes  [M][K/2]   E2M1 elements, element 2i of a row in the low nibble of
+ *                     byte i, element 2i + 1 in the high nibble; magnitudes
+ *                     0, 0.5, 1, 1.5, 2, 3, 4, 6 (codes 0-7), sign bit 8
+ *   scales [M][K/32]  one E8M0 byte s per block of 32 along K: 2^(s - 127);
+ *                     255: the whole block is NaN
+ * Row-major, no padding.  The same layout serves activations and weights (a
+ * weight matrix [N, K] is N rows).
+ *
+ * These calls need no handle: `device` names the HIP device whose memory the
+ * pointers are, and failures are read with moe_prefill_last_error(NULL).  They
+ * allocate nothing and keep no state; calls on different streams are
+ * independent, and all can be captured in a HIP graph.
+ */
+typedef struct moe_mxfp4_matrix {
+    uint32_t struct_size;
+    int32_t device;            /* HIP device ordinal */
+    int32_t dtype;             /* MOE_F32 / MOE_BF16 / MOE_F16: the type of values */
+    int32_t K;                 /* multiple of 32, >= 32 */
+    int64_t M;                 /* rows, >= 0 (0 is a no-op); M * K / 32 < 2^31 */
+    void* values;              /* device [M, K], rows `stride` elements apart; rows 16-byte aligned */
+    int64_t stride;            /* >= K */
+    uint8_t* codes;            /* device [M, K/2], 16-byte aligned */
+    uint8_t* scales;           /* device [M, K/32] */
+} moe_mxfp4_matrix_t;
+
+/* values -> codes, scales.  Scale byte: max(0, floor(log2 amax) + 125) of the
+ * block's largest magnitude (0 for a block of zeros); elements: value / scale to
+ * the nearest, ties to the even code, magnitudes above 6 to 6.  A block with an
+ * infinity or a NaN gets byte 255 and codes 0. */
+int moe_mxfp4_quantize(const moe_mxfp4_matrix_t* m, void* stream);
+/* codes, scales -> values, each rounded once to dtype (fp32 and bf16 hold every
+ * MXFP4 value below 2^128; fp16 overflows to infinity past 65504). */
+int moe_mxfp4_dequantize(const moe_mxfp4_matrix_t* m, void* stream);
+
+/*
+ * out[r, n] = sum over K of A[src(r), :] B[g(r), n, :] in fp32, rounded once to
+ * dtype; with swiglu B has 2N rows a group (N gate rows, then N up rows) and
+ * out[r, n] = silu(gate) * up.
+ *   - bounds == NULL: one matrix B, g(r) = 0.  Else group g holds the rows
+ *     [bounds[g], bounds[g+1]) of the product, as the row table of
+ *     moe_prefill_run_layer (its `bounds` export) does; groups may be empty.
+ *     Rows in no group are left as they were.
+ *   - src(r) = rows[r] / top_k with `rows` (the row table: row r holds pair
+ *     t * top_k + j, so A is [T, K] in token order); src(r) = r / top_k without.
+ *     A row index outside A is clamped into it; bounds are clamped to [0, M].
+ *   - A scale byte 255 makes the results it enters NaN.  Sums are independent of
+ *     M, of the grouping and of the other rows only within rounding: another
+ *     row count may take another split of K.
+ */
+typedef struct moe_mxfp4_gemm_args {
+    uint32_t struct_size;
+    int32_t device;
+    const uint8_t* a_codes;    /* device [a_rows, K/2], 16-byte aligned */
+    const uint8_t* a_scales;   /* device [a_rows, K/32] */
+    int64_t a_rows;            /* >= 1 if M > 0 */
+    const uint8_t* b_codes;    /* device [n_groups, N or 2N, K/2], 16-byte aligned */
+    const uint8_t* b_scales;   /* device [n_groups, N or 2N, K/32] */
+    const int32_t* bounds;     /* device [n_groups + 1], ascending within [0, M]; NULL: dense */
+    const int32_t* rows;       /* device [M]; NULL: in order */
+    int32_t n_groups;          /* 1..65535 (1 if dense) */
+    int32_t top_k;             /* >= 1 */
+    int64_t M;                 /* rows of out, >= 0 (0 is a no-op), < 2^31 */
+    int32_t N, K;              /* N >= 1, K a multiple of 32, >= 32 */
+    int32_t swiglu;            /* 0 or 1 */
+    int32_t dtype;             /* type of out */
+    void* out;                 /* device [M, N], rows out_stride elements apart */
+    int64_t out_stride;        /* >= N */
+} moe_mxfp4_gemm_args_t;
+
+int moe_mxfp4_gemm(const moe_mxfp4_gemm_args_t* a, void* stream);
+
 /* ---------------------------------------------------------- stream pool --- */
 
 typedef struct stream_pool_params {

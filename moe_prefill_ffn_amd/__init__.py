@@ -1,4 +1,5 @@
-"""MI355X-native MoE prompt (prefill) FFN layer -- Python binding.
+"""MI355X-native MoE prompt (prefill) FFN layer, the same layer for a few tokens, and the
+MXFP4 operators -- Python binding.
 
 A thin ctypes binding of ``libmoe_prefill.so`` (C ABI in
 ``include/moe_prefill.h``).  It only marshals arguments: routing, grouping,
@@ -51,6 +52,29 @@ class moe_layer_io_t(ctypes.Structure):
                 ("pos", _vp), ("xq", _vp), ("dx", _vp), ("gu", _vp), ("h", _vp), ("hq", _vp),
                 ("dh", _vp), ("dm", _vp), ("combine", _i32), ("reserved1", _i32)]
 
+
+class moe_decode_io_t(ctypes.Structure):
+    _fields_ = [("struct_size", _u32), ("layer", _i32), ("weights_dev", _vp), ("n_tokens", _i32),
+                ("dtype", _i32), ("x", _vp), ("x_stride", _i64), ("logits", _vp), ("logits_stride", _i64),
+                ("y", _vp), ("y_stride", _i64), ("workspace", _vp), ("workspace_bytes", _u64),
+                ("eidx", _vp), ("weights", _vp)]
+
+
+class moe_mxfp4_matrix_t(ctypes.Structure):
+    _fields_ = [("struct_size", _u32), ("device", _i32), ("dtype", _i32), ("K", _i32), ("M", _i64),
+                ("values", _vp), ("stride", _i64), ("codes", _vp), ("scales", _vp)]
+
+
+class moe_mxfp4_gemm_args_t(ctypes.Structure):
+    _fields_ = [("struct_size", _u32), ("device", _i32), ("a_codes", _vp), ("a_scales", _vp), ("a_rows", _i64),
+                ("b_codes", _vp), ("b_scales", _vp), ("bounds", _vp), ("rows", _vp), ("n_groups", _i32),
+                ("top_k", _i32), ("M", _i64), ("N", _i32), ("K", _i32), ("swiglu", _i32), ("dtype", _i32),
+                ("out", _vp), ("out_stride", _i64)]
+
+
+MOE_F32, MOE_BF16, MOE_F16 = 0, 1, 2
+_DTYPE_ID = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
+MOE_DECODE_MAX_PAIRS = 1024
 
 COMBINE_MODES = {"gather": 0, "atomic": 1}   # MOE_COMBINE_GATHER, MOE_COMBINE_ATOMIC
 
@@ -109,6 +133,8 @@ EXPORTED_SYMBOLS = [
     "moe_prefill_get_stats", "moe_prefill_set_log", "moe_prefill_set_timing",
     "moe_prefill_kernel_times", "moe_prefill_kernel_name",
     "moe_prefill_exp_host", "moe_prefill_exp_device", "moe_prefill_run_layer_noalloc",
+    "moe_decode_workspace_size", "moe_decode_run_layer",
+    "moe_mxfp4_quantize", "moe_mxfp4_dequantize", "moe_mxfp4_gemm",
 ]
 
 _lib = None
@@ -149,6 +175,11 @@ def lib():
                                                 ctypes.POINTER(moe_layer_io_t), _vp]
     L.moe_prefill_exp_host.argtypes = [_u32, _u64, _vp]
     L.moe_prefill_exp_device.argtypes = [_u32, _u64, _vp, _vp]
+    L.moe_decode_workspace_size.argtypes = [ctypes.POINTER(moe_prefill_params_t), ctypes.POINTER(_u64)]
+    L.moe_decode_run_layer.argtypes = [_vp, ctypes.POINTER(moe_decode_io_t), _vp]
+    L.moe_mxfp4_quantize.argtypes = [ctypes.POINTER(moe_mxfp4_matrix_t), _vp]
+    L.moe_mxfp4_dequantize.argtypes = [ctypes.POINTER(moe_mxfp4_matrix_t), _vp]
+    L.moe_mxfp4_gemm.argtypes = [ctypes.POINTER(moe_mxfp4_gemm_args_t), _vp]
     _lib = L
     return L
 
@@ -171,6 +202,7 @@ class Handle:
     def __init__(self, ptr: int, params: dict, keep=()):
         self.ptr = ptr
         self.params = params
+        self.layer_bytes = moe_prefill_layer_bytes(params["d_model"], params["d_ff"], params["n_experts"])
         self._keep = list(keep)
         self._pool_keep = []
         self._log_cb = None
@@ -348,6 +380,232 @@ def moe_prefill_run_layer_noalloc(d_model: int, d_ff: int, n_experts: int, top_k
     p = _params(d_model, d_ff, n_experts, top_k, max(T, 1), device)
     s = stream if stream is not None else torch.cuda.current_stream(x.device)
     _check(lib().moe_prefill_run_layer_noalloc(ctypes.byref(p), ctypes.byref(io), _vp(s.cuda_stream)))
+
+
+# ---------------------------------------------------- a few tokens' layer ---
+
+def _stream_of(stream: Optional[torch.cuda.Stream], device: torch.device) -> int:
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    if s.device_index != device.index:
+        raise ValueError(f"stream is on device {s.device_index}, the tensors are on {device}")
+    return s.cuda_stream
+
+
+def _rows_of(t: torch.Tensor, name: str, rows: int, cols: int, device: torch.device) -> int:
+    """Row stride of a [rows, cols] device matrix whose rows are contiguous."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name}: expected shape ({rows}, {cols}), got {tuple(t.shape)}")
+    if not t.is_cuda or t.device != device:
+        raise TypeError(f"{name}: expected a tensor on {device}, got {t.device}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    if rows <= 1:
+        return cols
+    if t.stride(0) < cols:
+        raise ValueError(f"{name}: rows overlap")
+    return t.stride(0)
+
+
+def moe_decode_workspace_size(d_model: int, d_ff: int, n_experts: int, top_k: int, max_tokens: int) -> int:
+    """Bytes of moe_decode_run_layer's workspace for up to max_tokens tokens."""
+    p = _params(d_model, d_ff, n_experts, top_k, max_tokens)
+    out = _u64()
+    _check(lib().moe_decode_workspace_size(ctypes.byref(p), ctypes.byref(out)))
+    return int(out.value)
+
+
+def moe_decode_run_layer(handle: Handle, x: torch.Tensor, logits: torch.Tensor, y: torch.Tensor,
+                         layer: int = -1, weights: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None,
+                         stream: Optional[torch.cuda.Stream] = None,
+                         exports: Optional[Dict[str, torch.Tensor]] = None) -> None:
+    """Enqueue the MoE FFN layer for a few tokens (x.shape[0] * top_k <= 1024) on ``stream``.
+
+    x, y: [T, d_model] fp32, bf16 or fp16, the same type (rows may be strided, 16-byte aligned);
+    logits: [T, n_experts] fp32, -inf where an expert is not available.  ``workspace``: device
+    uint8 scratch of moe_decode_workspace_size() bytes that no other call in flight uses;
+    without one the call takes it from torch's allocator.  exports: "eidx" int32 and
+    "weights" fp32, [T, top_k] each."""
+    P = handle.params
+    d, E, k = P["d_model"], P["n_experts"], P["top_k"]
+    T = x.shape[0]
+    if x.dtype not in _DTYPE_ID or y.dtype != x.dtype:
+        raise TypeError("x and y: expected the same of float32, bfloat16, float16")
+    if logits.dtype != torch.float32:
+        raise TypeError("logits: expected float32")
+    dev = x.device
+    if not x.is_cuda or dev.index != P["device"]:
+        raise TypeError(f"x: expected a tensor on the handle's device cuda:{P['device']}")
+    io = moe_decode_io_t()
+    io.struct_size = ctypes.sizeof(io)
+    io.layer = layer
+    io.n_tokens = T
+    io.dtype = _DTYPE_ID[x.dtype]
+    io.x_stride = _rows_of(x, "x", T, d, dev)
+    io.logits_stride = _rows_of(logits, "logits", T, E, dev)
+    io.y_stride = _rows_of(y, "y", T, d, dev)
+    io.x, io.logits, io.y = x.data_ptr(), logits.data_ptr(), y.data_ptr()
+    if layer < 0:
+        if weights is None:
+            raise ValueError("layer=-1 needs a resident weight blob")
+        if weights.device != dev:
+            raise TypeError(f"weights: expected a tensor on {dev}")
+        io.weights_dev = _dev_ptr(weights, torch.uint8, "weights", handle.layer_bytes)
+    for name, t in (exports or {}).items():
+        if name not in ("eidx", "weights"):
+            raise KeyError(name)
+        if t.device != dev:
+            raise TypeError(f"{name}: expected a tensor on {dev}")
+        setattr(io, name, _dev_ptr(t, torch.int32 if name == "eidx" else torch.float32, name, T * k))
+    s = _stream_of(stream, dev)
+    if workspace is None:
+        if 0 < T * k <= MOE_DECODE_MAX_PAIRS:
+            workspace = torch.empty(moe_decode_workspace_size(d, P["d_ff"], E, k, T), dtype=torch.uint8, device=dev)
+            if stream is not None:
+                workspace.record_stream(stream)
+    elif workspace.device != dev:
+        raise TypeError(f"workspace: expected a tensor on {dev}")
+    if workspace is not None:
+        io.workspace = _dev_ptr(workspace, torch.uint8, "workspace")
+        io.workspace_bytes = workspace.numel()
+    rc = lib().moe_decode_run_layer(handle.ptr, io, s)
+    if rc:
+        _check(rc, handle.ptr)
+
+
+# ----------------------------------------------------------------- MXFP4 ---
+
+def _mx_device(t: torch.Tensor, name: str) -> torch.device:
+    if not t.is_cuda:
+        raise TypeError(f"{name}: expected a device tensor")
+    return t.device
+
+
+def _mx_bytes(t: torch.Tensor, name: str, shape, device) -> int:
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != torch.uint8 or t.device != device or not t.is_contiguous():
+        raise TypeError(f"{name}: expected a contiguous uint8 tensor on {device}")
+    return t.data_ptr()
+
+
+def _mx_matrix(values, codes, scales, dev) -> moe_mxfp4_matrix_t:
+    if values.dtype not in _DTYPE_ID:
+        raise TypeError("expected float32, bfloat16 or float16 values")
+    M, K = values.shape
+    m = moe_mxfp4_matrix_t()
+    m.struct_size = ctypes.sizeof(m)
+    m.device = dev.index
+    m.dtype = _DTYPE_ID[values.dtype]
+    m.M, m.K = M, K
+    m.stride = _rows_of(values, "values", M, K, dev)
+    m.values = values.data_ptr()
+    m.codes = _mx_bytes(codes, "codes", (M, K // 2), dev)
+    m.scales = _mx_bytes(scales, "scales", (M, K // 32), dev)
+    return m
+
+
+def _new(shape, dtype, dev, stream) -> torch.Tensor:
+    t = torch.empty(shape, dtype=dtype, device=dev)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def moe_mxfp4_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
+                       scales: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None):
+    """x [M, K] (fp32, bf16 or fp16; K a multiple of 32) -> MXFP4 (codes [M, K/2] uint8, scales [M, K/32] uint8)."""
+    dev = _mx_device(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x: expected a matrix")
+    M, K = x.shape
+    if codes is None:
+        codes = _new((M, K // 2), torch.uint8, dev, stream)
+    if scales is None:
+        scales = _new((M, K // 32), torch.uint8, dev, stream)
+    m = _mx_matrix(x, codes, scales, dev)
+    rc = lib().moe_mxfp4_quantize(m, _stream_of(stream, dev))
+    if rc:
+        _check(rc)
+    return codes, scales
+
+
+def moe_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, out: Optional[torch.Tensor] = None,
+                         dtype: torch.dtype = torch.float32,
+                         stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """MXFP4 (codes [M, K/2], scales [M, K/32]) -> values [M, K] in ``out`` (or a new tensor of ``dtype``)."""
+    dev = _mx_device(codes, "codes")
+    if codes.dim() != 2:
+        raise ValueError("codes: expected a matrix")
+    M, K = codes.shape[0], codes.shape[1] * 2
+    if out is None:
+        out = _new((M, K), dtype, dev, stream)
+    elif out.dim() != 2 or tuple(out.shape) != (M, K):
+        raise ValueError(f"out: expected shape {(M, K)}, got {tuple(out.shape)}")
+    m = _mx_matrix(out, codes, scales, dev)
+    rc = lib().moe_mxfp4_dequantize(m, _stream_of(stream, dev))
+    if rc:
+        _check(rc)
+    return out
+
+
+def moe_mxfp4_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tensor, b_scales: torch.Tensor,
+                   out: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.float32,
+                   bounds: Optional[torch.Tensor] = None, rows: Optional[torch.Tensor] = None,
+                   top_k: int = 1, swiglu: bool = False,
+                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """out[r] = A[src(r)] B[g(r)]^T of two MXFP4 matrices (fp32 sums, one rounding to out's type).
+
+    a_codes [A, K/2], b_codes [N, K/2] or [G, N, K/2] (their scales with K/32); with swiglu B has
+    2N rows a group, gate then up.  bounds: int32 [G + 1], group g's rows of out; rows: int32 [M],
+    src(r) = rows[r] // top_k (the row table moe_prefill_run_layer exports); without rows
+    src(r) = r // top_k and M = A * top_k.  Rows of out in no group are left as they were."""
+    dev = _mx_device(a_codes, "a_codes")
+    if a_codes.dim() != 2 or b_codes.dim() not in (2, 3):
+        raise ValueError("a_codes: expected a matrix; b_codes: a matrix, or one per group")
+    if top_k < 1:
+        raise ValueError("top_k must be at least 1")
+    A, K2 = a_codes.shape
+    K = K2 * 2
+    G = b_codes.shape[0] if b_codes.dim() == 3 else 1
+    NB = b_codes.shape[-2]
+    if swiglu and NB % 2:
+        raise ValueError("b_codes: swiglu needs gate and up rows, an even number")
+    N = NB // 2 if swiglu else NB
+    M = rows.shape[0] if rows is not None else A * top_k
+    if out is None:
+        out = _new((M, N), dtype, dev, stream)
+    if out.dtype not in _DTYPE_ID:
+        raise TypeError("out: expected float32, bfloat16 or float16")
+    if bounds is None and G != 1:
+        raise ValueError("b_codes of several groups need bounds")
+    if bounds is not None and (bounds.dim() != 1 or bounds.shape[0] != G + 1):
+        raise ValueError(f"bounds: expected shape ({G + 1},)")
+    if rows is not None and rows.dim() != 1:
+        raise ValueError("rows: expected a vector")
+    for name, t in (("bounds", bounds), ("rows", rows)):
+        if t is not None and (t.device != dev or t.dtype != torch.int32 or not t.is_contiguous()):
+            raise TypeError(f"{name}: expected a contiguous int32 tensor on {dev}")
+    a = moe_mxfp4_gemm_args_t()
+    a.struct_size = ctypes.sizeof(a)
+    a.device = dev.index
+    a.a_codes = _mx_bytes(a_codes, "a_codes", (A, K2), dev)
+    a.a_scales = _mx_bytes(a_scales, "a_scales", (A, K // 32), dev)
+    a.a_rows = A
+    a.b_codes = _mx_bytes(b_codes, "b_codes", b_codes.shape[:-1] + (K2,), dev)
+    a.b_scales = _mx_bytes(b_scales, "b_scales", b_codes.shape[:-1] + (K // 32,), dev)
+    a.bounds = bounds.data_ptr() if bounds is not None else None
+    a.rows = rows.data_ptr() if rows is not None else None
+    a.n_groups, a.top_k, a.M, a.N, a.K = G, top_k, M, N, K
+    a.swiglu = 1 if swiglu else 0
+    a.dtype = _DTYPE_ID[out.dtype]
+    a.out_stride = _rows_of(out, "out", M, N, dev)
+    a.out = out.data_ptr()
+    rc = lib().moe_mxfp4_gemm(a, _stream_of(stream, dev))
+    if rc:
+        _check(rc)
+    return out
 
 
 # ----------------------------------------------------------- stream pool ---

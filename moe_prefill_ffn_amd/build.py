@@ -11,7 +11,7 @@ LIB = os.path.join(HERE, "libmoe_prefill.so")
 MICRO_LIB = os.path.join(HERE, "libmoe_micro.so")   # measurement kernels (roofline denominators)
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-SOURCES = ["moe_kernels.hip", "moe_runtime.cpp", "moe_pack.cpp", "moe_pool_plan.cpp"]
+SOURCES = ["moe_kernels.hip", "moe_decode.hip", "moe_mx.hip", "moe_runtime.cpp", "moe_pack.cpp", "moe_pool_plan.cpp"]
 
 # -ffp-contract=off: no fused multiply-adds beyond the ones written out.
 # No fast-math: IEEE division (correctly rounded), fp32 denormals kept.

@@ -16,8 +16,11 @@
 #include <vector>
 
 #include "../../include/moe_prefill.h"
+#include "moe_decode.h"
+#include "moe_dtype.h"
 #include "moe_kernels.h"
 #include "moe_layout.h"
+#include "moe_mx.h"
 #include "moe_pool_plan.h"
 
 namespace moe {
@@ -571,6 +574,129 @@ void pool_release(moe_prefill_t* h)
     h->warnings = 0;
 }
 
+// Where a layer's weights are for this call: the caller's resident blob, or a pool slot.
+struct LayerWeights {
+    const uint8_t* blob = nullptr;
+    int slot = -1;             // pool slot (-1: resident blob)
+    int sparse_slot = -1;      // the slot if the layer's kernels load the experts with rows
+};
+
+// The weights of `layer` (-1: weights_dev) made ready for work on st: a resident slot, a
+// prefetched slot (st waits for its copy), a stream-ordered load into a free slot, or a slot
+// for an active-expert load.
+int acquire_weights(moe_prefill_t* h, int layer, const void* weights_dev, hipStream_t st, LayerWeights* W)
+{
+    int slot = -1;
+    hipError_t e = hipSuccess;
+    if (layer < 0) {
+        if (!weights_dev) return fail(h, MOE_EINVAL, "layer == -1 needs weights_dev");
+        W->blob = static_cast<const uint8_t*>(weights_dev);
+    } else {
+        if (!h->pool_on) return fail(h, MOE_ESTATE, "layer >= 0 but no stream pool is configured");
+        if (layer >= h->nl) return fail(h, MOE_ESTATE, "layer index beyond the configured stack");
+        if (layer == 0 && h->reserve_bytes > 0 && h->vmm) {
+            // a pass starts: give memory back if the device runs short of the reserve
+            size_t fr = 0, tot = 0;
+            if (hipMemGetInfo(&fr, &tot) == hipSuccess && (int64_t)fr < h->reserve_bytes) {
+                const int64_t live = (int64_t)(h->res_live + count_slots(h, kSlotStreaming)) * (int64_t)h->slot_bytes;
+                uint64_t rel = 0;
+                int w = 0;
+                const int rc = pool_trim(h, live - (h->reserve_bytes - (int64_t)fr), &rel, &w);
+                if (rc != MOE_OK) return rc;
+                h->stats.pressure_trims++;
+                h->warnings |= w;
+                log_msg(h, MOE_LOG_WARN, "device memory below the reserve: the pool released " +
+                        std::to_string(rel) + " bytes, " + std::to_string(h->res_live) + " residents left");
+                log_warnings(h, w, "memory pressure");
+            }
+            (void)hipGetLastError();
+        }
+        slot = h->layer_slot[layer];
+        if (slot >= 0) {
+            if (h->slot_kind[slot] == kSlotStreaming && h->ready_set[slot])
+                e = hipStreamWaitEvent(st, h->ev_ready[slot], 0);
+            if (h->from_prefetch[slot]) {
+                h->stats.prefetch_activated++;
+                h->from_prefetch[slot] = 0;
+            }
+        } else if (h->active_only) {
+            // active-expert load: the kernels of this layer fill the slot after routing
+            slot = pick_victim(h, layer, -1);
+            if (slot < 0) return fail(h, MOE_ESTATE, "no pool slot available");
+            const int old = h->slot_layer[slot];
+            if (old >= 0) h->layer_slot[old] = -1;
+            h->slot_layer[slot] = -1;                     // a partial layer: never reused as whole
+            if (h->free_set[slot]) e = hipStreamWaitEvent(st, h->ev_free[slot], 0);
+            if (e == hipSuccess && h->poison)   // debug: the experts that are not loaded hold NaN bytes
+                e = launch_fill_u32(reinterpret_cast<uint32_t*>(h->pool + (uint64_t)slot * h->slot_bytes),
+                                    (int64_t)(h->slot_bytes / 4), 0xFFFFFFFFu, st);
+            W->sparse_slot = slot;
+            h->stats.sparse_loads++;
+        } else {
+            // load-then-compute: a stream-ordered copy into a free slot first
+            slot = pick_victim(h, layer, -1);
+            if (slot < 0) return fail(h, MOE_ESTATE, "no pool slot available");
+            e = enqueue_copy(h, slot, layer);
+            if (e == hipSuccess) e = hipStreamWaitEvent(st, h->ev_ready[slot], 0);
+            h->stats.sync_loads++;
+            log_msg(h, MOE_LOG_INFO, "layer " + std::to_string(layer) + ": not prefetched, loaded before compute");
+        }
+        if (e != hipSuccess) return hip_fail(h, e, "pool acquire");
+        W->blob = h->pool + (uint64_t)slot * h->slot_bytes;
+        W->slot = slot;
+    }
+    return MOE_OK;
+}
+
+// Lookahead after a layer: queue the next streamed layers behind it.
+void queue_prefetches(moe_prefill_t* h, int layer)
+{
+    if (layer >= 0) {
+        for (int y : window_after(h, layer)) {
+            if (h->layer_slot[y] >= 0) continue;
+            const int v = pick_victim(h, layer, h->active);
+            if (v < 0) break;
+            h->prefetch_counter++;
+            if (h->fail_at && h->prefetch_counter == h->fail_at) {
+                h->stats.prefetch_failed++;   // forced failure: this layer will load synchronously
+                log_msg(h, MOE_LOG_WARN, "prefetch of layer " + std::to_string(y) + " failed (test hook): it will load synchronously");
+                continue;
+            }
+            const hipError_t e = enqueue_copy(h, v, y);
+            if (e != hipSuccess) {
+                (void)hipGetLastError();
+                h->stats.prefetch_failed++;
+                log_msg(h, MOE_LOG_WARN, "prefetch of layer " + std::to_string(y) + " failed: it will load synchronously");
+                continue;
+            }
+            h->from_prefetch[v] = 1;
+            h->stats.prefetch_queued++;
+        }
+    }
+}
+
+// Argument checks of the few-token and MXFP4 entry points.
+bool dtype_ok(int t) { return t == MOE_F32 || t == MOE_BF16 || t == MOE_F16; }
+bool stride_ok(int64_t s, int64_t least) { return s >= least && s <= ((int64_t)1 << 40); }
+uint64_t addr(const void* p) { return reinterpret_cast<uintptr_t>(p); }
+static_assert(MOE_F32 == kF32 && MOE_BF16 == kBF16 && MOE_F16 == kF16, "one numbering");
+static_assert(MOE_DECODE_MAX_PAIRS == kDecodeMaxPairs, "one limit");
+
+// No C++ exception leaves a C entry point (only std::bad_alloc can arise: message strings).
+template <class F>
+int guarded(moe_prefill_t* h, F f) noexcept
+{
+    try {
+        return f();
+    } catch (...) {
+        if (h)
+            h->err.clear();
+        else
+            g_err.clear();
+        return MOE_ENOMEM;
+    }
+}
+
 }  // namespace
 
 // ======================================================================= ABI
@@ -729,65 +855,12 @@ int moe_prefill_run_layer(moe_prefill_t* h, const moe_layer_io_t* io_in, void* s
     hipStream_t st = static_cast<hipStream_t>(stream);
     DevGuard guard(h->dev);
 
-    const uint8_t* blob = nullptr;
-    int slot = -1, sparse_slot = -1;
+    LayerWeights W;
+    const int rc = acquire_weights(h, io.layer, io.weights_dev, st, &W);
+    if (rc != MOE_OK) return rc;
+    const uint8_t* blob = W.blob;
+    const int slot = W.slot, sparse_slot = W.sparse_slot;
     hipError_t e = hipSuccess;
-    if (io.layer < 0) {
-        if (!io.weights_dev) return fail(h, MOE_EINVAL, "layer == -1 needs weights_dev");
-        blob = static_cast<const uint8_t*>(io.weights_dev);
-    } else {
-        if (!h->pool_on) return fail(h, MOE_ESTATE, "layer >= 0 but no stream pool is configured");
-        if (io.layer >= h->nl) return fail(h, MOE_ESTATE, "layer index beyond the configured stack");
-        if (io.layer == 0 && h->reserve_bytes > 0 && h->vmm) {
-            // a pass starts: give memory back if the device runs short of the reserve
-            size_t fr = 0, tot = 0;
-            if (hipMemGetInfo(&fr, &tot) == hipSuccess && (int64_t)fr < h->reserve_bytes) {
-                const int64_t live = (int64_t)(h->res_live + count_slots(h, kSlotStreaming)) * (int64_t)h->slot_bytes;
-                uint64_t rel = 0;
-                int w = 0;
-                const int rc = pool_trim(h, live - (h->reserve_bytes - (int64_t)fr), &rel, &w);
-                if (rc != MOE_OK) return rc;
-                h->stats.pressure_trims++;
-                h->warnings |= w;
-                log_msg(h, MOE_LOG_WARN, "device memory below the reserve: the pool released " +
-                        std::to_string(rel) + " bytes, " + std::to_string(h->res_live) + " residents left");
-                log_warnings(h, w, "memory pressure");
-            }
-            (void)hipGetLastError();
-        }
-        slot = h->layer_slot[io.layer];
-        if (slot >= 0) {
-            if (h->slot_kind[slot] == kSlotStreaming && h->ready_set[slot])
-                e = hipStreamWaitEvent(st, h->ev_ready[slot], 0);
-            if (h->from_prefetch[slot]) {
-                h->stats.prefetch_activated++;
-                h->from_prefetch[slot] = 0;
-            }
-        } else if (h->active_only) {
-            // active-expert load: the kernels of this layer fill the slot after routing
-            slot = pick_victim(h, io.layer, -1);
-            if (slot < 0) return fail(h, MOE_ESTATE, "no pool slot available");
-            const int old = h->slot_layer[slot];
-            if (old >= 0) h->layer_slot[old] = -1;
-            h->slot_layer[slot] = -1;                     // a partial layer: never reused as whole
-            if (h->free_set[slot]) e = hipStreamWaitEvent(st, h->ev_free[slot], 0);
-            if (e == hipSuccess && h->poison)   // debug: the experts that are not loaded hold NaN bytes
-                e = launch_fill_u32(reinterpret_cast<uint32_t*>(h->pool + (uint64_t)slot * h->slot_bytes),
-                                    (int64_t)(h->slot_bytes / 4), 0xFFFFFFFFu, st);
-            sparse_slot = slot;
-            h->stats.sparse_loads++;
-        } else {
-            // load-then-compute: a stream-ordered copy into a free slot first
-            slot = pick_victim(h, io.layer, -1);
-            if (slot < 0) return fail(h, MOE_ESTATE, "no pool slot available");
-            e = enqueue_copy(h, slot, io.layer);
-            if (e == hipSuccess) e = hipStreamWaitEvent(st, h->ev_ready[slot], 0);
-            h->stats.sync_loads++;
-            log_msg(h, MOE_LOG_INFO, "layer " + std::to_string(io.layer) + ": not prefetched, loaded before compute");
-        }
-        if (e != hipSuccess) return hip_fail(h, e, "pool acquire");
-        blob = h->pool + (uint64_t)slot * h->slot_bytes;
-    }
 
     if (h->mask_dirty) {   // a launch failed part-way: restore the grouping state first
         e = launch_fill_u32(reinterpret_cast<uint32_t*>(h->ws + h->L.mask), (int64_t)mask_words(h->E, h->L.W), 0u, st);
@@ -856,29 +929,7 @@ int moe_prefill_run_layer(moe_prefill_t* h, const moe_layer_io_t* io_in, void* s
     if (e != hipSuccess) return hip_fail(h, e, "export copy");
     h->stats.layers_run++;
 
-    // lookahead: queue the next streamed layers behind this one
-    if (io.layer >= 0) {
-        for (int y : window_after(h, io.layer)) {
-            if (h->layer_slot[y] >= 0) continue;
-            const int v = pick_victim(h, io.layer, h->active);
-            if (v < 0) break;
-            h->prefetch_counter++;
-            if (h->fail_at && h->prefetch_counter == h->fail_at) {
-                h->stats.prefetch_failed++;   // forced failure: this layer will load synchronously
-                log_msg(h, MOE_LOG_WARN, "prefetch of layer " + std::to_string(y) + " failed (test hook): it will load synchronously");
-                continue;
-            }
-            e = enqueue_copy(h, v, y);
-            if (e != hipSuccess) {
-                (void)hipGetLastError();
-                h->stats.prefetch_failed++;
-                log_msg(h, MOE_LOG_WARN, "prefetch of layer " + std::to_string(y) + " failed: it will load synchronously");
-                continue;
-            }
-            h->from_prefetch[v] = 1;
-            h->stats.prefetch_queued++;
-        }
-    }
+    queue_prefetches(h, io.layer);
     h->err.clear();
     return MOE_OK;
 }
@@ -945,6 +996,200 @@ int moe_prefill_run_layer_noalloc(const moe_prefill_params_t* pin, const moe_lay
     if (e != hipSuccess) return hip_fail(nullptr, e, "noalloc: export copy");
     g_err.clear();
     return MOE_OK;
+}
+
+// ----------------------------------------------------- a few tokens' layer ---
+
+int moe_decode_workspace_size(const moe_prefill_params_t* pin, uint64_t* bytes)
+{
+    return guarded(nullptr, [&] {
+        moe_prefill_params_t p;
+        std::string why;
+        if (!bytes) return fail(nullptr, MOE_EINVAL, "null bytes pointer");
+        if (!read_struct(pin, &p, &why)) return fail(nullptr, MOE_EINVAL, why);
+        if (!dims_ok(p, &why)) return fail(nullptr, MOE_EINVAL, why);
+        if ((int64_t)p.max_tokens * p.top_k > MOE_DECODE_MAX_PAIRS)
+            return fail(nullptr, MOE_EINVAL, "decode: max_tokens * top_k above 1024; use moe_prefill_run_layer");
+        *bytes = decode_ws(p.d_model, p.d_ff, p.n_experts, p.top_k, p.max_tokens).total;
+        g_err.clear();
+        return (int)MOE_OK;
+    });
+}
+
+int moe_decode_run_layer(moe_prefill_t* h, const moe_decode_io_t* io_in, void* stream)
+{
+    return guarded(h, [&] {
+        if (!h) return fail(nullptr, MOE_EINVAL, "null handle");
+        moe_decode_io_t io;
+        std::string why;
+        if (!read_struct(io_in, &io, &why)) return fail(h, MOE_EINVAL, why);
+        const int T = io.n_tokens;
+        if (T < 0 || (int64_t)T * h->k > MOE_DECODE_MAX_PAIRS)
+            return fail(h, MOE_EINVAL, "decode: n_tokens < 0 or n_tokens * top_k above 1024; use moe_prefill_run_layer");
+        if (!dtype_ok(io.dtype)) return fail(h, MOE_EINVAL, "decode: dtype must be MOE_F32, MOE_BF16 or MOE_F16");
+        if (T == 0) {
+            h->err.clear();
+            return (int)MOE_OK;
+        }
+        if (!io.x || !io.logits || !io.y || !io.workspace)
+            return fail(h, MOE_EINVAL, "decode: x, logits, y and workspace are required");
+        const int eb = dtype_bytes(io.dtype);
+        if (!stride_ok(io.x_stride, h->d) || !stride_ok(io.y_stride, h->d) || !stride_ok(io.logits_stride, h->E))
+            return fail(h, MOE_EINVAL, "decode: a row stride below the row's length, or above 2^40");
+        if ((addr(io.x) | addr(io.y) | (uint64_t)(io.x_stride * eb) | (uint64_t)(io.y_stride * eb)) % 16)
+            return fail(h, MOE_EINVAL, "decode: the rows of x and y must be 16-byte aligned");
+        if ((addr(io.logits) | addr(io.eidx) | addr(io.weights)) % 4)
+            return fail(h, MOE_EINVAL, "decode: logits, eidx and weights must be 4-byte aligned");
+        if (addr(io.workspace) % 256) return fail(h, MOE_EINVAL, "decode: workspace must be 256-byte aligned");
+        DecodeLaunch D{};
+        D.L = decode_ws(h->d, h->f, h->E, h->k, T);
+        if (io.workspace_bytes < D.L.total)
+            return fail(h, MOE_EINVAL, "decode: workspace smaller than moe_decode_workspace_size()");
+        if (io.layer < 0 && addr(io.weights_dev) % 16)
+            return fail(h, MOE_EINVAL, "decode: weights_dev must be 16-byte aligned");
+        hipStream_t st = static_cast<hipStream_t>(stream);
+        DevGuard guard(h->dev);
+        LayerWeights W;
+        const int rc = acquire_weights(h, io.layer, io.weights_dev, st, &W);
+        if (rc != MOE_OK) return rc;
+        D.T = T;
+        D.d = h->d;
+        D.f = h->f;
+        D.E = h->E;
+        D.k = h->k;
+        D.dtype = io.dtype;
+        D.x = io.x;
+        D.x_stride = io.x_stride;
+        D.logits = io.logits;
+        D.logits_stride = io.logits_stride;
+        D.y = io.y;
+        D.y_stride = io.y_stride;
+        D.blob = W.blob;
+        D.expert_stride = h->B.expert_bytes;
+        D.gu_q_off = h->B.gu_q;
+        D.gu_s_off = h->B.gu_s;
+        D.d_q_off = h->B.d_q;
+        D.d_s_off = h->B.d_s;
+        D.ws = static_cast<uint8_t*>(io.workspace);
+        D.eidx_out = io.eidx;
+        D.wts_out = io.weights;
+        hipError_t e = launch_decode_route(D, st);
+        if (e == hipSuccess && W.sparse_slot >= 0)
+            e = launch_expert_load(h->blobs_dev[io.layer], h->pool + (uint64_t)W.sparse_slot * h->slot_bytes,
+                                   reinterpret_cast<const int32_t*>(D.ws + D.L.counts), h->E, h->B.expert_bytes,
+                                   reinterpret_cast<unsigned long long*>(h->ws + h->L.load_stats), st);
+        if (e == hipSuccess) e = launch_decode_products(D, st);
+        if (e != hipSuccess) return hip_fail(h, e, "decode: launch");
+        if (W.slot >= 0) {
+            e = hipEventRecord(h->ev_free[W.slot], st);   // the down product was the last reader
+            if (e != hipSuccess) return hip_fail(h, e, "hipEventRecord");
+            h->free_set[W.slot] = 1;
+            h->active = W.slot;
+        }
+        e = launch_decode_combine(D, st);
+        if (e != hipSuccess) return hip_fail(h, e, "decode: launch");
+        h->stats.layers_run++;
+        queue_prefetches(h, io.layer);
+        h->err.clear();
+        return (int)MOE_OK;
+    });
+}
+
+// ------------------------------------------------------------------- MXFP4 ---
+
+static int mx_matrix(const moe_mxfp4_matrix_t* in, bool quantize, void* stream)
+{
+    return guarded(nullptr, [&] {
+        moe_mxfp4_matrix_t m;
+        std::string why;
+        if (!read_struct(in, &m, &why)) return fail(nullptr, MOE_EINVAL, why);
+        if (!dtype_ok(m.dtype)) return fail(nullptr, MOE_EINVAL, "mxfp4: dtype must be MOE_F32, MOE_BF16 or MOE_F16");
+        if (m.K < 32 || m.K % 32) return fail(nullptr, MOE_EINVAL, "mxfp4: K must be a multiple of 32, at least 32");
+        if (m.M < 0 || m.M > INT32_MAX / (m.K / 32))
+            return fail(nullptr, MOE_EINVAL, "mxfp4: M < 0 or M * K / 32 not below 2^31");
+        if (m.M == 0) {
+            g_err.clear();
+            return (int)MOE_OK;
+        }
+        if (!m.values || !m.codes || !m.scales) return fail(nullptr, MOE_EINVAL, "mxfp4: values, codes and scales are required");
+        if (!stride_ok(m.stride, m.K)) return fail(nullptr, MOE_EINVAL, "mxfp4: stride below K, or above 2^40");
+        if ((addr(m.values) | addr(m.codes) | (uint64_t)(m.stride * dtype_bytes(m.dtype))) % 16)
+            return fail(nullptr, MOE_EINVAL, "mxfp4: the rows of values, and codes, must be 16-byte aligned");
+        const int rc = noalloc_device_ok(m.device);
+        if (rc != MOE_OK) return rc;
+        DevGuard guard(m.device);
+        MxQuant q{};
+        q.x = m.values;
+        q.y = m.values;
+        q.dtype = m.dtype;
+        q.M = m.M;
+        q.stride = m.stride;
+        q.K = m.K;
+        q.codes = m.codes;
+        q.scales = m.scales;
+        hipStream_t st = static_cast<hipStream_t>(stream);
+        const hipError_t e = quantize ? launch_mx_quantize(q, st) : launch_mx_dequantize(q, st);
+        if (e != hipSuccess) return hip_fail(nullptr, e, "mxfp4: launch");
+        g_err.clear();
+        return (int)MOE_OK;
+    });
+}
+
+int moe_mxfp4_quantize(const moe_mxfp4_matrix_t* m, void* stream) { return mx_matrix(m, true, stream); }
+int moe_mxfp4_dequantize(const moe_mxfp4_matrix_t* m, void* stream) { return mx_matrix(m, false, stream); }
+
+int moe_mxfp4_gemm(const moe_mxfp4_gemm_args_t* in, void* stream)
+{
+    return guarded(nullptr, [&] {
+        moe_mxfp4_gemm_args_t a;
+        std::string why;
+        if (!read_struct(in, &a, &why)) return fail(nullptr, MOE_EINVAL, why);
+        if (!dtype_ok(a.dtype)) return fail(nullptr, MOE_EINVAL, "mxfp4: dtype must be MOE_F32, MOE_BF16 or MOE_F16");
+        if (a.swiglu != 0 && a.swiglu != 1) return fail(nullptr, MOE_EINVAL, "mxfp4: swiglu must be 0 or 1");
+        if (a.K < 32 || a.K % 32) return fail(nullptr, MOE_EINVAL, "mxfp4: K must be a multiple of 32, at least 32");
+        if (a.N < 1 || a.N > (1 << 20)) return fail(nullptr, MOE_EINVAL, "mxfp4: N must be in [1, 2^20]");
+        if (a.M < 0 || a.M > INT32_MAX) return fail(nullptr, MOE_EINVAL, "mxfp4: M must be in [0, 2^31)");
+        if (a.n_groups < 1 || a.n_groups > 65535 || (!a.bounds && a.n_groups != 1))
+            return fail(nullptr, MOE_EINVAL, "mxfp4: n_groups must be in [1, 65535], and 1 without bounds");
+        if (a.top_k < 1) return fail(nullptr, MOE_EINVAL, "mxfp4: top_k must be at least 1");
+        if (a.M == 0) {
+            g_err.clear();
+            return (int)MOE_OK;
+        }
+        if (!a.a_codes || !a.a_scales || !a.b_codes || !a.b_scales || !a.out)
+            return fail(nullptr, MOE_EINVAL, "mxfp4: a_codes, a_scales, b_codes, b_scales and out are required");
+        if (a.a_rows < 1 || (!a.rows && a.a_rows < (a.M + a.top_k - 1) / a.top_k))
+            return fail(nullptr, MOE_EINVAL, "mxfp4: A has fewer rows than the product reads");
+        if (!stride_ok(a.out_stride, a.N)) return fail(nullptr, MOE_EINVAL, "mxfp4: out_stride below N, or above 2^40");
+        if ((addr(a.a_codes) | addr(a.b_codes)) % 16)
+            return fail(nullptr, MOE_EINVAL, "mxfp4: a_codes and b_codes must be 16-byte aligned");
+        if (addr(a.out) % dtype_bytes(a.dtype) || (addr(a.bounds) | addr(a.rows)) % 4)
+            return fail(nullptr, MOE_EINVAL, "mxfp4: out, bounds and rows must be aligned to their elements");
+        const int rc = noalloc_device_ok(a.device);
+        if (rc != MOE_OK) return rc;
+        DevGuard guard(a.device);
+        MxGemm g{};
+        g.a_codes = a.a_codes;
+        g.a_scales = a.a_scales;
+        g.a_rows = a.a_rows;
+        g.rows = a.rows;
+        g.row_div = a.top_k;
+        g.b_codes = a.b_codes;
+        g.b_scales = a.b_scales;
+        g.bounds = a.bounds;
+        g.G = a.n_groups;
+        g.M = a.M;
+        g.N = a.N;
+        g.K = a.K;
+        g.swiglu = a.swiglu;
+        g.out = a.out;
+        g.out_stride = a.out_stride;
+        g.dtype = a.dtype;
+        const hipError_t e = launch_mx_gemm(g, static_cast<hipStream_t>(stream));
+        if (e != hipSuccess) return hip_fail(nullptr, e, "mxfp4: launch");
+        g_err.clear();
+        return (int)MOE_OK;
+    });
 }
 
 int moe_prefill_plan_pool(moe_pool_plan_t* inout)
