@@ -135,12 +135,23 @@ __global__ __launch_bounds__(kQuantThreads) void k_mx_dequantize(MxQuant q, int6
 
 // ------------------------------------------------------------------ product ---
 // The scaled matrix instruction takes 32 codes of one block and the block's scale byte
-// per lane and adds the scaled products into fp32.
+// per lane and adds the scaled products into fp32.  Its first operand is the weights, the
+// second the activations, so a lane holds four consecutive output columns of one row in
+// consecutive result registers.
+//
+// Which K-block a lane's 32 codes are is free as long as both operands agree: lane half h
+// takes block 2 h + s in step s of a 128-code stage (4 blocks a row), so that its two
+// scale bytes are neighbours.
+//
+// A block past the end of K is read from the last block (in bounds, any finite codes) with
+// scale byte 0 on both sides: 2^-254 of a product below 2^11 is 0 in fp32.
 //
 // Groups of a row table: tile slot s belongs to the last group g whose first slot
 // bounds[g] / BM + g is <= s (a group of c rows never needs more than the
 // bounds[g + 1] / BM + 1 - bounds[g] / BM slots up to the next group's first), so a
 // workgroup finds its rows from the bounds alone, without a list of tiles.
+typedef int v4i __attribute__((ext_vector_type(4)));
+
 struct Tile {
     int g;
     int64_t m0, m1;           // rows [m0, m1) of the tile; m0 >= m1: nothing to do
@@ -153,88 +164,407 @@ __device__ __forceinline__ Tile tile_of_slot(const MxGemm& a, int64_t slot)
         const int64_t m0 = slot * BM;
         return {0, m0, m0 + BM < a.M ? m0 + BM : a.M};
     }
-    int lo = 0, hi = a.G - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if ((int64_t)(a.bounds[mid] / BM) + mid <= slot)
-            lo = mid;
-        else
-            hi = mid - 1;
+    // 64 groups are compared at a time, one per lane: two rounds of loads up to 4096 groups
+    int g = 0, span = a.G;
+    const int lane = threadIdx.x & 63;
+    while (span > 1) {
+        const int step = (span + 63) >> 6, at = g + lane * step;
+        const bool le = lane * step < span && (int64_t)(a.bounds[at] / BM) + at <= slot;
+        const int n = __popcll(__ballot(le));             // a run of lanes from 0 for sound bounds
+        const int skip = (n > 0 ? n - 1 : 0) * step;
+        g += skip;
+        span = span - skip < step ? span - skip : step;
     }
-    const int64_t b0 = a.bounds[lo], b1 = a.bounds[lo + 1];
-    int64_t m0 = b0 + (slot - (b0 / BM + lo)) * BM, m1 = m0 + BM < b1 ? m0 + BM : b1;
+    g = __builtin_amdgcn_readfirstlane(g);
+    const int64_t b0 = a.bounds[g], b1 = a.bounds[g + 1];
+    int64_t m0 = b0 + (slot - (b0 / BM + g)) * BM, m1 = m0 + BM < b1 ? m0 + BM : b1;
     // sound bounds ascend within [0, M]; this only keeps others from reaching outside
     if (m0 < b0 || m0 < 0) m0 = m1;
     if (m1 > a.M) m1 = a.M;
-    return {lo, m0, m1};
+    return {g, m0, m1};
 }
 
-constexpr int kMxWaves = 4;
-constexpr int kMxBM = 32, kMxBN = 32 * kMxWaves;          // columns per workgroup, per half
-
-// Each wave: 32 rows x two 32-column tiles, fed straight from memory.  SwiGLU: the two
-// tiles are the gate and the up rows of the same output columns.
-template <int kT, bool kSwiglu>
-__global__ __launch_bounds__(64 * kMxWaves) void k_mx_gemm(MxGemm a)
+// A row of the product reads this row of A.
+__device__ __forceinline__ int64_t a_row(const MxGemm& a, int64_t r)
 {
-    const Tile t = tile_of_slot<kMxBM>(a, blockIdx.x);
-    if (t.m0 >= t.m1) return;                             // uniform
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5, j = lane & 31;
-    const int nb = a.K / 32, NB = kSwiglu ? 2 * a.N : a.N;
-    const int n0 = ((int)blockIdx.y * kMxWaves + wave) * (kSwiglu ? 32 : 64);
-    if (n0 >= a.N) return;
-    const int64_t r = t.m0 + j < t.m1 ? t.m0 + j : t.m1 - 1;
-    int64_t src = (a.rows ? (int64_t)a.rows[r] : r) / a.row_div;
-    src = src < 0 ? 0 : (src >= a.a_rows ? a.a_rows - 1 : src);
-    int bn[2];
-    bn[0] = n0 + j < a.N ? n0 + j : a.N - 1;
-    bn[1] = kSwiglu ? a.N + bn[0] : (n0 + 32 + j < a.N ? n0 + 32 + j : a.N - 1);
-    const uint8_t* ac = a.a_codes + src * (a.K / 2);
-    const uint8_t* as = a.a_scales + src * nb;
-    const uint8_t* bc[2];
-    const uint8_t* bs[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int64_t row = (int64_t)t.g * NB + bn[i];
-        bc[i] = a.b_codes + row * (a.K / 2);
-        bs[i] = a.b_scales + row * nb;
+    const int64_t src = (a.rows ? (int64_t)a.rows[r] : r) / a.row_div;
+    return src < 0 ? 0 : (src >= a.a_rows ? a.a_rows - 1 : src);
+}
+
+__device__ __forceinline__ v16f mfma_fp4(v4i w, v4i x, v16f c, int sw, int sx, bool second)
+{
+    const v8i w8 = __builtin_shufflevector(w, w, 0, 1, 2, 3, -1, -1, -1, -1);
+    const v8i x8 = __builtin_shufflevector(x, x, 0, 1, 2, 3, -1, -1, -1, -1);
+    // formats 4, 4: E2M1; the scale byte is byte 0 or 1 of its register
+    return second ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, x8, c, 4, 4, 1, sw, 1, sx)
+                  : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, x8, c, 4, 4, 0, sw, 0, sx);
+}
+
+__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + exp_cw(-g)) * u; }
+
+// ------------------------------------------------------------- tiled kernel ---
+// Direct global->LDS loads, lane i's bytes at wave_base + size * i; inline asm so that the
+// compiler does not drain them (the ring waits for them itself).
+__device__ __forceinline__ uint32_t lds_addr(const void* p)
+{
+    return __builtin_amdgcn_readfirstlane(
+        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p);
+}
+__device__ __forceinline__ void g2lds16(const void* g, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(lds) : "memory", "m0");
+}
+__device__ __forceinline__ void g2lds4(const void* g, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(lds) : "memory", "m0");
+}
+
+// Chunk c (16 bytes, one block) of a 64-byte row r sits in slot c ^ swz(r): any 16
+// consecutive rows touch 16 distinct 16-byte bank groups.
+__device__ __forceinline__ int swz(int r) { return ((r >> 1) ^ (r >> 2)) & 3; }
+
+constexpr int kMxRing = 4;
+
+// WM x WN waves, each TM x TN tiles of 32 x 32: BM rows of A by BN rows of B, K in stages of
+// 128 codes through a ring of four LDS slots.
+template <int WM_, int WN_, int TM_, int TN_>
+struct MxShape {
+    static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_;
+    static constexpr int NW = WM * WN, BM = 32 * WM * TM, BN = 32 * WN * TN, kRows = BM + BN;
+    static constexpr int NL = kRows / 16 / NW;            // 1 KiB data loads per wave and stage
+    static_assert(NL * NW * 16 == kRows, "whole loads");
+};
+
+template <class S, bool kAligned>
+struct MxLds {
+    // scale dwords a row: one (4 blocks) where every row's bytes are 4-byte aligned, else the two
+    // aligned dwords around them
+    static constexpr int kDw = kAligned ? 1 : 2;
+    static constexpr int NS = (S::kRows * kDw + 64 * S::NW - 1) / (64 * S::NW);
+    static constexpr int kScaleOff = S::kRows * 64;
+    static constexpr int kSlot = kScaleOff + NS * S::NW * 256;
+    static constexpr int kBytes = kMxRing * kSlot;
+    static constexpr int kLoads = S::NL + NS;             // per wave and stage
+};
+
+template <class S, int kT, bool kSwiglu, bool kAligned>
+__global__ __launch_bounds__(64 * S::NW) void k_mx_tile(MxGemm a, int n_tiles, int64_t n_slots)
+{
+    using L = MxLds<S, kAligned>;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, j = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / S::WN, wn = wave % S::WN;
+
+    // Workgroups go round-robin over the 8 XCDs: XCD x takes a contiguous run of tiles, and
+    // inside a run bands of 8 slots by all column tiles, so that what an XCD runs at once
+    // shares rows of A and of B in its L2.
+    Tile t;
+    int nt;
+    {
+        const int64_t total = n_slots * n_tiles, per = (total + 7) >> 3;
+        const int64_t id = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+        if ((blockIdx.x >> 3) >= per || id >= total) return;
+        const int64_t band = id / (8 * n_tiles), first = band * 8;
+        const int high = n_slots - first < 8 ? (int)(n_slots - first) : 8;
+        const int in = (int)(id - first * n_tiles);
+        nt = in / high;
+        t = tile_of_slot<S::BM>(a, first + in % high);
     }
-    v16f acc[2];
+    if (t.m0 >= t.m1) return;                             // uniform
+    const int nb = a.K / 32, nst = (nb + 3) >> 2;
+    const int NB = kSwiglu ? 2 * a.N : a.N;
+    constexpr int kOutCols = kSwiglu ? S::BN / 2 : S::BN;
+    const int n0 = nt * kOutCols;
+
+    // row q of the stage: rows of A, then rows of B (SwiGLU: 32 gate rows and their 32 up rows in turn)
+    auto src_row = [&](int q, bool& is_a) -> int64_t {
+        is_a = q < S::BM;
+        if (is_a) {
+            const int64_t r = t.m0 + q < t.m1 ? t.m0 + q : t.m1 - 1;
+            return a_row(a, r);
+        }
+        q -= S::BM;
+        int n = kSwiglu ? n0 + (q >> 6) * 32 + (q & 31) : n0 + q;
+        n = n < a.N ? n : a.N - 1;
+        if (kSwiglu && (q & 32)) n += a.N;
+        return (int64_t)t.g * NB + n;
+    };
+
+    const uint8_t* dsrc[S::NL];                           // this lane's chunk of its row, per load
+    int dchunk[S::NL];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[0][i] = acc[1][i] = 0.0f;
-    for (int b0 = 0; b0 < nb; b0 += 2) {
-        const int b = b0 + h;
-        v8i av = {0, 0, 0, 0, 0, 0, 0, 0}, bv[2] = {av, av};
-        int sa = 127, sb[2] = {127, 127};
-        if (b < nb) {                                     // past the end: zeros with scale 1
-            const uint4 w = *reinterpret_cast<const uint4*>(ac + b * 16);
-            av[0] = (int)w.x, av[1] = (int)w.y, av[2] = (int)w.z, av[3] = (int)w.w;
-            sa = as[b];
+    for (int l = 0; l < S::NL; ++l) {
+        const int q = (wave * S::NL + l) * 16 + (lane >> 2);
+        bool is_a;
+        const int64_t r = src_row(q, is_a);
+        dchunk[l] = (lane & 3) ^ swz(q);
+        dsrc[l] = (is_a ? a.a_codes : a.b_codes) + r * (a.K / 2);
+    }
+    const uint8_t* ssrc[L::NS];                           // the dword this lane loads of a row's scales
+    const uint8_t* slast[L::NS];                          // the last aligned dword that holds one of them
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint4 u = *reinterpret_cast<const uint4*>(bc[i] + b * 16);
-                bv[i][0] = (int)u.x, bv[i][1] = (int)u.y, bv[i][2] = (int)u.z, bv[i][3] = (int)u.w;
-                sb[i] = bs[i][b];
+    for (int l = 0; l < L::NS; ++l) {
+        int i = (wave * L::NS + l) * 64 + lane;
+        i = i < S::kRows * L::kDw ? i : 0;
+        const int q = i / L::kDw;
+        bool is_a;
+        const int64_t r = src_row(q, is_a);
+        const uint8_t* p = (is_a ? a.a_scales : a.b_scales) + r * nb;
+        if (kAligned) {
+            ssrc[l] = p;
+        } else {
+            // the aligned dwords around the row's bytes; a dword that holds a valid byte lies in
+            // that byte's page
+            slast[l] = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(p + nb - 1) & ~(uintptr_t)3);
+            ssrc[l] = reinterpret_cast<const uint8_t*>((reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)3) + 4 * (i % L::kDw));
+        }
+    }
+    int mis[S::TM + S::TN];                               // unaligned: where the row's first byte is in its dword
+    if (!kAligned) {
+#pragma unroll
+        for (int i = 0; i < S::TM + S::TN; ++i) {
+            const int q = i < S::TM ? (wm * S::TM + i) * 32 + j : S::BM + (wn * S::TN + i - S::TM) * 32 + j;
+            bool is_a;
+            const int64_t r = src_row(q, is_a);
+            mis[i] = (int)(reinterpret_cast<uintptr_t>((is_a ? a.a_scales : a.b_scales) + r * nb) & 3);
+        }
+    }
+
+    const uint32_t lds0 = lds_addr(lds);
+    // load l (of kLoads) of stage s (clamped: tail loads repeat the last stage) into ring slot `slot`
+    auto issue = [&](int l, int s, int slot) {
+        const int sc = s < nst ? s : nst - 1;
+        const uint32_t base = lds0 + slot * L::kSlot;
+        if (l < S::NL) {
+            int c = sc * 4 + dchunk[l];
+            if (!kAligned) c = c < nb ? c : nb - 1;
+            g2lds16(dsrc[l] + c * 16, base + (wave * S::NL + l) * 1024);
+        } else {
+            const uint8_t* p = ssrc[l - S::NL] + sc * 4;
+            if (!kAligned) p = p < slast[l - S::NL] ? p : slast[l - S::NL];
+            g2lds4(p, base + L::kScaleOff + (wave * L::NS + l - S::NL) * 256);
+        }
+    };
+
+    // Operands of one step: tiles of the activations, then of the weights.  Tile rows are 32
+    // apart, so the swizzle is that of row j.
+    struct Ops {
+        v4i v[S::TM + S::TN];
+    };
+    struct Scales {
+        int v[S::TM + S::TN];
+    };
+    const int a_base = (wm * S::TM * 32 + j) * 64, b_base = (S::BM + wn * S::TN * 32 + j) * 64;
+    const int ch[2] = {((2 * h) ^ swz(j)) * 16, ((2 * h + 1) ^ swz(j)) * 16};
+    auto read_op = [&](int i, int slot, int step, Ops& o) {
+        const uint8_t* base = lds + slot * L::kSlot + ch[step];
+        o.v[i] = *reinterpret_cast<const v4i*>(base + (i < S::TM ? a_base + i * 2048 : b_base + (i - S::TM) * 2048));
+    };
+    // the scale bytes of both steps (bytes 0 and 1)
+    const int sa_base = wm * S::TM * 32 + j, sb_base = S::BM + wn * S::TN * 32 + j;
+    auto read_scale = [&](int i, int s, int slot, Scales& o) {
+        const uint8_t* base = lds + slot * L::kSlot + L::kScaleOff;
+        const int q = i < S::TM ? sa_base + i * 32 : sb_base + (i - S::TM) * 32;
+        if (kAligned) {
+            o.v[i] = *reinterpret_cast<const uint16_t*>(base + q * 4 + 2 * h);
+        } else {
+            const uint8_t* p = base + q * 8 + mis[i] + 2 * h;
+            const int b = 4 * s + 2 * h;
+            o.v[i] = (b < nb ? p[0] : 0) | (b + 1 < nb ? p[1] << 8 : 0);
+        }
+    };
+
+    v16f acc[S::TM][S::TN];
+#pragma unroll
+    for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+        for (int n = 0; n < S::TN; ++n)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][n][e] = 0.0f;
+
+    // Stage s: its second step's operands are read under the first step's products, the next
+    // stage's first step's under the second's.  The barrier between them frees stage s's slot
+    // (every wave has read it) for stage s + 4 and admits stage s + 1 (two stages may still be
+    // in flight behind it).  Each memory instruction is placed behind a product of its own, in
+    // whose 32 cycles it issues: the loads in a row before the products left the matrix core
+    // idle (8192 x 4096 x 4096: 100 us).
+    constexpr int kOps = S::TM + S::TN, kProd = S::TM * S::TN;
+    auto products = [&](const Ops& o, const Scales& sc, bool second, auto between) {
+#pragma unroll
+        for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+            for (int n = 0; n < S::TN; ++n) {
+                acc[i][n] = mfma_fp4(o.v[S::TM + n], o.v[i], acc[i][n], sc.v[S::TM + n], sc.v[i], second);
+                between(i * S::TN + n);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+    };
+    Ops o0, o1;
+    Scales sc0, sc1;
+    auto stage = [&](int s) {
+        const int slot = s % kMxRing, next = (s + 1) % kMxRing;
+        products(o0, sc0, false, [&](int at) {
+#pragma unroll
+            for (int i = at * kOps / kProd; i < (at + 1) * kOps / kProd; ++i) read_op(i, slot, 1, o1);
+        });
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((kMxRing - 2) * L::kLoads) : "memory");
+        products(o1, sc0, true, [&](int at) {
+            // past the last stage: a repeated one, not used
+#pragma unroll
+            for (int i = at * kOps / kProd; i < (at + 1) * kOps / kProd; ++i) {
+                read_op(i, next, 0, o0);
+                read_scale(i, s + 1, next, sc1);
+            }
+#pragma unroll
+            for (int l = at * L::kLoads / kProd; l < (at + 1) * L::kLoads / kProd; ++l) issue(l, s + kMxRing, slot);
+        });
+    };
+#pragma unroll
+    for (int u = 0; u < kMxRing; ++u)
+#pragma unroll
+        for (int l = 0; l < L::kLoads; ++l) issue(l, u, u);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((kMxRing - 1) * L::kLoads) : "memory");
+#pragma unroll
+    for (int i = 0; i < kOps; ++i) {
+        read_op(i, 0, 0, o0);
+        read_scale(i, 0, 0, sc0);
+    }
+    for (int s = 0; s < nst; ++s) {
+        stage(s);
+        sc0 = sc1;
+    }
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");   // the ring is dead: the epilogue takes it
+
+    // Epilogue: each wave turns its tile, 32 rows at a time, through LDS of its own into
+    // row-major order and writes 16 bytes a lane, whole runs of a row at a time.
+    typedef typename Elem<kT>::type T;
+    constexpr int kCols = (kSwiglu ? S::TN / 2 : S::TN) * 32;
+    constexpr int kStride = kCols * (int)sizeof(T) + 16;
+    constexpr int kVec = 16 / (int)sizeof(T), kLanes = kCols / kVec;   // lanes a row
+    static_assert(32 * kStride * S::NW <= L::kBytes, "the waves' turning space fits the ring");
+    static_assert(64 % kLanes == 0, "whole rows a pass");
+    uint8_t* mine = lds + wave * 32 * kStride;
+    const int c0 = n0 + wn * kCols;
+    const bool vec = (reinterpret_cast<uintptr_t>(a.out) | (uint64_t)(a.out_stride * (int64_t)sizeof(T))) % 16 == 0;
+#pragma unroll
+    for (int i = 0; i < S::TM; ++i) {
+#pragma unroll
+        for (int n = 0; n < (kSwiglu ? S::TN / 2 : S::TN); ++n)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (kSwiglu)
+                        v[e] = silu_mul(acc[i][2 * n][4 * g + e], acc[i][2 * n + 1][4 * g + e]);
+                    else
+                        v[e] = acc[i][n][4 * g + e];
+                }
+                store_n<kT, 4>(mine + j * kStride + (n * 32 + 8 * g + 4 * h) * sizeof(T), v);
+            }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int p = 0; p < 32 * kLanes / 64; ++p) {
+            const int row = p * (64 / kLanes) + lane / kLanes, col = (lane % kLanes) * kVec;
+            const int64_t r = t.m0 + (wm * S::TM + i) * 32 + row;
+            const uint8_t* from = mine + row * kStride + col * sizeof(T);
+            if (r < t.m1 && c0 + col < a.N) {
+                T* o = static_cast<T*>(a.out) + r * a.out_stride + c0 + col;
+                if (vec && c0 + col + kVec <= a.N) {
+                    *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(from);
+                } else {
+                    const T* f = reinterpret_cast<const T*>(from);
+                    for (int e = 0; e < kVec && c0 + col + e < a.N; ++e) o[e] = f[e];
+                }
             }
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            acc[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv[i], acc[i], 4, 4, 0, sa, 0, sb[i]);
+        __builtin_amdgcn_wave_barrier();
     }
-    uint8_t* out = static_cast<uint8_t*>(a.out);
+}
+
+// ----------------------------------------------------------- few-row kernel ---
+// Up to 32 rows of a group by 32 columns (SwiGLU: 32 gate and 32 up rows of B) per
+// workgroup; its waves take every eighth run of 256 codes of K, fed straight from memory,
+// and add up through LDS in wave order.  What bounds it is B's bytes, read once: lane half
+// h takes blocks 4 h + s of a run, 64 consecutive bytes of a row in four loads.
+constexpr int kFewWaves = 8;
+
+template <int kT, bool kSwiglu, bool kAligned>
+__global__ __launch_bounds__(64 * kFewWaves) void k_mx_few(MxGemm a)
+{
+    constexpr int NT = kSwiglu ? 2 : 1;
+    __shared__ float red[kFewWaves][NT][32][33];
+    const Tile t = tile_of_slot<32>(a, blockIdx.x);
+    if (t.m0 >= t.m1) return;                             // uniform
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, j = lane & 31;
+    const int nb = a.K / 32, NB = kSwiglu ? 2 * a.N : a.N;
+    const int n0 = (int)blockIdx.y * 32;
+    const int64_t ar = a_row(a, t.m0 + j < t.m1 ? t.m0 + j : t.m1 - 1);
+    const int bn = n0 + j < a.N ? n0 + j : a.N - 1;
+    const uint8_t* xc = a.a_codes + ar * (a.K / 2);
+    const uint8_t* xs = a.a_scales + ar * nb;
+    const uint8_t* wc[NT];
+    const uint8_t* ws[NT];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int64_t row = t.m0 + 8 * (i >> 2) + 4 * h + (i & 3);
-        if (row >= t.m1) continue;
-        typedef typename Elem<kT>::type T;
-        T* o = reinterpret_cast<T*>(out) + row * a.out_stride;
-        if (kSwiglu) {
-            const float gt = acc[0][i];
-            if (n0 + j < a.N) o[n0 + j] = from_f32<kT>(gt / (1.0f + exp_cw(-gt)) * acc[1][i]);
-        } else {
-            if (n0 + j < a.N) o[n0 + j] = from_f32<kT>(acc[0][i]);
-            if (n0 + 32 + j < a.N) o[n0 + 32 + j] = from_f32<kT>(acc[1][i]);
+    for (int i = 0; i < NT; ++i) {
+        const int64_t r = (int64_t)t.g * NB + bn + i * a.N;
+        wc[i] = a.b_codes + r * (a.K / 2);
+        ws[i] = a.b_scales + r * nb;
+    }
+    v16f acc[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][e] = 0.0f;
+    // four scale bytes from block b on: 0 past the end
+    auto scales4 = [&](const uint8_t* p, int b) -> uint32_t {
+        if (kAligned) return b < nb ? *reinterpret_cast<const uint32_t*>(p + b) : 0u;
+        uint32_t v = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (b + i < nb) v |= (uint32_t)p[b + i] << (8 * i);
+        return v;
+    };
+    const int runs = (nb + 7) >> 3;
+#pragma unroll 2
+    for (int u = wave; u < runs; u += kFewWaves) {
+        const int b = u * 8 + 4 * h;
+        v4i x[4], w[NT][4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const int c = b + s < nb ? b + s : nb - 1;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) w[i][s] = *reinterpret_cast<const v4i*>(wc[i] + c * 16);
+            x[s] = *reinterpret_cast<const v4i*>(xc + c * 16);
         }
+        uint32_t sw[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) sw[i] = scales4(ws[i], b);
+        const uint32_t sx = scales4(xs, b);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+                acc[i] = mfma_fp4(w[i][s], x[s], acc[i], (int)(sw[i] >> (16 * (s >> 1))), (int)(sx >> (16 * (s >> 1))), s & 1);
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) red[wave][i][j][8 * (e >> 2) + 4 * h + (e & 3)] = acc[i][e];
+    __syncthreads();
+    typedef typename Elem<kT>::type T;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const int row = p * 16 + (tid >> 5), col = tid & 31;
+        if (t.m0 + row >= t.m1 || n0 + col >= a.N) continue;
+        float z[NT] = {};
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int w = 0; w < kFewWaves; ++w) z[i] += red[w][i][row][col];
+        static_cast<T*>(a.out)[(t.m0 + row) * a.out_stride + n0 + col] =
+            from_f32<kT>(kSwiglu ? silu_mul(z[0], z[NT - 1]) : z[0]);
     }
 }
 
@@ -269,27 +599,65 @@ hipError_t launch_mx_dequantize(const MxQuant& q, hipStream_t st)
     return hipGetLastError();
 }
 
-template <int kT>
-static void gemm_typed(const MxGemm& g, dim3 grid, hipStream_t st)
+namespace {
+
+using Tile256 = MxShape<2, 2, 4, 4>;      // 256 x 256
+using Tile128 = MxShape<2, 2, 2, 2>;      // 128 x 128
+using Tile64 = MxShape<2, 2, 1, 2>;       // 64 x 128
+
+// Slots of BM rows: see tile_of_slot.
+int64_t slots_of(const MxGemm& g, int BM) { return g.bounds ? g.M / BM + g.G : (g.M + BM - 1) / BM; }
+
+template <class S, int kT, bool kSwiglu, bool kAligned>
+hipError_t launch_tile(const MxGemm& g, hipStream_t st)
 {
-    if (g.swiglu)
-        hipLaunchKernelGGL((k_mx_gemm<kT, true>), grid, dim3(64 * kMxWaves), 0, st, g);
-    else
-        hipLaunchKernelGGL((k_mx_gemm<kT, false>), grid, dim3(64 * kMxWaves), 0, st, g);
+    constexpr int lds = MxLds<S, kAligned>::kBytes;
+    const int n_tiles = (int)nblk(g.N, kSwiglu ? S::BN / 2 : S::BN);
+    const int64_t slots = slots_of(g, S::BM), total = slots * n_tiles;
+    if (total > INT32_MAX - 8) return hipErrorInvalidValue;
+    if (lds > 65536) {                    // more than the default limit of dynamic LDS
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_mx_tile<S, kT, kSwiglu, kAligned>),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((k_mx_tile<S, kT, kSwiglu, kAligned>), dim3(8 * nblk(total, 8)), dim3(64 * S::NW), lds, st, g,
+                       n_tiles, slots);
+    return hipGetLastError();
 }
+
+template <int kT, bool kSwiglu, bool kAligned>
+hipError_t launch_shape(const MxGemm& g, hipStream_t st)
+{
+    const int64_t rows = g.M / g.G;       // rows a group has on average
+    auto tiles = [&](int BM, int BN) { return (g.bounds ? g.M / BM + 1 : (g.M + BM - 1) / BM) * nblk(g.N, kSwiglu ? BN / 2 : BN); };
+    if (rows <= 32) {
+        hipLaunchKernelGGL((k_mx_few<kT, kSwiglu, kAligned>), dim3((unsigned)slots_of(g, 32), nblk(g.N, 32)),
+                           dim3(64 * kFewWaves), 0, st, g);
+        return hipGetLastError();
+    }
+    if (rows >= 192 && tiles(256, 256) >= 192) return launch_tile<Tile256, kT, kSwiglu, kAligned>(g, st);
+    if (rows >= 96 && tiles(128, 128) >= 192) return launch_tile<Tile128, kT, kSwiglu, kAligned>(g, st);
+    return launch_tile<Tile64, kT, kSwiglu, kAligned>(g, st);
+}
+
+template <int kT>
+hipError_t launch_typed(const MxGemm& g, hipStream_t st)
+{
+    // every row's scale bytes 4-byte aligned
+    const bool aligned = (g.K / 32) % 4 == 0 &&
+                         (reinterpret_cast<uintptr_t>(g.a_scales) | reinterpret_cast<uintptr_t>(g.b_scales)) % 4 == 0;
+    if (g.swiglu) return aligned ? launch_shape<kT, true, true>(g, st) : launch_shape<kT, true, false>(g, st);
+    return aligned ? launch_shape<kT, false, true>(g, st) : launch_shape<kT, false, false>(g, st);
+}
+
+}  // namespace
 
 hipError_t launch_mx_gemm(const MxGemm& g, hipStream_t st)
 {
     if (g.M == 0) return hipSuccess;
-    const int64_t slots = g.bounds ? g.M / kMxBM + g.G : (int64_t)nblk(g.M, kMxBM);
-    const dim3 grid((unsigned)slots, nblk(g.N, g.swiglu ? kMxBN : 2 * kMxBN));
-    if (g.dtype == kF32)
-        gemm_typed<kF32>(g, grid, st);
-    else if (g.dtype == kBF16)
-        gemm_typed<kBF16>(g, grid, st);
-    else
-        gemm_typed<kF16>(g, grid, st);
-    return hipGetLastError();
+    if (g.dtype == kF32) return launch_typed<kF32>(g, st);
+    if (g.dtype == kBF16) return launch_typed<kBF16>(g, st);
+    return launch_typed<kF16>(g, st);
 }
 
 }  // namespace moe

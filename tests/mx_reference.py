@@ -56,8 +56,9 @@ def mx_product(a, b, bounds=None, rows=None, top_k=1, swiglu=False):
     M = rows.numel() if rows is not None else a.shape[0] * top_k
     src = (rows.cpu().long() if rows is not None else torch.arange(M)) // top_k
     NB = b.shape[1]
-    z = torch.full((M, NB), math.nan, dtype=torch.float64)
-    mag = torch.full((M, NB), math.nan, dtype=torch.float64)
+    src = src.to(a.device)
+    z = torch.full((M, NB), math.nan, dtype=torch.float64, device=a.device)
+    mag = torch.full_like(z, math.nan)
     edges = bounds.tolist() if bounds is not None else [0, M]
     for g, (lo, hi) in enumerate(zip(edges, edges[1:])):
         if hi > lo:

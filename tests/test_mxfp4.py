@@ -190,6 +190,38 @@ def test_dense_product(M, N, K, dtype, swiglu):
     assert (buf[:, N:] == 77).all()
 
 
+@gpu
+@pytest.mark.parametrize("K", [128, 480])                 # scale bytes of a row 4-byte aligned, and not
+@pytest.mark.parametrize("swiglu,dtype", [(False, torch.bfloat16), (True, torch.float32), (False, torch.float32)])
+@pytest.mark.parametrize("M,N", [(3500, 3600), (1200, 2500), (4100, 1030)])
+def test_large_products_take_the_wider_tiles(M, N, K, swiglu, dtype):
+    """Row and column counts of no tile's multiple, at which each of the wider tiles is chosen."""
+    g = gen(M + N + K)
+    N = N // 2 if swiglu else N
+    ac, asc = random_mx(g, M, K, hi=122)
+    bc, bsc = random_mx(g, 2 * N if swiglu else N, K, hi=122)
+    out = torch.full((M + 2, N), 77.0, dtype=dtype, device="cuda")
+    mp.moe_mxfp4_gemm(ac.cuda(), asc.cuda(), bc.cuda(), bsc.cuda(), out[:M], swiglu=swiglu)
+    want, err = ref.mx_product(ref.mx_values(ac, asc).cuda(), ref.mx_values(bc, bsc)[None].cuda(), swiglu=swiglu)
+    check_product(out[:M], dtype, want.cpu(), err.cpu())
+    assert (out[M:] == 77).all()
+
+
+@gpu
+@pytest.mark.parametrize("M,G,k,N,K,swiglu", [(9000, 20, 3, 1500, 96, False), (6000, 40, 2, 1100, 256, True), (5000, 70, 1, 900, 160, False)])
+def test_large_grouped_products(M, G, k, N, K, swiglu):
+    g = gen(M + G)
+    ac, asc = random_mx(g, M // k, K, hi=122)
+    M = M // k * k
+    bc, bsc = random_mx(g, G, 2 * N if swiglu else N, K, hi=122)
+    bounds = groups_of("random", G, M, g)
+    rows = torch.randperm(M, generator=g).int()
+    out = torch.full((M, N), 77.0, device="cuda")
+    mp.moe_mxfp4_gemm(ac.cuda(), asc.cuda(), bc.cuda(), bsc.cuda(), out, bounds=bounds.cuda(), rows=rows.cuda(), top_k=k, swiglu=swiglu)
+    want, err = ref.mx_product(ref.mx_values(ac, asc).cuda(), ref.mx_values(bc, bsc).cuda(), bounds, rows, k, swiglu)
+    check_product(out, torch.float32, want.cpu(), err.cpu())
+
+
 def groups_of(kind, G, M, g):
     """Ascending bounds [G + 1] of M rows: empty groups at both ends and inside, one that holds all, ..."""
     if kind == "one":
