@@ -10,6 +10,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "moe_dtype.h"
 #include "moe_math.h"
 #include "moe_mx.h"
@@ -140,8 +142,8 @@ __global__ __launch_bounds__(kQuantThreads) void k_mx_dequantize(MxQuant q, int6
 // consecutive result registers.
 //
 // Which K-block a lane's 32 codes are is free as long as both operands agree: lane half h
-// takes block 2 h + s in step s of a 128-code stage (4 blocks a row), so that its two
-// scale bytes are neighbours.
+// takes block 4 h + s in step s of a 256-code stage (8 blocks a row), so that its four
+// scale bytes are one word.
 //
 // A block past the end of K is read from the last block (in bounds, any finite codes) with
 // scale byte 0 on both sides: 2^-254 of a product below 2^11 is 0 in fp32.
@@ -187,17 +189,18 @@ __device__ __forceinline__ Tile tile_of_slot(const MxGemm& a, int64_t slot)
 // A row of the product reads this row of A.
 __device__ __forceinline__ int64_t a_row(const MxGemm& a, int64_t r)
 {
-    const int64_t src = (a.rows ? (int64_t)a.rows[r] : r) / a.row_div;
+    int src = a.rows ? a.rows[r] : (int)r;                // r < 2^31
+    if (a.row_div > 1) src /= a.row_div;
     return src < 0 ? 0 : (src >= a.a_rows ? a.a_rows - 1 : src);
 }
 
-__device__ __forceinline__ v16f mfma_fp4(v4i w, v4i x, v16f c, int sw, int sx, bool second)
+// step: which byte of the two registers holds the scale (the instruction's own selector)
+template <int step>
+__device__ __forceinline__ v16f mfma_fp4(v4i w, v4i x, v16f c, int sw, int sx)
 {
     const v8i w8 = __builtin_shufflevector(w, w, 0, 1, 2, 3, -1, -1, -1, -1);
     const v8i x8 = __builtin_shufflevector(x, x, 0, 1, 2, 3, -1, -1, -1, -1);
-    // formats 4, 4: E2M1; the scale byte is byte 0 or 1 of its register
-    return second ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, x8, c, 4, 4, 1, sw, 1, sx)
-                  : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, x8, c, 4, 4, 0, sw, 0, sx);
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, x8, c, 4, 4, step, sw, step, sx);   // 4: E2M1
 }
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + exp_cw(-g)) * u; }
@@ -219,38 +222,45 @@ __device__ __forceinline__ void g2lds4(const void* g, uint32_t lds)
     asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(lds) : "memory", "m0");
 }
 
-// Chunk c (16 bytes, one block) of a 64-byte row r sits in slot c ^ swz(r): any 16
-// consecutive rows touch 16 distinct 16-byte bank groups.
-__device__ __forceinline__ int swz(int r) { return ((r >> 1) ^ (r >> 2)) & 3; }
-
-constexpr int kMxRing = 4;
+// Chunk c (16 bytes, one block) of a 128-byte row r sits in slot c ^ swz(r): any 8
+// consecutive rows touch 8 distinct 16-byte bank groups of 128 bytes, any 16 rows 16
+// distinct ones of 256.
+__device__ __forceinline__ int swz(int r) { return (r ^ ((r >> 3) & 1)) & 7; }
 
 // WM x WN waves, each TM x TN tiles of 32 x 32: BM rows of A by BN rows of B, K in stages of
-// 128 codes through a ring of four LDS slots.
+// 256 codes (128 bytes a row) through two LDS slots.
+//
+// A row's 128 bytes are one cache line: 64-byte rows (128-code stages) and scales loaded a
+// word per row asked the L2 for 20 M lines at 8192 x 4096 x 4096, more than its channels
+// serve in the products' time (97 us).
 template <int WM_, int WN_, int TM_, int TN_>
 struct MxShape {
     static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_;
     static constexpr int NW = WM * WN, BM = 32 * WM * TM, BN = 32 * WN * TN, kRows = BM + BN;
-    static constexpr int NL = kRows / 16 / NW;            // 1 KiB data loads per wave and stage
-    static_assert(NL * NW * 16 == kRows, "whole loads");
+    static constexpr int NL = kRows / 8 / NW;             // 1 KiB data loads per wave and stage
+    static_assert(NL * NW * 8 == kRows, "whole loads");
 };
 
-template <class S, bool kAligned>
+// How the scale bytes come in, by the alignment of the rows of both scale matrices: 16 bytes
+// a row every second stage; two words a row and stage; three words a row and stage around
+// bytes at any address.
+enum ScaleMode { kScale16, kScale4, kScale1 };
+
+template <class S, int kMode>
 struct MxLds {
-    // scale dwords a row: one (4 blocks) where every row's bytes are 4-byte aligned, else the two
-    // aligned dwords around them
-    static constexpr int kDw = kAligned ? 1 : 2;
-    static constexpr int NS = (S::kRows * kDw + 64 * S::NW - 1) / (64 * S::NW);
-    static constexpr int kScaleOff = S::kRows * 64;
-    static constexpr int kSlot = kScaleOff + NS * S::NW * 256;
-    static constexpr int kBytes = kMxRing * kSlot;
-    static constexpr int kLoads = S::NL + NS;             // per wave and stage
+    static constexpr int kRowBytes = kMode == kScale16 ? 16 : kMode == kScale4 ? 8 : 12;
+    static constexpr int kPerLoad = kMode == kScale16 ? 1024 : 256;         // bytes of a wave's scale load
+    static constexpr int NS = (S::kRows * kRowBytes + kPerLoad * S::NW - 1) / (kPerLoad * S::NW);
+    static constexpr int kDataBytes = S::kRows * 128;
+    static constexpr int kScaleBytes = NS * S::NW * kPerLoad;
+    static constexpr int kScaleOff = 2 * kDataBytes;
+    static constexpr int kBytes = 2 * kDataBytes + 2 * kScaleBytes;
 };
 
-template <class S, int kT, bool kSwiglu, bool kAligned>
+template <class S, int kT, bool kSwiglu, int kMode>
 __global__ __launch_bounds__(64 * S::NW) void k_mx_tile(MxGemm a, int n_tiles, int64_t n_slots)
 {
-    using L = MxLds<S, kAligned>;
+    using L = MxLds<S, kMode>;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, j = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -265,14 +275,14 @@ __global__ __launch_bounds__(64 * S::NW) void k_mx_tile(MxGemm a, int n_tiles, i
         const int64_t total = n_slots * n_tiles, per = (total + 7) >> 3;
         const int64_t id = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
         if ((blockIdx.x >> 3) >= per || id >= total) return;
-        const int64_t band = id / (8 * n_tiles), first = band * 8;
-        const int high = n_slots - first < 8 ? (int)(n_slots - first) : 8;
-        const int in = (int)(id - first * n_tiles);
-        nt = in / high;
+        const uint32_t band = (uint32_t)id / (uint32_t)(8 * n_tiles), first = band * 8;   // total < 2^31
+        const uint32_t high = n_slots - first < 8 ? (uint32_t)(n_slots - first) : 8;
+        const uint32_t in = (uint32_t)id - first * n_tiles;
+        nt = (int)(in / high);
         t = tile_of_slot<S::BM>(a, first + in % high);
     }
     if (t.m0 >= t.m1) return;                             // uniform
-    const int nb = a.K / 32, nst = (nb + 3) >> 2;
+    const int nb = a.K / 32, nst = (nb + 7) >> 3;
     const int NB = kSwiglu ? 2 * a.N : a.N;
     constexpr int kOutCols = kSwiglu ? S::BN / 2 : S::BN;
     const int n0 = nt * kOutCols;
@@ -291,87 +301,101 @@ __global__ __launch_bounds__(64 * S::NW) void k_mx_tile(MxGemm a, int n_tiles, i
         return (int64_t)t.g * NB + n;
     };
 
-    const uint8_t* dsrc[S::NL];                           // this lane's chunk of its row, per load
-    int dchunk[S::NL];
+    const uint8_t* dsrc[S::NL];                           // this lane's row, per load
+    const int dchunk = lane & 7;                          // ... and slot in it
+    int dswz[S::NL];
 #pragma unroll
     for (int l = 0; l < S::NL; ++l) {
-        const int q = (wave * S::NL + l) * 16 + (lane >> 2);
+        const int q = (wave * S::NL + l) * 8 + (lane >> 3);
         bool is_a;
         const int64_t r = src_row(q, is_a);
-        dchunk[l] = (lane & 3) ^ swz(q);
+        dswz[l] = dchunk ^ swz(q);
         dsrc[l] = (is_a ? a.a_codes : a.b_codes) + r * (a.K / 2);
+        if (kMode == kScale16) dsrc[l] += dswz[l] * 16;   // K is a multiple of 512: no clamp below
     }
-    const uint8_t* ssrc[L::NS];                           // the dword this lane loads of a row's scales
-    const uint8_t* slast[L::NS];                          // the last aligned dword that holds one of them
+    const uint8_t* ssrc[L::NS];                           // where this lane's scale loads start
+    const uint8_t* slast[L::NS];                          // kScale1: the last aligned word that holds one of the row's bytes
 #pragma unroll
     for (int l = 0; l < L::NS; ++l) {
         int i = (wave * L::NS + l) * 64 + lane;
-        i = i < S::kRows * L::kDw ? i : 0;
-        const int q = i / L::kDw;
+        constexpr int kParts = kMode == kScale16 ? 1 : L::kRowBytes / 4;
+        i = i < S::kRows * kParts ? i : 0;
+        const int q = i / kParts, part = i % kParts;
         bool is_a;
         const int64_t r = src_row(q, is_a);
         const uint8_t* p = (is_a ? a.a_scales : a.b_scales) + r * nb;
-        if (kAligned) {
-            ssrc[l] = p;
-        } else {
-            // the aligned dwords around the row's bytes; a dword that holds a valid byte lies in
-            // that byte's page
+        if constexpr (kMode == kScale1) {
+            // a word that holds a valid byte lies in that byte's page
             slast[l] = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(p + nb - 1) & ~(uintptr_t)3);
-            ssrc[l] = reinterpret_cast<const uint8_t*>((reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)3) + 4 * (i % L::kDw));
+            p = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)3);
+        } else {
+            slast[l] = p + nb - 4;
         }
+        ssrc[l] = p + 4 * part;
     }
-    int mis[S::TM + S::TN];                               // unaligned: where the row's first byte is in its dword
-    if (!kAligned) {
+    constexpr int kOps = S::TM + S::TN, kProd = S::TM * S::TN;
+    const int sa_base = wm * S::TM * 32 + j, sb_base = S::BM + wn * S::TN * 32 + j;
+    auto op_row = [&](int i) { return i < S::TM ? sa_base + i * 32 : sb_base + (i - S::TM) * 32; };
+    int mis[kOps];                                        // kScale1: where the row's first byte is in its word
+    if constexpr (kMode == kScale1) {
 #pragma unroll
-        for (int i = 0; i < S::TM + S::TN; ++i) {
-            const int q = i < S::TM ? (wm * S::TM + i) * 32 + j : S::BM + (wn * S::TN + i - S::TM) * 32 + j;
+        for (int i = 0; i < kOps; ++i) {
             bool is_a;
-            const int64_t r = src_row(q, is_a);
+            const int64_t r = src_row(op_row(i), is_a);
             mis[i] = (int)(reinterpret_cast<uintptr_t>((is_a ? a.a_scales : a.b_scales) + r * nb) & 3);
         }
     }
 
     const uint32_t lds0 = lds_addr(lds);
-    // load l (of kLoads) of stage s (clamped: tail loads repeat the last stage) into ring slot `slot`
-    auto issue = [&](int l, int s, int slot) {
+    // data load l of stage s (clamped: a load past the last stage repeats it) into slot s % 2
+    auto issue_data = [&](int l, int s) {
+        const uint32_t to = lds0 + (s & 1) * L::kDataBytes + (wave * S::NL + l) * 1024;
         const int sc = s < nst ? s : nst - 1;
-        const uint32_t base = lds0 + slot * L::kSlot;
-        if (l < S::NL) {
-            int c = sc * 4 + dchunk[l];
-            if (!kAligned) c = c < nb ? c : nb - 1;
-            g2lds16(dsrc[l] + c * 16, base + (wave * S::NL + l) * 1024);
+        if constexpr (kMode == kScale16) {
+            g2lds16(dsrc[l] + sc * 128, to);
         } else {
-            const uint8_t* p = ssrc[l - S::NL] + sc * 4;
-            if (!kAligned) p = p < slast[l - S::NL] ? p : slast[l - S::NL];
-            g2lds4(p, base + L::kScaleOff + (wave * L::NS + l - S::NL) * 256);
+            const int c = sc * 8 + dswz[l];
+            g2lds16(dsrc[l] + (c < nb ? c : nb - 1) * 16, to);
+        }
+    };
+    // scale load l of stage s (kScale16: of the stages s, s + 1 for an even s, buffer s / 2 % 2)
+    auto issue_scales = [&](int l, int s) {
+        const int sc = s < nst ? s : (kMode == kScale16 ? (nst - 1) & ~1 : nst - 1);
+        const int buf = kMode == kScale16 ? (s >> 1) & 1 : s & 1;
+        const uint32_t to = lds0 + L::kScaleOff + buf * L::kScaleBytes + (wave * L::NS + l) * L::kPerLoad;
+        const uint8_t* p = ssrc[l] + sc * 8;
+        if constexpr (kMode == kScale16) {
+            g2lds16(p, to);
+        } else {
+            g2lds4(p < slast[l] ? p : slast[l], to);
         }
     };
 
     // Operands of one step: tiles of the activations, then of the weights.  Tile rows are 32
     // apart, so the swizzle is that of row j.
     struct Ops {
-        v4i v[S::TM + S::TN];
+        v4i v[kOps];
     };
     struct Scales {
-        int v[S::TM + S::TN];
+        int v[kOps];
     };
-    const int a_base = (wm * S::TM * 32 + j) * 64, b_base = (S::BM + wn * S::TN * 32 + j) * 64;
-    const int ch[2] = {((2 * h) ^ swz(j)) * 16, ((2 * h + 1) ^ swz(j)) * 16};
-    auto read_op = [&](int i, int slot, int step, Ops& o) {
-        const uint8_t* base = lds + slot * L::kSlot + ch[step];
-        o.v[i] = *reinterpret_cast<const v4i*>(base + (i < S::TM ? a_base + i * 2048 : b_base + (i - S::TM) * 2048));
+    auto read_op = [&](int i, int s, int step, Ops& o) {
+        o.v[i] = *reinterpret_cast<const v4i*>(lds + (s & 1) * L::kDataBytes + op_row(i) * 128 +
+                                               (((4 * h + step) ^ swz(j)) << 4));
     };
-    // the scale bytes of both steps (bytes 0 and 1)
-    const int sa_base = wm * S::TM * 32 + j, sb_base = S::BM + wn * S::TN * 32 + j;
-    auto read_scale = [&](int i, int s, int slot, Scales& o) {
-        const uint8_t* base = lds + slot * L::kSlot + L::kScaleOff;
-        const int q = i < S::TM ? sa_base + i * 32 : sb_base + (i - S::TM) * 32;
-        if (kAligned) {
-            o.v[i] = *reinterpret_cast<const uint16_t*>(base + q * 4 + 2 * h);
+    // the scale bytes of this lane half's four blocks of stage s: 0 past the end of K
+    auto read_scale = [&](int i, int s, Scales& o) {
+        const uint8_t* base = lds + L::kScaleOff;
+        if constexpr (kMode == kScale16) {
+            o.v[i] = *reinterpret_cast<const int*>(base + ((s >> 1) & 1) * L::kScaleBytes + op_row(i) * 16 + (s & 1) * 8 + 4 * h);
+        } else if constexpr (kMode == kScale4) {
+            const int v = *reinterpret_cast<const int*>(base + (s & 1) * L::kScaleBytes + op_row(i) * 8 + 4 * h);
+            o.v[i] = 8 * s + 4 * h < nb ? v : 0;
         } else {
-            const uint8_t* p = base + q * 8 + mis[i] + 2 * h;
-            const int b = 4 * s + 2 * h;
-            o.v[i] = (b < nb ? p[0] : 0) | (b + 1 < nb ? p[1] << 8 : 0);
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(base + (s & 1) * L::kScaleBytes + op_row(i) * 12 + 4 * h);
+            const uint32_t v = __builtin_amdgcn_alignbyte(p[1], p[0], mis[i]);
+            const int left = nb - (8 * s + 4 * h);
+            o.v[i] = (int)(left >= 4 ? v : left <= 0 ? 0u : v & ((1u << (8 * left)) - 1u));
         }
     };
 
@@ -383,58 +407,75 @@ __global__ __launch_bounds__(64 * S::NW) void k_mx_tile(MxGemm a, int n_tiles, i
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][n][e] = 0.0f;
 
-    // Stage s: its second step's operands are read under the first step's products, the next
-    // stage's first step's under the second's.  The barrier between them frees stage s's slot
-    // (every wave has read it) for stage s + 4 and admits stage s + 1 (two stages may still be
-    // in flight behind it).  Each memory instruction is placed behind a product of its own, in
-    // whose 32 cycles it issues: the loads in a row before the products left the matrix core
-    // idle (8192 x 4096 x 4096: 100 us).
-    constexpr int kOps = S::TM + S::TN, kProd = S::TM * S::TN;
-    auto products = [&](const Ops& o, const Scales& sc, bool second, auto between) {
+    // Stage s, four steps of kProd products.  Steps 0 and 1 read the operands of steps 1 to 3;
+    // then every wave has read its share of slot s % 2, and the barrier frees it for stage
+    // s + 2 and admits stage s + 1 (its loads, the only ones out, have had a stage's time).
+    // Step 2 issues the loads of stage s + 2, step 3 reads step 0 of stage s + 1.  Each memory
+    // instruction is placed behind a product of its own, in whose 32 cycles it issues.
+    auto products = [&](auto step_c, const Ops& o, const Scales& sc, auto between) {
 #pragma unroll
         for (int i = 0; i < S::TM; ++i)
 #pragma unroll
             for (int n = 0; n < S::TN; ++n) {
-                acc[i][n] = mfma_fp4(o.v[S::TM + n], o.v[i], acc[i][n], sc.v[S::TM + n], sc.v[i], second);
+                acc[i][n] = mfma_fp4<decltype(step_c)::value>(o.v[S::TM + n], o.v[i], acc[i][n], sc.v[S::TM + n], sc.v[i]);
                 between(i * S::TN + n);
                 __builtin_amdgcn_sched_barrier(0);
             }
     };
-    Ops o0, o1;
+    Ops o0, o1, o2, o3;
     Scales sc0, sc1;
     auto stage = [&](int s) {
-        const int slot = s % kMxRing, next = (s + 1) % kMxRing;
-        products(o0, sc0, false, [&](int at) {
+        products(std::integral_constant<int, 0>{}, o0, sc0, [&](int at) {
 #pragma unroll
-            for (int i = at * kOps / kProd; i < (at + 1) * kOps / kProd; ++i) read_op(i, slot, 1, o1);
+            for (int i = at * 2 * kOps / kProd; i < (at + 1) * 2 * kOps / kProd; ++i) {
+                if (i < kOps)
+                    read_op(i, s, 1, o1);
+                else
+                    read_op(i - kOps, s, 2, o2);
+            }
         });
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((kMxRing - 2) * L::kLoads) : "memory");
-        products(o1, sc0, true, [&](int at) {
+        products(std::integral_constant<int, 1>{}, o1, sc0, [&](int at) {
+#pragma unroll
+            for (int i = at * kOps / kProd; i < (at + 1) * kOps / kProd; ++i) read_op(i, s, 3, o3);
+        });
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        products(std::integral_constant<int, 2>{}, o2, sc0, [&](int at) {
+            if (kMode != kScale16 || (s & 1) == 0) {
+#pragma unroll
+                for (int l = at * L::NS / kProd; l < (at + 1) * L::NS / kProd; ++l) issue_scales(l, s + 2);
+            }
+#pragma unroll
+            for (int l = at * S::NL / kProd; l < (at + 1) * S::NL / kProd; ++l) issue_data(l, s + 2);
+        });
+        products(std::integral_constant<int, 3>{}, o3, sc0, [&](int at) {
             // past the last stage: a repeated one, not used
 #pragma unroll
             for (int i = at * kOps / kProd; i < (at + 1) * kOps / kProd; ++i) {
-                read_op(i, next, 0, o0);
-                read_scale(i, s + 1, next, sc1);
+                read_op(i, s + 1, 0, o0);
+                read_scale(i, s + 1, sc1);
             }
-#pragma unroll
-            for (int l = at * L::kLoads / kProd; l < (at + 1) * L::kLoads / kProd; ++l) issue(l, s + kMxRing, slot);
         });
     };
 #pragma unroll
-    for (int u = 0; u < kMxRing; ++u)
+    for (int u = 0; u < 2; ++u) {
+        if (kMode != kScale16 || u == 0) {
 #pragma unroll
-        for (int l = 0; l < L::kLoads; ++l) issue(l, u, u);
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((kMxRing - 1) * L::kLoads) : "memory");
+            for (int l = 0; l < L::NS; ++l) issue_scales(l, u);
+        }
+#pragma unroll
+        for (int l = 0; l < S::NL; ++l) issue_data(l, u);
+    }
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(S::NL + (kMode == kScale16 ? 0 : L::NS)) : "memory");
 #pragma unroll
     for (int i = 0; i < kOps; ++i) {
         read_op(i, 0, 0, o0);
-        read_scale(i, 0, 0, sc0);
+        read_scale(i, 0, sc0);
     }
     for (int s = 0; s < nst; ++s) {
         stage(s);
         sc0 = sc1;
     }
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");   // the ring is dead: the epilogue takes it
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");   // the slots are dead: the epilogue takes them
 
     // Epilogue: each wave turns its tile, 32 rows at a time, through LDS of its own into
     // row-major order and writes 16 bytes a lane, whole runs of a row at a time.
@@ -546,7 +587,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx_few(MxGemm a)
         for (int s = 0; s < 4; ++s)
 #pragma unroll
             for (int i = 0; i < NT; ++i)
-                acc[i] = mfma_fp4(w[i][s], x[s], acc[i], (int)(sw[i] >> (16 * (s >> 1))), (int)(sx >> (16 * (s >> 1))), s & 1);
+                acc[i] = mfma_fp4<0>(w[i][s], x[s], acc[i], (int)(sw[i] >> (8 * s)), (int)(sx >> (8 * s)));
     }
 #pragma unroll
     for (int i = 0; i < NT; ++i)
@@ -608,46 +649,50 @@ using Tile64 = MxShape<2, 2, 1, 2>;       // 64 x 128
 // Slots of BM rows: see tile_of_slot.
 int64_t slots_of(const MxGemm& g, int BM) { return g.bounds ? g.M / BM + g.G : (g.M + BM - 1) / BM; }
 
-template <class S, int kT, bool kSwiglu, bool kAligned>
+template <class S, int kT, bool kSwiglu, int kMode>
 hipError_t launch_tile(const MxGemm& g, hipStream_t st)
 {
-    constexpr int lds = MxLds<S, kAligned>::kBytes;
+    constexpr int lds = MxLds<S, kMode>::kBytes;
     const int n_tiles = (int)nblk(g.N, kSwiglu ? S::BN / 2 : S::BN);
     const int64_t slots = slots_of(g, S::BM), total = slots * n_tiles;
     if (total > INT32_MAX - 8) return hipErrorInvalidValue;
-    if (lds > 65536) {                    // more than the default limit of dynamic LDS
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_mx_tile<S, kT, kSwiglu, kAligned>),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-        if (e != hipSuccess) return e;
-    }
-    hipLaunchKernelGGL((k_mx_tile<S, kT, kSwiglu, kAligned>), dim3(8 * nblk(total, 8)), dim3(64 * S::NW), lds, st, g,
+    // more than the default limit of dynamic LDS
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_mx_tile<S, kT, kSwiglu, kMode>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_mx_tile<S, kT, kSwiglu, kMode>), dim3(8 * nblk(total, 8)), dim3(64 * S::NW), lds, st, g,
                        n_tiles, slots);
     return hipGetLastError();
 }
 
-template <int kT, bool kSwiglu, bool kAligned>
+template <int kT, bool kSwiglu, int kMode>
 hipError_t launch_shape(const MxGemm& g, hipStream_t st)
 {
     const int64_t rows = g.M / g.G;       // rows a group has on average
     auto tiles = [&](int BM, int BN) { return (g.bounds ? g.M / BM + 1 : (g.M + BM - 1) / BM) * nblk(g.N, kSwiglu ? BN / 2 : BN); };
     if (rows <= 32) {
-        hipLaunchKernelGGL((k_mx_few<kT, kSwiglu, kAligned>), dim3((unsigned)slots_of(g, 32), nblk(g.N, 32)),
+        hipLaunchKernelGGL((k_mx_few<kT, kSwiglu, kMode != kScale1>), dim3((unsigned)slots_of(g, 32), nblk(g.N, 32)),
                            dim3(64 * kFewWaves), 0, st, g);
         return hipGetLastError();
     }
-    if (rows >= 192 && tiles(256, 256) >= 192) return launch_tile<Tile256, kT, kSwiglu, kAligned>(g, st);
-    if (rows >= 96 && tiles(128, 128) >= 192) return launch_tile<Tile128, kT, kSwiglu, kAligned>(g, st);
-    return launch_tile<Tile64, kT, kSwiglu, kAligned>(g, st);
+    if (rows >= 192 && tiles(256, 256) >= 192) return launch_tile<Tile256, kT, kSwiglu, kMode>(g, st);
+    if (rows >= 96 && tiles(128, 128) >= 192) return launch_tile<Tile128, kT, kSwiglu, kMode>(g, st);
+    return launch_tile<Tile64, kT, kSwiglu, kMode>(g, st);
+}
+
+template <int kT, bool kSwiglu>
+hipError_t launch_mode(const MxGemm& g, hipStream_t st)
+{
+    const uint64_t at = reinterpret_cast<uintptr_t>(g.a_scales) | reinterpret_cast<uintptr_t>(g.b_scales) | (uint64_t)(g.K / 32);
+    if (at % 16 == 0) return launch_shape<kT, kSwiglu, kScale16>(g, st);
+    if (at % 4 == 0) return launch_shape<kT, kSwiglu, kScale4>(g, st);
+    return launch_shape<kT, kSwiglu, kScale1>(g, st);
 }
 
 template <int kT>
 hipError_t launch_typed(const MxGemm& g, hipStream_t st)
 {
-    // every row's scale bytes 4-byte aligned
-    const bool aligned = (g.K / 32) % 4 == 0 &&
-                         (reinterpret_cast<uintptr_t>(g.a_scales) | reinterpret_cast<uintptr_t>(g.b_scales)) % 4 == 0;
-    if (g.swiglu) return aligned ? launch_shape<kT, true, true>(g, st) : launch_shape<kT, true, false>(g, st);
-    return aligned ? launch_shape<kT, false, true>(g, st) : launch_shape<kT, false, false>(g, st);
+    return g.swiglu ? launch_mode<kT, true>(g, st) : launch_mode<kT, false>(g, st);
 }
 
 }  // namespace
