@@ -9,13 +9,14 @@
 namespace moe {
 
 constexpr int kDecodeMaxPairs = 1024;   // n_tokens * top_k of one call
-constexpr int kChunkRows = 8;           // rows of one expert that share one read of its weights
+constexpr int kChunkRows = 16;          // most rows of one expert that share one read of its weights
+constexpr int kChunkRowsF32 = 8;        // ... of fp32 activations (three limbs a row instead of two)
 
-// One work item of the expert products: up to kChunkRows (token, slot) pairs of one expert.
+// One work item of the expert products: (token, slot) pairs of one expert.
 struct DecodeChunk {
     int32_t expert, n;
     int32_t pair[kChunkRows];
-    int32_t pad[6];
+    int32_t pad[2];
 };
 
 struct DecodeWs {
@@ -28,7 +29,7 @@ static inline DecodeWs decode_ws(int d, int f, int E, int k, int T)
     DecodeWs L;
     const uint64_t R = (uint64_t)T * k;
     // sum over experts of ceil(rows / 8): at most one partial chunk per reached expert
-    L.max_chunks = (int)(R / kChunkRows) + (int)(R < (uint64_t)E ? R : (uint64_t)E);
+    L.max_chunks = (int)(R / kChunkRowsF32) + (int)(R < (uint64_t)E ? R : (uint64_t)E);
     uint64_t o = 0;
     auto take = [&](uint64_t bytes) { uint64_t at = o; o = align_up(o + bytes, 256); return at; };
     L.eidx = take(R * 4);
@@ -59,12 +60,14 @@ struct DecodeLaunch {
     DecodeWs L;
     int32_t* eidx_out;         // optional exports
     float* wts_out;
+    bool need_counts;          // the rows per expert (DecodeWs::counts) are read after the routing
 };
 
-// Routing, the chunk table and x's fixed-point form.
+// Routing, the chunk table and x's fixed-point form; nothing where the products route themselves.
 hipError_t launch_decode_route(const DecodeLaunch& D, hipStream_t st);
-// Both expert products (the last reader of the weights).
+// Both expert products (the last reader of the weights), and the combine where they hold it.
 hipError_t launch_decode_products(const DecodeLaunch& D, hipStream_t st);
+// The combine, where the products left it.
 hipError_t launch_decode_combine(const DecodeLaunch& D, hipStream_t st);
 
 }  // namespace moe

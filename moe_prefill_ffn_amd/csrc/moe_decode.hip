@@ -9,16 +9,21 @@
 //   combine   y[t] = sum_j w[t, j] dm[t, j], j ascending
 //
 // What bounds it: the bytes of the experts reached (0.5625 per weight); a token brings
-// two operations per weight, far below the matrix cores' rate.  So the activations can
-// be carried exactly enough to leave no rounding of their own: a block of 32 values is
-// held as 24-bit integers times one power of two (error at most 2^-23 of the block's
-// largest value), split into three signed bytes ("limbs"), and the
-// int8 matrix instruction multiplies the limbs with the 4-bit codes exactly.  The three
-// limbs of eight tokens fill the 32 rows of one instruction, which at these row counts
-// would idle otherwise.  Per 32-block the limb sums are joined exactly in integers and
-// scaled into an fp32 accumulator.
+// two operations per weight, far below the matrix cores' rate.  So the activations are
+// carried with more bits than a quantised product would need: a block of 32 values is held
+// as integers times one power of two, split into signed bytes ("limbs"), and the int8
+// matrix instruction multiplies the limbs with the 4-bit codes exactly.  The limbs of
+// several tokens fill the 32 rows of one instruction, which at these row counts would idle
+// otherwise.  Per 32-block the limb sums are joined exactly in integers and scaled into an
+// fp32 accumulator.
+//   fp32 activations: 24 bits, three limbs (error at most 2^-23 of the block's largest value)
+//   bf16 and fp16: 16 bits, two limbs (2^-15 of the block's largest value: an eighth of an
+//   fp16's own last place there; a third limb costs the sums half as much again and the
+//   output's rounding hides it)
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "moe_decode.h"
 #include "moe_dtype.h"
@@ -32,97 +37,140 @@ typedef int v16i __attribute__((ext_vector_type(16)));
 namespace {
 
 // -------------------------------------------------------------- fixed point ---
-// Exponent field of the fixed-point scale of a block whose largest magnitude has the
-// fp32 bits u: with E = that field, the value is q * 2^(E - 149), |q| <= 0x7F7F7F, so
-// that three signed bytes hold q.  2^17 added to the mantissa moves the top 1/64 of a
-// binade to the next one (q would pass 0x7F7F7F).  E >= 23 keeps 2^(E - 149) normal.
+// NL limbs: integers q of 8 NL bits.  Exponent field of the scale of a block whose largest
+// magnitude has the fp32 bits u: with E = that field, the value is q * 2^(E - 125 - 8 NL) and
+// |q| <= 0x7F7F7F (0x7F7F), so that signed bytes hold it.  2^17 added to the mantissa moves
+// the top 1/64 of a binade to the next one (q would pass that).  E >= 8 NL - 1 keeps the
+// scale normal.
+template <int NL>
 __device__ __forceinline__ int fix_exp(uint32_t u)
 {
     const int e = (int)((u + (1u << 17)) >> 23);
-    return e < 23 ? 23 : e;
+    return e < 8 * NL - 1 ? 8 * NL - 1 : e;
 }
 // the block scale; NaN for a block that holds an infinity or a NaN
+template <int NL>
 __device__ __forceinline__ float fix_scale(uint32_t u, int e)
 {
-    return u >= 0x7f800000u ? __builtin_nanf("") : __uint_as_float((uint32_t)(e - 22) << 23);
+    return u >= 0x7f800000u ? __builtin_nanf("") : __uint_as_float((uint32_t)(e - (8 * NL - 2)) << 23);
 }
-__device__ __forceinline__ int fix_code(float v, int e) { return (int)__builtin_rintf(ldexpf(v, 149 - e)); }
+template <int NL>
+__device__ __forceinline__ int fix_code(float v, int e) { return (int)__builtin_rintf(ldexpf(v, 125 + 8 * NL - e)); }
 
-// q = l0 + 256 l1 + 65536 l2 with signed bytes
-__device__ __forceinline__ void limbs(int q, int& l0, int& l1, int& l2)
+// q = l0 + 256 l1 (+ 65536 l2) with signed bytes
+template <int NL>
+__device__ __forceinline__ void limbs(int q, int (&l)[3])
 {
-    l0 = (int8_t)q;
-    q = (q - l0) >> 8;
-    l1 = (int8_t)q;
-    l2 = (q - l1) >> 8;
+    l[0] = (int8_t)q;
+    q = (q - l[0]) >> 8;
+    l[1] = NL == 2 ? q : (int)(int8_t)q;
+    l[2] = NL == 2 ? 0 : (q - l[1]) >> 8;
 }
+
+// Limb l of token m is row kRowStep m + l of the instruction's 32 rows, so that a lane gets the
+// limb sums of a (token, column) in neighbouring result registers: quad c of lane half h holds
+// rows 8 c + 4 h .. + 3, that is token 2 c + h of three limbs, or tokens 4 c + 2 h and the next
+// of two.
+template <int NL>
+struct Limbs {
+    static constexpr int kRowStep = NL == 2 ? 2 : 4;
+    static constexpr int kTokens = 32 / kRowStep;         // tokens of one instruction, rows of a chunk
+    static constexpr int kPerQuad = 4 / kRowStep;         // tokens of a lane's quad
+    __device__ static __forceinline__ int token(int c, int i, int h) { return kPerQuad * (2 * c + h) + i; }
+};
+constexpr int limbs_of(int dtype) { return dtype == kF32 ? 3 : 2; }
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
 // ------------------------------------------------------------------ routing ---
-// Keys order as (logit descending, expert ascending), -0 as +0: the order of the
-// prompt path's routing.
-__device__ __forceinline__ uint64_t route_key(float v, int e)
+// Keys order the logits (larger first), -0 as +0; equal keys go to the lower expert: the
+// order of the prompt path's routing.  Never 0, which marks a taken slot.
+__device__ __forceinline__ uint32_t route_key(float v)
 {
     uint32_t u = v == 0.0f ? 0u : __float_as_uint(v);
     u = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-    return ((uint64_t)u << 32) | (uint32_t)(0xFFFFFFFFu - (uint32_t)e);
+    return u ? u : 1u;
 }
+constexpr uint32_t kKeyMinusInf = 0x007fffffu;            // route_key(-inf)
 
-__device__ __forceinline__ uint64_t wave_max_u64(uint64_t v)
+// Reductions over a wave by lane moves inside the VALU (a shuffle through LDS takes ten times
+// as long, and a token's routing is a chain of them).  The result is on every lane.
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp0(uint32_t v)
 {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const uint64_t w = ((uint64_t)(uint32_t)__shfl_xor((int)(uint32_t)(v >> 32), o) << 32) |
-                           (uint32_t)__shfl_xor((int)(uint32_t)v, o);
-        v = v > w ? v : w;
-    }
-    return v;
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xf, 0xf, false);
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+    v = umax(v, dpp0<0x111>(v));                          // row_shr 1, 2, 4, 8: rows of 16 lanes
+    v = umax(v, dpp0<0x112>(v));
+    v = umax(v, dpp0<0x114>(v));
+    v = umax(v, dpp0<0x118>(v));
+    v = umax(v, dpp0<0x142>(v));                          // row_bcast 15, 31: row into the next
+    v = umax(v, dpp0<0x143>(v));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ __forceinline__ float add_dpp(float v, uint32_t moved) { return v + __uint_as_float(moved); }
+__device__ __forceinline__ float wave_sum(float v)
+{
+    v = add_dpp(v, dpp0<0x111>(__float_as_uint(v)));
+    v = add_dpp(v, dpp0<0x112>(__float_as_uint(v)));
+    v = add_dpp(v, dpp0<0x114>(__float_as_uint(v)));
+    v = add_dpp(v, dpp0<0x118>(__float_as_uint(v)));
+    v = add_dpp(v, dpp0<0x142>(__float_as_uint(v)));
+    v = add_dpp(v, dpp0<0x143>(__float_as_uint(v)));
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 
-// One token by one wave: the experts of its k slots (-1: not available) and their logits.
-template <int NK>   // keys per lane: E <= 64 * NK
-__device__ __forceinline__ void route_token(const float* __restrict__ lt, int E, int k,
-                                            int* eidx, float* z)
+// One token by one wave: slot(j, e, key) for its first k slots; e = -1: not available.
+template <int NK, class F>   // keys per lane: E <= 64 * NK
+__device__ __forceinline__ void route_token(const float* __restrict__ lt, int E, int k, F slot)
 {
     const int lane = threadIdx.x & 63;
-    uint64_t key[NK];
+    uint32_t key[NK];
 #pragma unroll
     for (int i = 0; i < NK; ++i) {
         const int e = lane + 64 * i;
-        key[i] = e < E ? route_key(lt[e], e) : 0ull;      // 0: below every real key
+        const uint32_t u = route_key(lt[e < E ? e : E - 1]);
+        key[i] = e < E ? u : 0u;
     }
     for (int j = 0; j < k; ++j) {
-        uint64_t m = key[0];
+        uint32_t m = key[0];
 #pragma unroll
-        for (int i = 1; i < NK; ++i) m = key[i] > m ? key[i] : m;
-        m = wave_max_u64(m);
+        for (int i = 1; i < NK; ++i) m = umax(m, key[i]);
+        m = wave_max(m);
+        // the lowest expert that holds it: experts lane + 64 i, so the lowest i, then lane
+        int e = -1;
 #pragma unroll
-        for (int i = 0; i < NK; ++i) key[i] = key[i] == m ? 0ull : key[i];
-        if (lane == 0) {
-            const int e = (int)(0xFFFFFFFFu - (uint32_t)m);
-            const float l = lt[e];
-            eidx[j] = l == -__builtin_inff() ? -1 : e;
-            z[j] = l;
+        for (int i = NK - 1; i >= 0; --i) {
+            const uint64_t has = __ballot(key[i] == m);
+            e = has ? 64 * i + (int)__builtin_ctzll(has) : e;
         }
+#pragma unroll
+        for (int i = 0; i < NK; ++i) key[i] = lane + 64 * i == e ? 0u : key[i];
+        slot(j, m == kKeyMinusInf ? -1 : e, m);
     }
 }
 
-// Weights of one token's slots by one wave: softmax over the available ones, summed in
-// slot order; 0 for the others (also where none is available).
+// the logit of a key
+__device__ __forceinline__ float key_logit(uint32_t u)
+{
+    return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
+}
+
+// Weights of one token's k slots by one wave, from the experts (-1: weight 0) and the logits in
+// z (LDS), which they replace: softmax over the available ones; all 0 where there is none.
 __device__ __forceinline__ void route_weights(int k, const int* eidx, float* z)
 {
     const int lane = threadIdx.x & 63;
     __builtin_amdgcn_wave_barrier();
     const float top = z[0];
+    float part = 0.0f;
+    for (int j = lane; j < k; j += 64) part += eidx[j] < 0 ? 0.0f : exp_cw(z[j] - top);
+    const float sum = wave_sum(part);
+    for (int j = lane; j < k; j += 64) z[j] = eidx[j] < 0 ? 0.0f : exp_cw(z[j] - top) / sum;
     __builtin_amdgcn_wave_barrier();
-    for (int j = lane; j < k; j += 64) z[j] = eidx[j] < 0 ? 0.0f : exp_cw(z[j] - top);
-    __builtin_amdgcn_wave_barrier();
-    float sum = 0.0f;
-    for (int j = 0; j < k; ++j) sum += z[j];
-    __builtin_amdgcn_wave_barrier();
-    for (int j = lane; j < k; j += 64) z[j] = eidx[j] < 0 ? 0.0f : z[j] / sum;
 }
 
 constexpr int kRouteThreads = 1024;
@@ -133,12 +181,12 @@ struct RouteArgs {
     const float* logits;
     int64_t logits_stride;
     int T, E, k;
+    int chunk_rows;
     int32_t* eidx;
     float* wts;
     int32_t* counts;
     int32_t* nchunks;
     DecodeChunk* chunks;
-    int max_chunks;
     int32_t* eidx_out;
     float* wts_out;
     const void* x;
@@ -149,7 +197,7 @@ struct RouteArgs {
 };
 
 // Workgroup 0 routes every token (a token per wave at a time) and lists the chunks: per
-// expert its pairs in groups of kChunkRows.  A pair's row inside its chunk depends on
+// expert its pairs in groups of chunk_rows.  A pair's row inside its chunk depends on
 // the order of LDS atomics; nothing else does, since every row is computed by itself.
 __device__ __forceinline__ void route_all(const RouteArgs& a)
 {
@@ -163,11 +211,21 @@ __device__ __forceinline__ void route_all(const RouteArgs& a)
     s_fill[tid] = 0;
     for (int t = wave; t < a.T; t += kRouteWaves) {
         const float* lt = a.logits + (int64_t)t * a.logits_stride;
-        if (a.E <= 256)
-            route_token<4>(lt, a.E, a.k, s_eidx + t * a.k, s_z + t * a.k);
+        int* te = s_eidx + t * a.k;
+        float* tz = s_z + t * a.k;
+        auto slot = [&](int j, int e, uint32_t key) {
+            if (lane == 0) {
+                te[j] = e;
+                tz[j] = key_logit(key);
+            }
+        };
+        if (a.E <= 128)
+            route_token<2>(lt, a.E, a.k, slot);
+        else if (a.E <= 256)
+            route_token<4>(lt, a.E, a.k, slot);
         else
-            route_token<16>(lt, a.E, a.k, s_eidx + t * a.k, s_z + t * a.k);
-        route_weights(a.k, s_eidx + t * a.k, s_z + t * a.k);
+            route_token<16>(lt, a.E, a.k, slot);
+        route_weights(a.k, te, tz);
     }
     __syncthreads();
     const int e_of = tid < R ? s_eidx[tid] : -1;          // R <= kRouteThreads
@@ -180,7 +238,7 @@ __device__ __forceinline__ void route_all(const RouteArgs& a)
     }
     __syncthreads();
     const int c = tid < a.E ? s_cnt[tid] : 0;
-    const int nc = (c + kChunkRows - 1) / kChunkRows;
+    const int nc = (c + a.chunk_rows - 1) / a.chunk_rows;
     int incl = nc;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -200,45 +258,57 @@ __device__ __forceinline__ void route_all(const RouteArgs& a)
         a.counts[tid] = c;
         for (int i = 0; i < nc; ++i) {
             a.chunks[first + i].expert = tid;
-            a.chunks[first + i].n = c - i * kChunkRows < kChunkRows ? c - i * kChunkRows : kChunkRows;
+            a.chunks[first + i].n = c - i * a.chunk_rows < a.chunk_rows ? c - i * a.chunk_rows : a.chunk_rows;
         }
     }
     if (tid == 0) *a.nchunks = total;
     __syncthreads();
     if (e_of >= 0) {
         const int r = atomicAdd(&s_fill[e_of], 1);
-        a.chunks[s_first[e_of] + r / kChunkRows].pair[r % kChunkRows] = tid;
+        a.chunks[s_first[e_of] + r / a.chunk_rows].pair[r % a.chunk_rows] = tid;
     }
 }
 
-// x in fixed point: 8 lanes per block of 32, limb plane l of token t at xl[(3 t + l) d].
+// Four values of a block of 32 by each of 8 lanes: their limbs as a word per plane, and the
+// block's scale.
+template <int NL>
+__device__ __forceinline__ void block_to_fixed(const float (&v)[4], uint32_t (&w)[3], float& scale)
+{
+    uint32_t u = umax(umax(abs_bits(v[0]), abs_bits(v[1])), umax(abs_bits(v[2]), abs_bits(v[3])));
+    u = umax(u, dpp0<0xB1>(u));                           // quad_perm: lane ^ 1
+    u = umax(u, dpp0<0x4E>(u));                           // quad_perm: lane ^ 2
+    u = umax(u, dpp0<0x141>(u));                          // row_half_mirror: the other quad of the 8
+    const int e = fix_exp<NL>(u);
+    w[0] = w[1] = w[2] = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        int l[3];
+        limbs<NL>(u >= 0x7f800000u ? 0 : fix_code<NL>(v[i], e), l);
+#pragma unroll
+        for (int j = 0; j < NL; ++j) w[j] |= (uint32_t)(l[j] & 0xff) << (8 * i);
+    }
+    scale = fix_scale<NL>(u, e);
+}
+
+// x in fixed point: 8 lanes per block of 32, limb plane l of token t at xl[(NL t + l) d].
 template <int kT>
 __device__ __forceinline__ void x_to_fixed(const RouteArgs& a, int64_t first)
 {
+    constexpr int NL = limbs_of(kT);
     const int nb = a.d / 32;
     const int64_t blk = first + (threadIdx.x >> 3);
     if (blk >= (int64_t)a.T * nb) return;                 // uniform over the 8-lane group
     const int sub = threadIdx.x & 7;
-    const int t = (int)(blk / nb), b = (int)(blk - (int64_t)t * nb);
-    float v[4];
+    const int t = (int)((uint32_t)blk / (uint32_t)nb), b = (int)blk - t * nb;
+    float v[4], scale;
+    uint32_t w[3];
     load_n<kT, 4>(static_cast<const uint8_t*>(a.x) +
                   ((int64_t)t * a.x_stride + b * 32 + sub * 4) * dtype_bytes(kT), v);
-    uint32_t u = umax(umax(abs_bits(v[0]), abs_bits(v[1])), umax(abs_bits(v[2]), abs_bits(v[3])));
+    block_to_fixed<NL>(v, w, scale);
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) u = umax(u, (uint32_t)__shfl_xor((int)u, o));
-    const int e = fix_exp(u);
-    uint32_t w[3] = {0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        int l[3];
-        limbs(u >= 0x7f800000u ? 0 : fix_code(v[i], e), l[0], l[1], l[2]);
-#pragma unroll
-        for (int j = 0; j < 3; ++j) w[j] |= (uint32_t)(l[j] & 0xff) << (8 * i);
-    }
-#pragma unroll
-    for (int j = 0; j < 3; ++j)
-        *reinterpret_cast<uint32_t*>(a.xl + ((int64_t)t * 3 + j) * a.d + b * 32 + sub * 4) = w[j];
-    if (sub == 0) a.xs[(int64_t)t * nb + b] = fix_scale(u, e);
+    for (int j = 0; j < NL; ++j)
+        *reinterpret_cast<uint32_t*>(a.xl + ((int64_t)t * NL + j) * a.d + b * 32 + sub * 4) = w[j];
+    if (sub == 0) a.xs[(int64_t)t * nb + b] = scale;
 }
 
 template <int kT>
@@ -252,23 +322,6 @@ __global__ __launch_bounds__(kRouteThreads) void k_decode_route(RouteArgs a)
 }
 
 // ---------------------------------------------------------- expert products ---
-struct ProductArgs {
-    const int32_t* nchunks;
-    const DecodeChunk* chunks;
-    const uint8_t* blob;
-    uint64_t expert_stride, q_off, s_off;
-    const int8_t* al;         // fixed-point activations: limb plane l of row r at al[(3 r + l) K]
-    const float* as;          // their block scales [rows][K / 32]
-    int K, E;
-    int pair_div;             // row of a pair: pair / pair_div (gate/up: top_k, down: 1)
-    int max_rows;             // rows of al (bounds the pair list)
-    int8_t* hl;               // gate/up: h in fixed point
-    float* hs;
-    int f;
-    float* dm;                // down: [pairs][d]
-    int d;
-};
-
 // Eight codes of a word as bytes holding 16 x the weight (see moe_kernels.hip's grouped
 // GEMM: the code with its top bit flipped is the weight in 4-bit two's complement).
 __device__ __forceinline__ v4i unpack16x(uint32_t w0, uint32_t w1)
@@ -281,115 +334,472 @@ __device__ __forceinline__ v4i unpack16x(uint32_t w0, uint32_t w1)
     return b;
 }
 
-constexpr int kProdWaves = 4;
-constexpr int kMaxBlocks = 16384 / 32;
-
-// One chunk of one expert times one 32-column tile of its matrix (gate/up: the gate tile
-// and the up tile of the same columns).  The waves of a workgroup split K and add up
-// through LDS in wave order.  Row 4 m + l of the instruction's 32 rows holds limb l of
-// token m, so that a lane gets the three limb sums of a (token, column) in one quad of
-// its result registers: token m is register quad m / 2 of lane half m % 2.
-template <bool kGateUp>
-__global__ __launch_bounds__(64 * kProdWaves) void k_decode_product(ProductArgs g)
+// Where one wave reads the weights: this lane's words of tile 0, tile t further by *_step.
+struct WeightAt {
+    const uint8_t* q;
+    const uint8_t* s;
+    int64_t q_step, s_step;
+};
+__device__ __forceinline__ WeightAt weights_at(const uint8_t* expert, uint64_t q_off, uint64_t s_off, int tile, int K)
 {
-    constexpr int NT = kGateUp ? 2 : 1;
-    __shared__ float s_scale[kChunkRows * kMaxBlocks];
-    __shared__ float s_red[kProdWaves][NT][kChunkRows][32];
-    if ((int)blockIdx.y >= *g.nchunks) return;            // uniform
-    const DecodeChunk& ch = g.chunks[blockIdx.y];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, j32 = lane & 31;
-    const int nb = g.K / 32, npairs = k_pairs(g.K), ngroups = scale_groups(g.K);
-    int n = ch.n, e = ch.expert;
-    n = n < 1 ? 1 : (n > kChunkRows ? kChunkRows : n);
-    e = e < 0 ? 0 : (e >= g.E ? g.E - 1 : e);
-    auto row_of = [&](int m) {
-        int r = ch.pair[m] / g.pair_div;
-        return r < 0 ? 0 : (r >= g.max_rows ? g.max_rows - 1 : r);
-    };
-    for (int i = tid; i < n * nb; i += 64 * kProdWaves) {
-        const int m = i / nb;
-        s_scale[i] = g.as[(int64_t)row_of(m) * nb + (i - m * nb)];
-    }
-    const int m_a = j32 >> 2, l_a = j32 & 3;              // the A row this lane feeds
-    const bool a_on = m_a < n && l_a < 3;
-    const int8_t* al = g.al + ((int64_t)row_of(a_on ? m_a : 0) * 3 + (a_on ? l_a : 0)) * g.K + 16 * h;
-    const uint8_t* ex = g.blob + (uint64_t)e * g.expert_stride;
-    const int nt0 = (int)blockIdx.x * NT;
-    const uint8_t* wq = ex + g.q_off + (uint64_t)nt0 * npairs * 1024 + lane * 16;
-    const uint8_t* wsc = ex + g.s_off + ((uint64_t)nt0 * ngroups * 32 + j32) * 16;
-    __syncthreads();
+    const int lane = threadIdx.x & 63, npairs = k_pairs(K), ngroups = scale_groups(K);
+    return {expert + q_off + (uint64_t)tile * npairs * 1024 + lane * 16,
+            expert + s_off + ((uint64_t)tile * ngroups * 32 + (lane & 31)) * 16, (int64_t)npairs * 1024,
+            (int64_t)ngroups * 512};
+}
 
-    float acc[NT][4] = {};
-    const v16i zero = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-    const int ng = (n + 1) >> 1;
-    const int p0 = wave * npairs / kProdWaves, p1 = (wave + 1) * npairs / kProdWaves;
-#pragma unroll 2
-    for (int pr = p0; pr < p1; ++pr) {
-        uint4 bq[NT];
-        uint32_t bs[NT];
+// The weights of U K pairs of NT 32-column tiles in registers, all in flight at first; a pair's
+// registers take the pair U further as soon as it is used, so that U * NT KiB a wave stay in
+// flight.
+template <int NT, int U>
+struct Ring {
+    uint4 q[U][NT];
+    uint32_t s[U][NT];        // the scales of the pair's two blocks for this lane's column
+
+    __device__ __forceinline__ void load(int u, const WeightAt& w, int pr)
+    {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            bq[t] = *reinterpret_cast<const uint4*>(wq + ((uint64_t)t * npairs + pr) * 1024);
-            bs[t] = *reinterpret_cast<const uint32_t*>(wsc + ((uint64_t)t * ngroups + (pr >> 2)) * 512 + (pr & 3) * 4);
-        }
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int b = 2 * pr + q;
-            if (b >= nb) break;                           // uniform: the padded block of an odd count
-            v4i a = {0, 0, 0, 0};
-            if (a_on) a = *reinterpret_cast<const v4i*>(al + b * 32);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const v4i w = q ? unpack16x(bq[t].z, bq[t].w) : unpack16x(bq[t].x, bq[t].y);
-                const uint16_t hb = (uint16_t)(q ? bs[t] >> 16 : bs[t] & 0xffffu);
-                const float ws = (float)__builtin_bit_cast(_Float16, hb) * 0.0625f;
-                const v16i s = __builtin_amdgcn_mfma_i32_32x32x32_i8(a, w, zero, 0, 0, 0);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (c < ng) {                         // uniform
-                        // 16 x the limb sums; s0 + 256 s1 is a multiple of 16 below 2^28: exact in fp32
-                        const float lo = (float)(s[4 * c] + (s[4 * c + 1] << 8));
-                        const float v = __builtin_fmaf((float)s[4 * c + 2], 65536.0f, lo);
-                        const int m = 2 * c + h < n ? 2 * c + h : n - 1;
-                        acc[t][c] = __builtin_fmaf(v, ws * s_scale[m * nb + b], acc[t][c]);
-                    }
-                }
-            }
+            q[u][t] = *reinterpret_cast<const uint4*>(w.q + t * w.q_step + (int64_t)pr * 1024);
+            s[u][t] = *reinterpret_cast<const uint32_t*>(w.s + t * w.s_step + (pr >> 2) * 512 + (pr & 3) * 4);
         }
     }
+    __device__ __forceinline__ void fill(const WeightAt& w, int p0, int p1)
+    {
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+        for (int u = 0; u < U; ++u)
+            if (p0 + u < p1) load(u, w, p0 + u);          // uniform
+    }
+};
+
+// acc[t][kPerQuad c + i] += block b's products for token i of quad c (NQ quads): q = 0 / 1, the
+// first / second block of ring slot u.
+//   a             the 16 bytes of the block that this lane feeds
+//   scl(c, i, b)  the scale of that token's block
+template <int NL, int NT, int NQ, int U, class Scl>
+__device__ __forceinline__ void block_product(float (&acc)[NT][8], const Ring<NT, U>& r, int u, int q, v4i a, int b, Scl scl)
+{
+    constexpr int kPer = Limbs<NL>::kPerQuad;
+    const v16i zero = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+    v16i s[NT];
+    float ws[NT];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s_red[wave][t][2 * c + h][j32] = acc[t][c];
+    for (int t = 0; t < NT; ++t) {
+        const v4i w = q ? unpack16x(r.q[u][t].z, r.q[u][t].w) : unpack16x(r.q[u][t].x, r.q[u][t].y);
+        s[t] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a, w, zero, 0, 0, 0);
+        const uint16_t hb = (uint16_t)(q ? r.s[u][t] >> 16 : r.s[u][t] & 0xffffu);
+        ws[t] = (float)__builtin_bit_cast(_Float16, hb) * 0.0625f;
+    }
+#pragma unroll
+    for (int c = 0; c < NQ; ++c)
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const float x = scl(c, i, b);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                // 16 x the limb sums; s0 + 256 s1 is a multiple of 16 below 2^28: exact in fp32
+                const int k = 4 * c + (NL == 2 ? 2 * i : 0);
+                float v = (float)(s[t][k] + (s[t][k + 1] << 8));
+                if (NL == 3) v = __builtin_fmaf((float)s[t][k + 2], 65536.0f, v);
+                acc[t][kPer * c + i] = __builtin_fmaf(v, ws[t] * x, acc[t][kPer * c + i]);
+            }
+        }
+    __builtin_amdgcn_sched_barrier(0);                    // one block's sums at a time in registers
+}
+
+// K pairs [p0, p1) of a filled ring.  act(b): the bytes of block b that this lane feeds, read one
+// pair ahead of their use.
+template <int NL, int NT, int NQ, int U, class Act, class Scl>
+__device__ __forceinline__ void ring_product(float (&acc)[NT][8], Ring<NT, U>& r, const WeightAt& w, int p0, int p1, int nb,
+                                             Act act, Scl scl)
+{
+    // the padded block of an odd count is left out; its place here repeats the one before
+    auto second = [&](int pr) { return 2 * pr + 1 < nb ? 2 * pr + 1 : 2 * pr; };
+    v4i a0 = act(2 * p0), a1 = act(second(p0));
+    for (int pb = p0; pb < p1; pb += U) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int pr = pb + u;
+            if (pr >= p1) break;                          // uniform
+            const int ahead = pr + 1 < p1 ? pr + 1 : pr;
+            const v4i n0 = act(2 * ahead), n1 = act(second(ahead));
+            block_product<NL, NT, NQ>(acc, r, u, 0, a0, 2 * pr, scl);
+            if (2 * pr + 1 < nb) block_product<NL, NT, NQ>(acc, r, u, 1, a1, 2 * pr + 1, scl);
+            if (pr + U < p1) r.load(u, w, pr + U);
+            a0 = n0;
+            a1 = n1;
+        }
+    }
+}
+
+constexpr int kMaxBlocks = 16384 / 32;
+
+struct GateUpArgs {
+    RouteArgs r;              // routing and x
+    const int32_t* nchunks;
+    const DecodeChunk* chunks;
+    const uint8_t* blob;
+    uint64_t expert_stride, q_off, s_off;
+    int8_t* hl;               // h in fixed point: limb plane l of pair p at hl[(NL p + l) f]
+    float* hs;                // its block scales [pairs][f / 32]
+    int f;
+};
+
+// h = silu(gate) * up of pair p, 32 columns by a 32-lane half, in fixed point.
+template <int NL>
+__device__ __forceinline__ void store_h(const GateUpArgs& g, int p, int fb, float gate, float up)
+{
+    const int j32 = threadIdx.x & 31;
+    const float hv = gate / (1.0f + exp_cw(-gate)) * up;
+    uint32_t u = abs_bits(hv);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) u = umax(u, (uint32_t)__shfl_xor((int)u, o));
+    const int e = fix_exp<NL>(u);
+    int l[3];
+    limbs<NL>(u >= 0x7f800000u ? 0 : fix_code<NL>(hv, e), l);
+    int8_t* o = g.hl + (int64_t)p * NL * g.f + fb * 32 + j32;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) o[i * g.f] = (int8_t)l[i];
+    if (j32 == 0) g.hs[(int64_t)p * (g.f / 32) + fb] = fix_scale<NL>(u, e);
+}
+
+// ------------------------------------------------------- few pairs: gate/up ---
+// Workgroup (f-block, pair) finds its pair's expert itself -- every wave routes the token, in
+// registers -- and turns the token's x into fixed point in LDS, so that no launch comes before
+// it.  Pairs of the same expert each read its weights (from a cache).  The workgroups of
+// f-block 0 and slot 0 leave the token's routing for the next kernel.
+constexpr int kPairWaves = 8;
+
+template <int kT>
+__global__ __launch_bounds__(64 * kPairWaves) void k_decode_pair_gate_up(GateUpArgs g)
+{
+    constexpr int NL = limbs_of(kT);
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];   // xl [NL][d], then xs [d / 32]
+    __shared__ float s_red[kPairWaves][2][32];
+    __shared__ int s_eidx[kMaxE];
+    __shared__ float s_z[kMaxE];
+    const RouteArgs& r = g.r;
+    const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, j32 = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int p = blockIdx.y, t = p / r.k, j = p - t * r.k, fb = blockIdx.x;
+    const int d = r.d, nb = d / 32, npairs = k_pairs(d);
+    int8_t* xl = reinterpret_cast<int8_t*>(lds);
+    float* xs = reinterpret_cast<float*>(lds + NL * d);
+    const bool record = fb == 0 && j == 0;                // uniform
+    const float* lt = r.logits + (int64_t)t * r.logits_stride;
+
+    int e = -1;
+    auto slot = [&](int jj, int ee, uint32_t key) {
+        if (jj == j) e = ee;
+        if (record && wave == 0 && lane == 0) {
+            s_eidx[jj] = ee;
+            s_z[jj] = key_logit(key);
+        }
+    };
+    const int slots = record && wave == 0 ? r.k : j + 1;
+    if (r.E <= 128)
+        route_token<2>(lt, r.E, slots, slot);
+    else if (r.E <= 256)
+        route_token<4>(lt, r.E, slots, slot);
+    else
+        route_token<16>(lt, r.E, slots, slot);
+    e = __builtin_amdgcn_readfirstlane(e);
+    const int p0 = wave * npairs / kPairWaves, p1 = (wave + 1) * npairs / kPairWaves;
+    const WeightAt w = weights_at(g.blob + (uint64_t)(e < 0 ? 0 : e) * g.expert_stride, g.q_off, g.s_off, 2 * fb, d);
+    Ring<2, 4> ring;
+    if (e >= 0) ring.fill(w, p0, p1);                     // in flight while x is turned
+    if (record && wave == 0) {
+        route_weights(r.k, s_eidx, s_z);
+        for (int i = lane; i < r.k; i += 64) {
+            r.eidx[p + i] = s_eidx[i];
+            r.wts[p + i] = s_z[i];
+            if (r.eidx_out) r.eidx_out[p + i] = s_eidx[i];
+            if (r.wts_out) r.wts_out[p + i] = s_z[i];
+        }
+    }
+    if (e < 0) return;                                    // the same on every wave
+
+    for (int blk = tid >> 3; blk < nb; blk += 64 * kPairWaves / 8) {
+        const int sub = tid & 7;
+        float v[4], scale;
+        uint32_t x[3];
+        load_n<kT, 4>(static_cast<const uint8_t*>(r.x) +
+                      ((int64_t)t * r.x_stride + blk * 32 + sub * 4) * dtype_bytes(kT), v);
+        block_to_fixed<NL>(v, x, scale);
+#pragma unroll
+        for (int l = 0; l < NL; ++l) *reinterpret_cast<uint32_t*>(xl + l * d + blk * 32 + sub * 4) = x[l];
+        if (sub == 0) xs[blk] = scale;
+    }
     __syncthreads();
-    const int m = tid >> 5, col = (int)blockIdx.x * 32 + j32;
-    static_assert(64 * kProdWaves == 32 * kChunkRows, "one thread per (row, column)");
-    if (m >= n) return;                                   // uniform over the 32-lane half
-    float z[NT] = {};
+
+    auto act = [&](int b) -> v4i {
+        v4i a = {0, 0, 0, 0};
+        if (j32 < NL) a = *reinterpret_cast<const v4i*>(xl + j32 * d + b * 32 + 16 * h);
+        return a;
+    };
+    float acc[2][8] = {};
+    if (p0 < p1) ring_product<NL, 2, 1>(acc, ring, w, p0, p1, nb, act, [&](int, int, int b) { return xs[b]; });
+    if (h == 0) {
+        s_red[wave][0][j32] = acc[0][0];
+        s_red[wave][1][j32] = acc[1][0];
+    }
+    __syncthreads();
+    if (tid >= 32) return;
+    float z[2] = {};
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int v = 0; v < kPairWaves; ++v) {
+        z[0] += s_red[v][0][j32];
+        z[1] += s_red[v][1][j32];
+    }
+    store_h<NL>(g, p, fb, z[0], z[1]);
+}
+
+// ----------------------------------------------------- chunks: gate/up, down ---
+// Rows (token, slot pairs) that share an expert's weights: a chunk of the route kernel's list,
+// or a pair by itself.
+struct Rows {
+    int e, n;                 // expert (-1: not available), pairs
+    const int32_t* list;      // null: the pair `own`
+    int own;
+    __device__ __forceinline__ int pair(int m) const { return list ? list[m] : own; }
+};
+
+// f(quads) with the quads that n tokens need as a compile-time number
+template <int NL, class F>
+__device__ __forceinline__ void for_quads(int n, F f)
+{
+    constexpr int kPer = 2 * Limbs<NL>::kPerQuad;         // tokens of a quad of both lane halves
+    if (n <= kPer)
+        f(std::integral_constant<int, 1>{});
+    else if (n <= 2 * kPer)
+        f(std::integral_constant<int, 2>{});
+    else if (n <= 3 * kPer)
+        f(std::integral_constant<int, 3>{});
+    else
+        f(std::integral_constant<int, 4>{});
+}
+
+// Each (chunk, f-block) is an item; a fixed number of workgroups go through the items, since
+// only the device knows how many there are.  The waves split K.
+constexpr int kChunkWaves = 4;
+
+template <int NL>
+__global__ __launch_bounds__(64 * kChunkWaves) __attribute__((amdgpu_waves_per_eu(3))) void k_decode_chunk_gate_up(GateUpArgs g)
+{
+    using Lb = Limbs<NL>;
+    extern __shared__ float s_scale[];                    // [kTokens][d / 32]
+    __shared__ float s_red[kChunkWaves][2][Lb::kTokens][32];
+    const RouteArgs& r = g.r;
+    const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, j32 = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int d = r.d, nb = d / 32, npairs = k_pairs(d), nfb = g.f / 32;
+    const int items = *g.nchunks * nfb;
+    const int m_a = j32 / Lb::kRowStep, l_a = j32 % Lb::kRowStep;   // the A row this lane feeds
+    const int p0 = wave * npairs / kChunkWaves, p1 = (wave + 1) * npairs / kChunkWaves;
+    for (int it = blockIdx.x; it < items; it += gridDim.x) {
+        const int ci = it / nfb, fb = it - ci * nfb;
+        const DecodeChunk& ch = g.chunks[ci];
+        const int n = ch.n, e = ch.expert;
+        const WeightAt w = weights_at(g.blob + (uint64_t)e * g.expert_stride, g.q_off, g.s_off, 2 * fb, d);
+        Ring<2, 2> ring;
+        ring.fill(w, p0, p1);                             // in flight while the scales are staged
+        __syncthreads();                                  // the previous item's LDS is read
+        for (int i = tid; i < n * nb; i += 64 * kChunkWaves) {
+            const int m = i / nb;
+            s_scale[i] = r.xs[(int64_t)(ch.pair[m] / r.k) * nb + (i - m * nb)];
+        }
+        const bool on = m_a < n && l_a < NL;
+        const int8_t* al = r.xl + ((int64_t)(ch.pair[on ? m_a : 0] / r.k) * NL + (on ? l_a : 0)) * d + 16 * h;
+        auto act = [&](int b) -> v4i {
+            v4i a = {0, 0, 0, 0};
+            if (on) a = *reinterpret_cast<const v4i*>(al + b * 32);
+            return a;
+        };
+        __syncthreads();
+        float acc[2][8] = {};
+        // an absent token's column is not stored: whatever its place in the array holds will do
+        const float* xs = s_scale + Lb::token(0, 0, h) * nb;
+        auto scl = [&](int c, int i, int b) { return xs[(2 * Lb::kPerQuad * c + i) * nb + b]; };
+        if (p0 < p1)
+            for_quads<NL>(n, [&](auto nq) { ring_product<NL, 2, decltype(nq)::value>(acc, ring, w, p0, p1, nb, act, scl); });
 #pragma unroll
-        for (int w = 0; w < kProdWaves; ++w) z[t] += s_red[w][t][m][j32];
-    int p = ch.pair[m];
-    if (kGateUp) {
-        const float hv = z[0] / (1.0f + exp_cw(-z[0])) * z[NT - 1];
-        uint32_t u = abs_bits(hv);
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) u = umax(u, (uint32_t)__shfl_xor((int)u, o));
-        const int ex2 = fix_exp(u);
-        int l0, l1, l2;
-        limbs(u >= 0x7f800000u ? 0 : fix_code(hv, ex2), l0, l1, l2);
-        int8_t* o = g.hl + (int64_t)p * 3 * g.f + col;
-        o[0] = (int8_t)l0;
-        o[g.f] = (int8_t)l1;
-        o[2 * g.f] = (int8_t)l2;
-        if (j32 == 0) g.hs[(int64_t)p * (g.f / 32) + blockIdx.x] = fix_scale(u, ex2);
-    } else {
-        g.dm[(int64_t)p * g.d + col] = z[0];
+            for (int i = 0; i < Lb::kPerQuad; ++i) {
+                s_red[wave][0][Lb::token(c, i, h)][j32] = acc[0][Lb::kPerQuad * c + i];
+                s_red[wave][1][Lb::token(c, i, h)][j32] = acc[1][Lb::kPerQuad * c + i];
+            }
+        __syncthreads();
+        for (int m = tid >> 5; m < n; m += 2 * kChunkWaves) {   // uniform over the 32-lane half
+            float z[2] = {};
+#pragma unroll
+            for (int v = 0; v < kChunkWaves; ++v) {
+                z[0] += s_red[v][0][m][j32];
+                z[1] += s_red[v][1][m][j32];
+            }
+            store_h<NL>(g, ch.pair[m], fb, z[0], z[1]);
+        }
+    }
+}
+
+struct DownArgs {
+    const int32_t* nchunks;   // null: pair p is the chunk of itself
+    const DecodeChunk* chunks;
+    const int32_t* eidx;
+    const float* wts;
+    const uint8_t* blob;
+    uint64_t expert_stride, q_off, s_off;
+    const int8_t* hl;
+    const float* hs;
+    int T, k, d, f, ksplit;
+    float* dm;                // [pairs][d]; not written for a pair without an expert
+    void* y;
+    int64_t y_stride;
+};
+
+// Each wave takes (chunk, two 32-column tiles) units by itself: all of K, no barrier.
+constexpr int kDownWaves = 4;
+constexpr int kDownSeg = 32;  // K pairs whose scales a wave holds in LDS at a time
+
+template <int NL>
+__global__ __launch_bounds__(64 * kDownWaves) __attribute__((amdgpu_waves_per_eu(3))) void k_decode_chunk_down(DownArgs g)
+{
+    using Lb = Limbs<NL>;
+    __shared__ float s_scales[kDownWaves][Lb::kTokens][2 * kDownSeg];
+    const int lane = threadIdx.x & 63, h = lane >> 5, j32 = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int R = g.T * g.k, nb = g.f / 32, npairs = k_pairs(g.f), tiles = g.d / 32, tile2 = (tiles + 1) / 2;
+    const int units = (g.nchunks ? *g.nchunks : R) * tile2;
+    const int m_a = j32 / Lb::kRowStep, l_a = j32 % Lb::kRowStep;
+    float(&scales)[Lb::kTokens][2 * kDownSeg] = s_scales[wave];
+    for (int u = blockIdx.x * kDownWaves + wave; u < units; u += gridDim.x * kDownWaves) {
+        const int ci = u / tile2, nt = 2 * (u - ci * tile2);
+        const Rows rw = g.nchunks ? Rows{g.chunks[ci].expert, g.chunks[ci].n, g.chunks[ci].pair, 0}
+                                  : Rows{g.eidx[ci], 1, nullptr, ci};
+        if (rw.e < 0) continue;
+        const int n = rw.n;
+        // an odd tile count: the last unit's second tile is its first again, not stored
+        WeightAt w = weights_at(g.blob + (uint64_t)rw.e * g.expert_stride, g.q_off, g.s_off, nt, g.f);
+        const bool two = nt + 1 < tiles;
+        if (!two) w.q_step = w.s_step = 0;
+        const bool on = m_a < n && l_a < NL;
+        const int8_t* al = g.hl + ((int64_t)rw.pair(on ? m_a : 0) * NL + (on ? l_a : 0)) * g.f + 16 * h;
+        auto act = [&](int b) -> v4i {
+            v4i a = {0, 0, 0, 0};
+            if (on) a = *reinterpret_cast<const v4i*>(al + b * 32);
+            return a;
+        };
+        float acc[2][8] = {};
+        for (int s0 = 0; s0 < npairs; s0 += kDownSeg) {
+            const int s1 = s0 + kDownSeg < npairs ? s0 + kDownSeg : npairs;
+            Ring<2, 2> ring;
+            ring.fill(w, s0, s1);
+            __builtin_amdgcn_wave_barrier();
+            for (int m = 0; m < n; ++m) {
+                const int b = 2 * s0 + lane;              // 2 kDownSeg = 64 blocks
+                if (b < nb) scales[m][lane] = g.hs[(int64_t)rw.pair(m) * nb + b];
+            }
+            __builtin_amdgcn_wave_barrier();
+            const float* xs = &scales[Lb::token(0, 0, h)][0] - 2 * s0;   // as above for absent tokens
+            auto scl = [&](int c, int i, int b) { return xs[(2 * Lb::kPerQuad * c + i) * 2 * kDownSeg + b]; };
+            for_quads<NL>(n, [&](auto nq) { ring_product<NL, 2, decltype(nq)::value>(acc, ring, w, s0, s1, nb, act, scl); });
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < Lb::kPerQuad; ++i) {
+                const int m = Lb::token(c, i, h);
+                if (m >= n) continue;
+                float* o = g.dm + (int64_t)rw.pair(m) * g.d + nt * 32 + j32;
+                o[0] = acc[0][Lb::kPerQuad * c + i];
+                if (two) o[32] = acc[1][Lb::kPerQuad * c + i];
+            }
+    }
+}
+
+// ------------------------------------------- few pairs: down and combine in one ---
+// A workgroup owns 32 columns of y for all tokens.  Its 16 waves take the (pair, K split) units
+// in turn, the pairs' h in LDS, and leave the units' rows there, where each token's slots are
+// added up in slot order.
+constexpr int kPairDownWaves = 16;
+
+struct PairDownLds {
+    int hl, hs, dm, bytes;
+    MOE_HD PairDownLds(int R, int f, int NL, int ksplit)
+    {
+        hl = 0;
+        hs = R * NL * f;
+        dm = hs + R * (f / 32) * 4;
+        bytes = dm + R * ksplit * 32 * 4;
+    }
+};
+
+template <int kT>
+__global__ __launch_bounds__(64 * kPairDownWaves) void k_decode_pair_down(DownArgs g)
+{
+    constexpr int NL = limbs_of(kT);
+    constexpr int kMost = 64;                             // pairs, at most
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    __shared__ float s_w[kMost];
+    const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, j32 = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int R = g.T * g.k, nb = g.f / 32, npairs = k_pairs(g.f), nt = blockIdx.x;
+    const PairDownLds L(R, g.f, NL, g.ksplit);
+    int8_t* s_hl = reinterpret_cast<int8_t*>(lds);
+    float* s_hs = reinterpret_cast<float*>(lds + L.hs);
+    float* s_dm = reinterpret_cast<float*>(lds + L.dm);   // [ksplit][pairs][32]
+
+    const int units = R * g.ksplit;
+    Ring<1, 6> ring;
+    WeightAt w{};
+    int e = -1, p0 = 0, p1 = 0;
+    auto open = [&](int u) {                              // unit u's weights on their way
+        const int p = u / g.ksplit, ks = u - p * g.ksplit;
+        e = g.eidx[p];
+        p0 = ks * npairs / g.ksplit;
+        p1 = (ks + 1) * npairs / g.ksplit;
+        w = weights_at(g.blob + (uint64_t)(e < 0 ? 0 : e) * g.expert_stride, g.q_off, g.s_off, nt, g.f);
+        if (e >= 0) ring.fill(w, p0, p1);
+    };
+    if (wave < units) open(wave);
+    if (tid < R) s_w[tid] = g.wts[tid];
+    for (int i = tid * 16; i < L.hs; i += 64 * kPairDownWaves * 16)   // R NL f: a multiple of 32
+        *reinterpret_cast<uint4*>(s_hl + i) = *reinterpret_cast<const uint4*>(g.hl + i);
+    for (int i = tid; i < R * nb; i += 64 * kPairDownWaves) s_hs[i] = g.hs[i];
+    __syncthreads();
+    for (int u = wave; u < units; u += kPairDownWaves) {
+        if (u != wave) open(u);
+        const int p = u / g.ksplit, ks = u - p * g.ksplit;
+        float acc[1][8] = {};
+        if (e >= 0) {
+            const int8_t* al = s_hl + (p * NL + j32) * g.f + 16 * h;
+            auto act = [&](int b) -> v4i {
+                v4i a = {0, 0, 0, 0};
+                if (j32 < NL) a = *reinterpret_cast<const v4i*>(al + b * 32);
+                return a;
+            };
+            ring_product<NL, 1, 1>(acc, ring, w, p0, p1, nb, act, [&](int, int, int b) { return s_hs[p * nb + b]; });
+        }
+        if (h == 0) s_dm[(ks * R + p) * 32 + j32] = acc[0][0];
+    }
+    __syncthreads();
+    typedef typename Elem<kT>::type E;
+    for (int i = tid; i < g.T * 32; i += 64 * kPairDownWaves) {
+        const int t = i >> 5, col = i & 31;
+        float a = 0.0f;
+        for (int j = 0; j < g.k; ++j) {
+            const int p = t * g.k + j;
+            float v = 0.0f;                               // 0 with weight 0 where there is no expert
+            for (int ks = 0; ks < g.ksplit; ++ks) v += s_dm[(ks * R + p) * 32 + col];
+            a = __builtin_fmaf(s_w[p], v, a);
+        }
+        static_cast<E*>(g.y)[(int64_t)t * g.y_stride + nt * 32 + col] = from_f32<kT>(a);
     }
 }
 
 // ------------------------------------------------------------------ combine ---
+// y[t] = sum over j of w[t, j] dm[t, j].  Four slots' rows are loaded together; a slot without
+// an expert reads the row of slot 0 (present if any is) and adds nothing.
 template <int kT>
 __global__ __launch_bounds__(256) void k_decode_combine(const float* __restrict__ dm,
                                                         const float* __restrict__ wts,
@@ -397,19 +807,31 @@ __global__ __launch_bounds__(256) void k_decode_combine(const float* __restrict_
                                                         int d, void* __restrict__ y, int64_t y_stride)
 {
     const int d4 = d >> 2;
-    const int64_t gid = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (gid >= (int64_t)T * d4) return;
-    const int t = (int)(gid / d4), c = (int)(gid - (int64_t)t * d4) * 4;
+    const int t = blockIdx.y, c = ((int)blockIdx.x * 256 + (int)threadIdx.x) * 4;
+    if (c >= d4 * 4) return;
+    const int32_t* te = eidx + t * k;
+    const float* tw = wts + t * k;
     float acc[4] = {};
-    for (int j = 0; j < k; ++j) {
-        const int p = t * k + j;
-        if (eidx[p] < 0) continue;
-        const float w = wts[p];
-        const float4 v = *reinterpret_cast<const float4*>(dm + (int64_t)p * d + c);
-        acc[0] = __builtin_fmaf(w, v.x, acc[0]);
-        acc[1] = __builtin_fmaf(w, v.y, acc[1]);
-        acc[2] = __builtin_fmaf(w, v.z, acc[2]);
-        acc[3] = __builtin_fmaf(w, v.w, acc[3]);
+    if (te[0] >= 0) {                                     // available experts come first
+        for (int j0 = 0; j0 < k; j0 += 4) {
+            float4 v[4];
+            float w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = j0 + i < k ? j0 + i : k - 1;
+                const bool live = j0 + i < k && te[j] >= 0;
+                w[i] = live ? tw[j] : 0.0f;
+                v[i] = *reinterpret_cast<const float4*>(dm + (int64_t)(t * k + (live ? j : 0)) * d + c);
+                if (!live) v[i] = float4{0.0f, 0.0f, 0.0f, 0.0f};
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                acc[0] = __builtin_fmaf(w[i], v[i].x, acc[0]);
+                acc[1] = __builtin_fmaf(w[i], v[i].y, acc[1]);
+                acc[2] = __builtin_fmaf(w[i], v[i].z, acc[2]);
+                acc[3] = __builtin_fmaf(w[i], v[i].w, acc[3]);
+            }
+        }
     }
     store_n<kT, 4>(static_cast<uint8_t*>(y) + ((int64_t)t * y_stride + c) * dtype_bytes(kT), acc);
 }
@@ -419,7 +841,36 @@ unsigned nblk(int64_t n, int per) { return (unsigned)((n + per - 1) / per); }
 }  // namespace
 
 // ----------------------------------------------------------------- launches ---
-hipError_t launch_decode_route(const DecodeLaunch& D, hipStream_t st)
+namespace {
+
+// Tokens from which the route kernel pays: below it every pair's workgroups route for
+// themselves and pairs that share an expert read its weights again.
+constexpr int kPairTokens = 6;
+// Column tiles from which one workgroup a tile fills enough of the chip, and the pairs up to
+// which it does so faster than a wave for every (pair, two tiles) and a combine.
+constexpr int kPairDownTiles = 64;
+constexpr int kPairDownPairs = 16;
+constexpr int kPairDownLds = 96 << 10;
+
+bool by_pairs(const DecodeLaunch& D) { return D.T <= kPairTokens && !D.need_counts; }
+
+// K splits that give every wave of the fused down kernel a unit
+int down_ksplit(const DecodeLaunch& D)
+{
+    const int R = D.T * D.k, np = k_pairs(D.f);
+    int ks = 1;
+    while (R * ks < kPairDownWaves && 2 * ks <= np && ks < 8) ks *= 2;
+    return ks;
+}
+
+bool down_fused(const DecodeLaunch& D)
+{
+    const int R = D.T * D.k;
+    return by_pairs(D) && D.d / 32 >= kPairDownTiles && R <= kPairDownPairs &&
+           PairDownLds(R, D.f, limbs_of(D.dtype), down_ksplit(D)).bytes <= kPairDownLds;
+}
+
+RouteArgs route_args(const DecodeLaunch& D)
 {
     RouteArgs a;
     a.logits = D.logits;
@@ -427,12 +878,12 @@ hipError_t launch_decode_route(const DecodeLaunch& D, hipStream_t st)
     a.T = D.T;
     a.E = D.E;
     a.k = D.k;
+    a.chunk_rows = limbs_of(D.dtype) == 3 ? Limbs<3>::kTokens : Limbs<2>::kTokens;
     a.eidx = reinterpret_cast<int32_t*>(D.ws + D.L.eidx);
     a.wts = reinterpret_cast<float*>(D.ws + D.L.wts);
     a.counts = reinterpret_cast<int32_t*>(D.ws + D.L.counts);
     a.nchunks = reinterpret_cast<int32_t*>(D.ws + D.L.nchunks);
     a.chunks = reinterpret_cast<DecodeChunk*>(D.ws + D.L.chunks);
-    a.max_chunks = D.L.max_chunks;
     a.eidx_out = D.eidx_out;
     a.wts_out = D.wts_out;
     a.x = D.x;
@@ -440,61 +891,127 @@ hipError_t launch_decode_route(const DecodeLaunch& D, hipStream_t st)
     a.d = D.d;
     a.xl = reinterpret_cast<int8_t*>(D.ws + D.L.xl);
     a.xs = reinterpret_cast<float*>(D.ws + D.L.xs);
-    const dim3 grid(1 + nblk((int64_t)D.T * (D.d / 32), kRouteThreads / 8)), block(kRouteThreads);
-    if (D.dtype == kF32)
-        hipLaunchKernelGGL(k_decode_route<kF32>, grid, block, 0, st, a);
-    else if (D.dtype == kBF16)
-        hipLaunchKernelGGL(k_decode_route<kBF16>, grid, block, 0, st, a);
-    else
-        hipLaunchKernelGGL(k_decode_route<kF16>, grid, block, 0, st, a);
-    return hipGetLastError();
+    return a;
 }
 
-hipError_t launch_decode_products(const DecodeLaunch& D, hipStream_t st)
+GateUpArgs gate_up_args(const DecodeLaunch& D)
 {
-    ProductArgs g;
-    g.nchunks = reinterpret_cast<const int32_t*>(D.ws + D.L.nchunks);
-    g.chunks = reinterpret_cast<const DecodeChunk*>(D.ws + D.L.chunks);
+    GateUpArgs g;
+    g.r = route_args(D);
+    g.nchunks = g.r.nchunks;
+    g.chunks = g.r.chunks;
     g.blob = D.blob;
     g.expert_stride = D.expert_stride;
     g.q_off = D.gu_q_off;
     g.s_off = D.gu_s_off;
-    g.al = reinterpret_cast<const int8_t*>(D.ws + D.L.xl);
-    g.as = reinterpret_cast<const float*>(D.ws + D.L.xs);
-    g.K = D.d;
-    g.E = D.E;
-    g.pair_div = D.k;
-    g.max_rows = D.T;
     g.hl = reinterpret_cast<int8_t*>(D.ws + D.L.hl);
     g.hs = reinterpret_cast<float*>(D.ws + D.L.hs);
     g.f = D.f;
-    g.dm = reinterpret_cast<float*>(D.ws + D.L.dm);
-    g.d = D.d;
-    hipLaunchKernelGGL(k_decode_product<true>, dim3(D.f / 32, D.L.max_chunks), dim3(64 * kProdWaves), 0, st, g);
+    return g;
+}
+
+DownArgs down_args(const DecodeLaunch& D)
+{
+    DownArgs g;
+    const bool pairs = by_pairs(D);
+    g.nchunks = pairs ? nullptr : reinterpret_cast<const int32_t*>(D.ws + D.L.nchunks);
+    g.chunks = reinterpret_cast<const DecodeChunk*>(D.ws + D.L.chunks);
+    g.eidx = reinterpret_cast<const int32_t*>(D.ws + D.L.eidx);
+    g.wts = reinterpret_cast<const float*>(D.ws + D.L.wts);
+    g.blob = D.blob;
+    g.expert_stride = D.expert_stride;
     g.q_off = D.d_q_off;
     g.s_off = D.d_s_off;
-    g.al = g.hl;
-    g.as = g.hs;
-    g.K = D.f;
-    g.pair_div = 1;
-    g.max_rows = D.T * D.k;
-    hipLaunchKernelGGL(k_decode_product<false>, dim3(D.d / 32, D.L.max_chunks), dim3(64 * kProdWaves), 0, st, g);
+    g.hl = reinterpret_cast<const int8_t*>(D.ws + D.L.hl);
+    g.hs = reinterpret_cast<const float*>(D.ws + D.L.hs);
+    g.T = D.T;
+    g.k = D.k;
+    g.d = D.d;
+    g.f = D.f;
+    g.ksplit = down_ksplit(D);
+    g.dm = reinterpret_cast<float*>(D.ws + D.L.dm);
+    g.y = D.y;
+    g.y_stride = D.y_stride;
+    return g;
+}
+
+template <int kT>
+hipError_t route_typed(const DecodeLaunch& D, hipStream_t st)
+{
+    if (by_pairs(D)) return hipSuccess;                   // the gate/up kernel routes
+    const dim3 grid(1 + nblk((int64_t)D.T * (D.d / 32), kRouteThreads / 8));
+    hipLaunchKernelGGL(k_decode_route<kT>, grid, dim3(kRouteThreads), 0, st, route_args(D));
     return hipGetLastError();
+}
+
+template <class K>
+hipError_t lds_limit(K kernel, int bytes)
+{
+    if (bytes <= 16 << 10) return hipSuccess;             // within the default limit next to the static arrays
+    return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <int kT>
+hipError_t products_typed(const DecodeLaunch& D, hipStream_t st)
+{
+    constexpr int NL = limbs_of(kT);
+    hipError_t e = hipSuccess;
+    if (by_pairs(D)) {
+        const int lds = NL * D.d + D.d / 32 * 4;
+        e = lds_limit(&k_decode_pair_gate_up<kT>, lds);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(k_decode_pair_gate_up<kT>, dim3(D.f / 32, D.T * D.k), dim3(64 * kPairWaves), lds, st, gate_up_args(D));
+    } else {
+        const int64_t items = (int64_t)D.L.max_chunks * (D.f / 32);
+        const int lds = Limbs<NL>::kTokens * (D.d / 32) * 4;
+        e = lds_limit(&k_decode_chunk_gate_up<NL>, lds);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(k_decode_chunk_gate_up<NL>, dim3((unsigned)(items < 768 ? items : 768)), dim3(64 * kChunkWaves), lds, st,
+                           gate_up_args(D));
+    }
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const DownArgs g = down_args(D);
+    if (down_fused(D)) {
+        const int lds = PairDownLds(D.T * D.k, D.f, NL, g.ksplit).bytes;
+        e = lds_limit(&k_decode_pair_down<kT>, lds);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(k_decode_pair_down<kT>, dim3(D.d / 32), dim3(64 * kPairDownWaves), lds, st, g);
+    } else {
+        const int64_t units = (int64_t)(by_pairs(D) ? D.T * D.k : D.L.max_chunks) * ((D.d / 32 + 1) / 2);
+        const unsigned grid = nblk(units, kDownWaves);
+        hipLaunchKernelGGL(k_decode_chunk_down<NL>, dim3(grid < 768 ? grid : 768), dim3(64 * kDownWaves), 0, st, g);
+    }
+    return hipGetLastError();
+}
+
+template <int kT>
+hipError_t combine_typed(const DecodeLaunch& D, hipStream_t st)
+{
+    if (down_fused(D)) return hipSuccess;
+    const DownArgs g = down_args(D);
+    hipLaunchKernelGGL(k_decode_combine<kT>, dim3(nblk(D.d / 4, 256), D.T), dim3(256), 0, st, g.dm, g.wts, g.eidx, D.T, D.k, D.d,
+                       D.y, D.y_stride);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_decode_route(const DecodeLaunch& D, hipStream_t st)
+{
+    return D.dtype == kF32 ? route_typed<kF32>(D, st) : D.dtype == kBF16 ? route_typed<kBF16>(D, st) : route_typed<kF16>(D, st);
+}
+
+hipError_t launch_decode_products(const DecodeLaunch& D, hipStream_t st)
+{
+    return D.dtype == kF32 ? products_typed<kF32>(D, st)
+                           : D.dtype == kBF16 ? products_typed<kBF16>(D, st) : products_typed<kF16>(D, st);
 }
 
 hipError_t launch_decode_combine(const DecodeLaunch& D, hipStream_t st)
 {
-    const float* dm = reinterpret_cast<const float*>(D.ws + D.L.dm);
-    const float* wts = reinterpret_cast<const float*>(D.ws + D.L.wts);
-    const int32_t* eidx = reinterpret_cast<const int32_t*>(D.ws + D.L.eidx);
-    const dim3 grid(nblk((int64_t)D.T * (D.d / 4), 256)), block(256);
-    if (D.dtype == kF32)
-        hipLaunchKernelGGL(k_decode_combine<kF32>, grid, block, 0, st, dm, wts, eidx, D.T, D.k, D.d, D.y, D.y_stride);
-    else if (D.dtype == kBF16)
-        hipLaunchKernelGGL(k_decode_combine<kBF16>, grid, block, 0, st, dm, wts, eidx, D.T, D.k, D.d, D.y, D.y_stride);
-    else
-        hipLaunchKernelGGL(k_decode_combine<kF16>, grid, block, 0, st, dm, wts, eidx, D.T, D.k, D.d, D.y, D.y_stride);
-    return hipGetLastError();
+    return D.dtype == kF32 ? combine_typed<kF32>(D, st)
+                           : D.dtype == kBF16 ? combine_typed<kBF16>(D, st) : combine_typed<kF16>(D, st);
 }
 
 }  // namespace moe

@@ -1073,6 +1073,7 @@ int moe_decode_run_layer(moe_prefill_t* h, const moe_decode_io_t* io_in, void* s
         D.ws = static_cast<uint8_t*>(io.workspace);
         D.eidx_out = io.eidx;
         D.wts_out = io.weights;
+        D.need_counts = W.sparse_slot >= 0;
         hipError_t e = launch_decode_route(D, st);
         if (e == hipSuccess && W.sparse_slot >= 0)
             e = launch_expert_load(h->blobs_dev[io.layer], h->pool + (uint64_t)W.sparse_slot * h->slot_bytes,

@@ -84,9 +84,10 @@ def layer(x, logits, k, gu_q, gu_s, d_q, d_s):
     Returns (y, bound on |kernel - y| before the rounding to the output's type, eidx, weights).
 
     The bound: a block of 32 activations in fixed point is off by 2^-23 (1 + 1/64) of its largest
-    magnitude; a sum over nb blocks in fp32 makes at most nb + 6 roundings of 2^-24 of the sum of
+    magnitude (24 bits, for fp32 x) or 2^-15 (1 + 1/64) (16 bits, for bf16 and fp16); a sum over nb blocks in fp32 makes at most nb + 6 roundings of 2^-24 of the sum of
     magnitudes (join, scale product and fma per block, then the waves' sums); the router weights
     are off by k + 8 half steps and the combine by k."""
+    step = 2.0 ** -23 if x.dtype == torch.float32 else 2.0 ** -15
     x, logits = x.double().cpu(), logits.double().cpu()
     T, E = logits.shape
     d, f = x.shape[1], gu_q.shape[1] // 2
@@ -98,7 +99,7 @@ def layer(x, logits, k, gu_q, gu_s, d_q, d_s):
     def product(v, ev, q, s):
         w = q.double().cpu() * s.double().cpu().repeat_interleave(32, -1)
         nb = v.numel() // 32
-        fixed = v.reshape(nb, 32).abs().amax(-1).repeat_interleave(32) * 2.0 ** -23 * (1 + 1 / 64)
+        fixed = v.reshape(nb, 32).abs().amax(-1).repeat_interleave(32) * step * (1 + 1 / 64)
         err = w.abs() @ (ev + fixed) + 2 * (nb + 6) * 2.0 ** -24 * (w.abs() @ v.abs())
         return w @ v, err
 

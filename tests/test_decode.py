@@ -59,7 +59,9 @@ def check(y, ex, L, x, logits):
     got = y.double()
     bad = ~((got - want).abs() <= tol)
     assert not bad.any(), (int(bad.sum()), bad.nonzero()[0].tolist(), float((got - want).abs().max()))
-    assert float((got - want).norm()) <= (2e-6 + 1.2 * ref.half_step(x.dtype)) * float(want.norm()) + ref.least_step(x.dtype) * got.numel() ** 0.5
+    # the fixed-point steps average out over a row: 2^-23 (2^-15) of a block's largest, a few times its rms
+    fixed = 2e-6 if x.dtype == torch.float32 else 2.0 ** -14
+    assert float((got - want).norm()) <= (fixed + 1.2 * ref.half_step(x.dtype)) * float(want.norm()) + ref.least_step(x.dtype) * got.numel() ** 0.5
     if ex is not None:
         assert torch.equal(ex["eidx"], eidx)
         assert ((ex["weights"].double() - wts).abs() <= (2 * L.k + 8) * 2.0 ** -24 * wts + 1e-30).all()
