@@ -9,14 +9,14 @@
 namespace moe {
 
 constexpr int kDecodeMaxPairs = 1024;   // n_tokens * top_k of one call
-constexpr int kChunkRows = 16;          // most rows of one expert that share one read of its weights
-constexpr int kChunkRowsF32 = 8;        // ... of fp32 activations (three limbs a row instead of two)
+constexpr int kChunkRows = 4;           // most rows of one expert that share one read of its weights
+constexpr int kChunkRowsF32 = 2;        // ... of fp32 activations (three limbs a row instead of two)
 
 // One work item of the expert products: (token, slot) pairs of one expert.
 struct DecodeChunk {
     int32_t expert, n;
     int32_t pair[kChunkRows];
-    int32_t pad[2];
+    int32_t pad[2];            // 32 bytes
 };
 
 struct DecodeWs {
@@ -28,7 +28,7 @@ static inline DecodeWs decode_ws(int d, int f, int E, int k, int T)
 {
     DecodeWs L;
     const uint64_t R = (uint64_t)T * k;
-    // sum over experts of ceil(rows / 8): at most one partial chunk per reached expert
+    // sum over experts of ceil(rows / 2): at most one partial chunk per reached expert
     L.max_chunks = (int)(R / kChunkRowsF32) + (int)(R < (uint64_t)E ? R : (uint64_t)E);
     uint64_t o = 0;
     auto take = [&](uint64_t bytes) { uint64_t at = o; o = align_up(o + bytes, 256); return at; };

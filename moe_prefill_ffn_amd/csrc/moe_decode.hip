@@ -68,15 +68,16 @@ __device__ __forceinline__ void limbs(int q, int (&l)[3])
 }
 
 // Limb l of token m is row kRowStep m + l of the instruction's 32 rows, so that a lane gets the
-// limb sums of a (token, column) in neighbouring result registers: quad c of lane half h holds
-// rows 8 c + 4 h .. + 3, that is token 2 c + h of three limbs, or tokens 4 c + 2 h and the next
-// of two.
+// limb sums of a (token, column) in neighbouring result registers.  Only the first 8 rows are
+// used, the first register quad of both lane halves: half h holds rows 4 h .. 4 h + 3, that is
+// token h of three limbs, or tokens 2 h and 2 h + 1 of two.  (More rows a read cost registers,
+// and so waves in flight, and LDS for their activations: 24 tokens on the wide layer took 75 us
+// of gate/up with up to 16 rows.)
 template <int NL>
 struct Limbs {
     static constexpr int kRowStep = NL == 2 ? 2 : 4;
-    static constexpr int kTokens = 32 / kRowStep;         // tokens of one instruction, rows of a chunk
-    static constexpr int kPerQuad = 4 / kRowStep;         // tokens of a lane's quad
-    __device__ static __forceinline__ int token(int c, int i, int h) { return kPerQuad * (2 * c + h) + i; }
+    static constexpr int kTokens = 8 / kRowStep;          // rows of a chunk
+    static constexpr int kPerHalf = 4 / kRowStep;         // tokens of a lane half
 };
 constexpr int limbs_of(int dtype) { return dtype == kF32 ? 3 : 2; }
 
@@ -372,14 +373,13 @@ struct Ring {
     }
 };
 
-// acc[t][kPerQuad c + i] += block b's products for token i of quad c (NQ quads): q = 0 / 1, the
-// first / second block of ring slot u.
-//   a             the 16 bytes of the block that this lane feeds
-//   scl(c, i, b)  the scale of that token's block
-template <int NL, int NT, int NQ, int U, class Scl>
-__device__ __forceinline__ void block_product(float (&acc)[NT][8], const Ring<NT, U>& r, int u, int q, v4i a, int b, Scl scl)
+// acc[t][i] += block b's products for token i of this lane half: q = 0 / 1, the first / second
+// block of ring slot u.
+//   a          the 16 bytes of the block that this lane feeds
+//   scl(i, b)  the scale of that token's block
+template <int NL, int kTok, int NT, int U, class Scl>
+__device__ __forceinline__ void block_product(float (&acc)[NT][kTok], const Ring<NT, U>& r, int u, int q, v4i a, int b, Scl scl)
 {
-    constexpr int kPer = Limbs<NL>::kPerQuad;
     const v16i zero = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
     v16i s[NT];
     float ws[NT];
@@ -391,43 +391,34 @@ __device__ __forceinline__ void block_product(float (&acc)[NT][8], const Ring<NT
         ws[t] = (float)__builtin_bit_cast(_Float16, hb) * 0.0625f;
     }
 #pragma unroll
-    for (int c = 0; c < NQ; ++c)
+    for (int i = 0; i < kTok; ++i) {
+        const float x = scl(i, b);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const float x = scl(c, i, b);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                // 16 x the limb sums; s0 + 256 s1 is a multiple of 16 below 2^28: exact in fp32
-                const int k = 4 * c + (NL == 2 ? 2 * i : 0);
-                float v = (float)(s[t][k] + (s[t][k + 1] << 8));
-                if (NL == 3) v = __builtin_fmaf((float)s[t][k + 2], 65536.0f, v);
-                acc[t][kPer * c + i] = __builtin_fmaf(v, ws[t] * x, acc[t][kPer * c + i]);
-            }
+        for (int t = 0; t < NT; ++t) {
+            // 16 x the limb sums; s0 + 256 s1 is a multiple of 16 below 2^28: exact in fp32
+            float v = (float)(s[t][2 * i] + (s[t][2 * i + 1] << 8));
+            if (NL == 3) v = __builtin_fmaf((float)s[t][2], 65536.0f, v);
+            acc[t][i] = __builtin_fmaf(v, ws[t] * x, acc[t][i]);
         }
+    }
     __builtin_amdgcn_sched_barrier(0);                    // one block's sums at a time in registers
 }
 
-// K pairs [p0, p1) of a filled ring.  act(b): the bytes of block b that this lane feeds, read one
-// pair ahead of their use.
-template <int NL, int NT, int NQ, int U, class Act, class Scl>
-__device__ __forceinline__ void ring_product(float (&acc)[NT][8], Ring<NT, U>& r, const WeightAt& w, int p0, int p1, int nb,
-                                             Act act, Scl scl)
+// K pairs [p0, p1) of a filled ring, the activations in LDS: act(b) gives the bytes of block b
+// that this lane feeds.
+template <int NL, int kTok, int NT, int U, class Act, class Scl>
+__device__ __forceinline__ void ring_product(float (&acc)[NT][kTok], Ring<NT, U>& r, const WeightAt& w, int p0, int p1,
+                                             int nb, Act act, Scl scl)
 {
-    // the padded block of an odd count is left out; its place here repeats the one before
-    auto second = [&](int pr) { return 2 * pr + 1 < nb ? 2 * pr + 1 : 2 * pr; };
-    v4i a0 = act(2 * p0), a1 = act(second(p0));
     for (int pb = p0; pb < p1; pb += U) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int pr = pb + u;
             if (pr >= p1) break;                          // uniform
-            const int ahead = pr + 1 < p1 ? pr + 1 : pr;
-            const v4i n0 = act(2 * ahead), n1 = act(second(ahead));
-            block_product<NL, NT, NQ>(acc, r, u, 0, a0, 2 * pr, scl);
-            if (2 * pr + 1 < nb) block_product<NL, NT, NQ>(acc, r, u, 1, a1, 2 * pr + 1, scl);
+            block_product<NL, kTok>(acc, r, u, 0, act(2 * pr), 2 * pr, scl);
+            // the padded block of an odd count is left out
+            if (2 * pr + 1 < nb) block_product<NL, kTok>(acc, r, u, 1, act(2 * pr + 1), 2 * pr + 1, scl);
             if (pr + U < p1) r.load(u, w, pr + U);
-            a0 = n0;
-            a1 = n1;
         }
     }
 }
@@ -468,9 +459,7 @@ __device__ __forceinline__ void store_h(const GateUpArgs& g, int p, int fb, floa
 // registers -- and turns the token's x into fixed point in LDS, so that no launch comes before
 // it.  Pairs of the same expert each read its weights (from a cache).  The workgroups of
 // f-block 0 and slot 0 leave the token's routing for the next kernel.
-constexpr int kPairWaves = 8;
-
-template <int kT>
+template <int kT, int kPairWaves>
 __global__ __launch_bounds__(64 * kPairWaves) void k_decode_pair_gate_up(GateUpArgs g)
 {
     constexpr int NL = limbs_of(kT);
@@ -537,8 +526,8 @@ __global__ __launch_bounds__(64 * kPairWaves) void k_decode_pair_gate_up(GateUpA
         if (j32 < NL) a = *reinterpret_cast<const v4i*>(xl + j32 * d + b * 32 + 16 * h);
         return a;
     };
-    float acc[2][8] = {};
-    if (p0 < p1) ring_product<NL, 2, 1>(acc, ring, w, p0, p1, nb, act, [&](int, int, int b) { return xs[b]; });
+    float acc[2][1] = {};
+    if (p0 < p1) ring_product<NL, 1>(acc, ring, w, p0, p1, nb, act, [&](int, int b) { return xs[b]; });
     if (h == 0) {
         s_red[wave][0][j32] = acc[0][0];
         s_red[wave][1][j32] = acc[1][0];
@@ -555,93 +544,6 @@ __global__ __launch_bounds__(64 * kPairWaves) void k_decode_pair_gate_up(GateUpA
 }
 
 // ----------------------------------------------------- chunks: gate/up, down ---
-// Rows (token, slot pairs) that share an expert's weights: a chunk of the route kernel's list,
-// or a pair by itself.
-struct Rows {
-    int e, n;                 // expert (-1: not available), pairs
-    const int32_t* list;      // null: the pair `own`
-    int own;
-    __device__ __forceinline__ int pair(int m) const { return list ? list[m] : own; }
-};
-
-// f(quads) with the quads that n tokens need as a compile-time number
-template <int NL, class F>
-__device__ __forceinline__ void for_quads(int n, F f)
-{
-    constexpr int kPer = 2 * Limbs<NL>::kPerQuad;         // tokens of a quad of both lane halves
-    if (n <= kPer)
-        f(std::integral_constant<int, 1>{});
-    else if (n <= 2 * kPer)
-        f(std::integral_constant<int, 2>{});
-    else if (n <= 3 * kPer)
-        f(std::integral_constant<int, 3>{});
-    else
-        f(std::integral_constant<int, 4>{});
-}
-
-// Each (chunk, f-block) is an item; a fixed number of workgroups go through the items, since
-// only the device knows how many there are.  The waves split K.
-constexpr int kChunkWaves = 4;
-
-template <int NL>
-__global__ __launch_bounds__(64 * kChunkWaves) __attribute__((amdgpu_waves_per_eu(3))) void k_decode_chunk_gate_up(GateUpArgs g)
-{
-    using Lb = Limbs<NL>;
-    extern __shared__ float s_scale[];                    // [kTokens][d / 32]
-    __shared__ float s_red[kChunkWaves][2][Lb::kTokens][32];
-    const RouteArgs& r = g.r;
-    const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, j32 = lane & 31;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int d = r.d, nb = d / 32, npairs = k_pairs(d), nfb = g.f / 32;
-    const int items = *g.nchunks * nfb;
-    const int m_a = j32 / Lb::kRowStep, l_a = j32 % Lb::kRowStep;   // the A row this lane feeds
-    const int p0 = wave * npairs / kChunkWaves, p1 = (wave + 1) * npairs / kChunkWaves;
-    for (int it = blockIdx.x; it < items; it += gridDim.x) {
-        const int ci = it / nfb, fb = it - ci * nfb;
-        const DecodeChunk& ch = g.chunks[ci];
-        const int n = ch.n, e = ch.expert;
-        const WeightAt w = weights_at(g.blob + (uint64_t)e * g.expert_stride, g.q_off, g.s_off, 2 * fb, d);
-        Ring<2, 2> ring;
-        ring.fill(w, p0, p1);                             // in flight while the scales are staged
-        __syncthreads();                                  // the previous item's LDS is read
-        for (int i = tid; i < n * nb; i += 64 * kChunkWaves) {
-            const int m = i / nb;
-            s_scale[i] = r.xs[(int64_t)(ch.pair[m] / r.k) * nb + (i - m * nb)];
-        }
-        const bool on = m_a < n && l_a < NL;
-        const int8_t* al = r.xl + ((int64_t)(ch.pair[on ? m_a : 0] / r.k) * NL + (on ? l_a : 0)) * d + 16 * h;
-        auto act = [&](int b) -> v4i {
-            v4i a = {0, 0, 0, 0};
-            if (on) a = *reinterpret_cast<const v4i*>(al + b * 32);
-            return a;
-        };
-        __syncthreads();
-        float acc[2][8] = {};
-        // an absent token's column is not stored: whatever its place in the array holds will do
-        const float* xs = s_scale + Lb::token(0, 0, h) * nb;
-        auto scl = [&](int c, int i, int b) { return xs[(2 * Lb::kPerQuad * c + i) * nb + b]; };
-        if (p0 < p1)
-            for_quads<NL>(n, [&](auto nq) { ring_product<NL, 2, decltype(nq)::value>(acc, ring, w, p0, p1, nb, act, scl); });
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int i = 0; i < Lb::kPerQuad; ++i) {
-                s_red[wave][0][Lb::token(c, i, h)][j32] = acc[0][Lb::kPerQuad * c + i];
-                s_red[wave][1][Lb::token(c, i, h)][j32] = acc[1][Lb::kPerQuad * c + i];
-            }
-        __syncthreads();
-        for (int m = tid >> 5; m < n; m += 2 * kChunkWaves) {   // uniform over the 32-lane half
-            float z[2] = {};
-#pragma unroll
-            for (int v = 0; v < kChunkWaves; ++v) {
-                z[0] += s_red[v][0][m][j32];
-                z[1] += s_red[v][1][m][j32];
-            }
-            store_h<NL>(g, ch.pair[m], fb, z[0], z[1]);
-        }
-    }
-}
-
 struct DownArgs {
     const int32_t* nchunks;   // null: pair p is the chunk of itself
     const DecodeChunk* chunks;
@@ -657,63 +559,112 @@ struct DownArgs {
     int64_t y_stride;
 };
 
-// Each wave takes (chunk, two 32-column tiles) units by itself: all of K, no barrier.
-constexpr int kDownWaves = 4;
-constexpr int kDownSeg = 32;  // K pairs whose scales a wave holds in LDS at a time
+struct ChunkArgs {
+    GateUpArgs g;
+    DownArgs d;
+};
 
+// LDS of a chunk kernel: the rows' activations (rows kPad apart in bank groups), their block
+// scales.
+constexpr int kActPad = 32;
 template <int NL>
-__global__ __launch_bounds__(64 * kDownWaves) __attribute__((amdgpu_waves_per_eu(3))) void k_decode_chunk_down(DownArgs g)
+constexpr int chunk_lds(int K) { return Limbs<NL>::kTokens * (NL * (K + kActPad) + K / 32 * 4); }
+
+// Rows that share an expert's weights: a chunk of the route kernel's list (up to kTokens), or a
+// pair by itself.  A workgroup takes a chunk by two 32-column tiles -- the gate and the up tile of
+// an f-block, or two tiles of the down matrix -- its waves split K and add up through LDS.  A
+// fixed number of workgroups goes through the items, since only the device knows how many there
+// are; the chunks of an expert follow each other at a multiple of 8 workgroups, so that one XCD
+// reads a tile for all of them (the first from memory, the others from its L2).
+constexpr int kChunkWaves = 4;
+
+template <int NL, bool kGateUp>
+__global__ __launch_bounds__(64 * kChunkWaves) __attribute__((amdgpu_waves_per_eu(4))) void k_decode_chunk(ChunkArgs a)
 {
     using Lb = Limbs<NL>;
-    __shared__ float s_scales[kDownWaves][Lb::kTokens][2 * kDownSeg];
-    const int lane = threadIdx.x & 63, h = lane >> 5, j32 = lane & 31;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int R = g.T * g.k, nb = g.f / 32, npairs = k_pairs(g.f), tiles = g.d / 32, tile2 = (tiles + 1) / 2;
-    const int units = (g.nchunks ? *g.nchunks : R) * tile2;
-    const int m_a = j32 / Lb::kRowStep, l_a = j32 % Lb::kRowStep;
-    float(&scales)[Lb::kTokens][2 * kDownSeg] = s_scales[wave];
-    for (int u = blockIdx.x * kDownWaves + wave; u < units; u += gridDim.x * kDownWaves) {
-        const int ci = u / tile2, nt = 2 * (u - ci * tile2);
-        const Rows rw = g.nchunks ? Rows{g.chunks[ci].expert, g.chunks[ci].n, g.chunks[ci].pair, 0}
-                                  : Rows{g.eidx[ci], 1, nullptr, ci};
-        if (rw.e < 0) continue;
-        const int n = rw.n;
-        // an odd tile count: the last unit's second tile is its first again, not stored
-        WeightAt w = weights_at(g.blob + (uint64_t)rw.e * g.expert_stride, g.q_off, g.s_off, nt, g.f);
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    __shared__ float s_red[kChunkWaves][2][Lb::kTokens][32];
+    const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, j32 = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int K = kGateUp ? a.g.r.d : a.d.f, nb = K / 32, npairs = k_pairs(K);
+    const int tiles = kGateUp ? a.g.f / 32 * 2 : a.d.d / 32, tile2 = (tiles + 1) / 2, stride = (tile2 + 7) & ~7;
+    const int32_t* nchunks = kGateUp ? a.g.nchunks : a.d.nchunks;
+    const int items = (nchunks ? *nchunks : a.d.T * a.d.k) * stride;
+    const int p0 = wave * npairs / kChunkWaves, p1 = (wave + 1) * npairs / kChunkWaves;
+    int8_t* s_act = reinterpret_cast<int8_t*>(lds);
+    float* s_scale = reinterpret_cast<float*>(lds + Lb::kTokens * NL * (K + kActPad));
+    const int8_t* acts = kGateUp ? a.g.r.xl : a.d.hl;
+    const float* scales = kGateUp ? a.g.r.xs : a.d.hs;
+
+    for (int it = blockIdx.x; it < items; it += gridDim.x) {
+        const int ci = it / stride, nt = 2 * (it - ci * stride);
+        if (nt >= tiles) continue;
+        const DecodeChunk* ch = (kGateUp ? a.g.chunks : a.d.chunks) + ci;
+        const int e = nchunks ? ch->expert : a.d.eidx[ci], n = nchunks ? ch->n : 1;
+        if (e < 0) continue;
         const bool two = nt + 1 < tiles;
-        if (!two) w.q_step = w.s_step = 0;
-        const bool on = m_a < n && l_a < NL;
-        const int8_t* al = g.hl + ((int64_t)rw.pair(on ? m_a : 0) * NL + (on ? l_a : 0)) * g.f + 16 * h;
-        auto act = [&](int b) -> v4i {
-            v4i a = {0, 0, 0, 0};
-            if (on) a = *reinterpret_cast<const v4i*>(al + b * 32);
-            return a;
-        };
-        float acc[2][8] = {};
-        for (int s0 = 0; s0 < npairs; s0 += kDownSeg) {
-            const int s1 = s0 + kDownSeg < npairs ? s0 + kDownSeg : npairs;
-            Ring<2, 2> ring;
-            ring.fill(w, s0, s1);
-            __builtin_amdgcn_wave_barrier();
-            for (int m = 0; m < n; ++m) {
-                const int b = 2 * s0 + lane;              // 2 kDownSeg = 64 blocks
-                if (b < nb) scales[m][lane] = g.hs[(int64_t)rw.pair(m) * nb + b];
+        WeightAt w = weights_at(kGateUp ? a.g.blob + (uint64_t)e * a.g.expert_stride : a.d.blob + (uint64_t)e * a.d.expert_stride,
+                                kGateUp ? a.g.q_off : a.d.q_off, kGateUp ? a.g.s_off : a.d.s_off, nt, K);
+        if (!two) w.q_step = w.s_step = 0;                // an odd count's last tile twice, stored once
+        Ring<2, 4> ring;
+        ring.fill(w, p0, p1);                             // in flight while the activations are staged
+        int pair[Lb::kTokens];
+#pragma unroll
+        for (int m = 0; m < Lb::kTokens; ++m) pair[m] = nchunks ? ch->pair[m < n ? m : 0] : ci;
+        __syncthreads();                                  // the previous item's LDS is read
+#pragma unroll
+        for (int m = 0; m < Lb::kTokens; ++m) {
+            if (m >= n) break;                            // uniform
+            const int64_t src = kGateUp ? pair[m] / a.g.r.k : pair[m];
+            for (int i = tid * 16; i < NL * K; i += 64 * kChunkWaves * 16) {
+                const int l = (i >= K) + (i >= 2 * K);    // K is a multiple of 32: a piece is in one plane
+                *reinterpret_cast<uint4*>(s_act + (m * NL + l) * (K + kActPad) + i - l * K) =
+                    *reinterpret_cast<const uint4*>(acts + src * NL * K + i);
             }
-            __builtin_amdgcn_wave_barrier();
-            const float* xs = &scales[Lb::token(0, 0, h)][0] - 2 * s0;   // as above for absent tokens
-            auto scl = [&](int c, int i, int b) { return xs[(2 * Lb::kPerQuad * c + i) * 2 * kDownSeg + b]; };
-            for_quads<NL>(n, [&](auto nq) { ring_product<NL, 2, decltype(nq)::value>(acc, ring, w, s0, s1, nb, act, scl); });
+            for (int i = tid; i < nb; i += 64 * kChunkWaves) s_scale[m * nb + i] = scales[src * nb + i];
         }
+        __syncthreads();
+        const int m_a = j32 / Lb::kRowStep, l_a = j32 % Lb::kRowStep;   // the A row this lane feeds
+        const bool on = m_a < n && l_a < NL;
+        const int8_t* al = s_act + (m_a * NL + l_a) * (K + kActPad) + 16 * h;
+        auto act = [&](int b) -> v4i {
+            v4i v = {0, 0, 0, 0};
+            if (on) v = *reinterpret_cast<const v4i*>(al + b * 32);
+            return v;
+        };
+        // an absent token's column is not stored: whatever its place in the array holds will do
+        const float* xs = s_scale + Lb::kPerHalf * h * nb;
+        float acc[2][Lb::kPerHalf] = {};
+        if (p0 < p1)
+            ring_product<NL, Lb::kPerHalf>(acc, ring, w, p0, p1, nb, act, [&](int i, int b) { return xs[i * nb + b]; });
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int i = 0; i < Lb::kPerHalf; ++i) {
+            s_red[wave][0][Lb::kPerHalf * h + i][j32] = acc[0][i];
+            s_red[wave][1][Lb::kPerHalf * h + i][j32] = acc[1][i];
+        }
+        __syncthreads();
+        // gate/up: row m by a half wave; down: row m's tile t by a half wave
+        if (kGateUp) {
+            const int m = tid >> 5;
+            if (m < n) {                                  // uniform over the 32-lane half
+                float z[2] = {};
 #pragma unroll
-            for (int i = 0; i < Lb::kPerQuad; ++i) {
-                const int m = Lb::token(c, i, h);
-                if (m >= n) continue;
-                float* o = g.dm + (int64_t)rw.pair(m) * g.d + nt * 32 + j32;
-                o[0] = acc[0][Lb::kPerQuad * c + i];
-                if (two) o[32] = acc[1][Lb::kPerQuad * c + i];
+                for (int v = 0; v < kChunkWaves; ++v) {
+                    z[0] += s_red[v][0][m][j32];
+                    z[1] += s_red[v][1][m][j32];
+                }
+                store_h<NL>(a.g, nchunks ? ch->pair[m] : ci, nt >> 1, z[0], z[1]);
             }
+        } else {
+            const int m = tid >> 6, t = (tid >> 5) & 1;
+            if (m < n && (t == 0 || two)) {
+                float z = 0.0f;
+#pragma unroll
+                for (int v = 0; v < kChunkWaves; ++v) z += s_red[v][t][m][j32];
+                a.d.dm[(int64_t)(nchunks ? ch->pair[m] : ci) * a.d.d + (nt + t) * 32 + j32] = z;
+            }
+        }
+        static_assert(Lb::kTokens <= kChunkWaves, "a wave per row");
     }
 }
 
@@ -770,7 +721,7 @@ __global__ __launch_bounds__(64 * kPairDownWaves) void k_decode_pair_down(DownAr
     for (int u = wave; u < units; u += kPairDownWaves) {
         if (u != wave) open(u);
         const int p = u / g.ksplit, ks = u - p * g.ksplit;
-        float acc[1][8] = {};
+        float acc[1][1] = {};
         if (e >= 0) {
             const int8_t* al = s_hl + (p * NL + j32) * g.f + 16 * h;
             auto act = [&](int b) -> v4i {
@@ -778,7 +729,7 @@ __global__ __launch_bounds__(64 * kPairDownWaves) void k_decode_pair_down(DownAr
                 if (j32 < NL) a = *reinterpret_cast<const v4i*>(al + b * 32);
                 return a;
             };
-            ring_product<NL, 1, 1>(acc, ring, w, p0, p1, nb, act, [&](int, int, int b) { return s_hs[p * nb + b]; });
+            ring_product<NL, 1>(acc, ring, w, p0, p1, nb, act, [&](int, int b) { return s_hs[p * nb + b]; });
         }
         if (h == 0) s_dm[(ks * R + p) * 32 + j32] = acc[0][0];
     }
@@ -951,6 +902,22 @@ hipError_t lds_limit(K kernel, int bytes)
     return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
+// chunks: the most there can be; tile2: two-tile columns of the matrix
+template <int NL, bool kGateUp>
+hipError_t launch_chunk(const DecodeLaunch& D, int chunks, int K, int tile2, hipStream_t st)
+{
+    const int64_t items = (int64_t)chunks * align_up(tile2, 8);
+    const int lds = chunk_lds<NL>(K);
+    const hipError_t e = lds_limit(&k_decode_chunk<NL, kGateUp>, lds);
+    if (e != hipSuccess) return e;
+    ChunkArgs a;
+    a.g = gate_up_args(D);
+    a.d = down_args(D);
+    hipLaunchKernelGGL((k_decode_chunk<NL, kGateUp>), dim3((unsigned)(items < 1024 ? items : 1024)), dim3(64 * kChunkWaves), lds,
+                       st, a);
+    return hipGetLastError();
+}
+
 template <int kT>
 hipError_t products_typed(const DecodeLaunch& D, hipStream_t st)
 {
@@ -958,16 +925,22 @@ hipError_t products_typed(const DecodeLaunch& D, hipStream_t st)
     hipError_t e = hipSuccess;
     if (by_pairs(D)) {
         const int lds = NL * D.d + D.d / 32 * 4;
-        e = lds_limit(&k_decode_pair_gate_up<kT>, lds);
-        if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(k_decode_pair_gate_up<kT>, dim3(D.f / 32, D.T * D.k), dim3(64 * kPairWaves), lds, st, gate_up_args(D));
+        const dim3 grid(D.f / 32, D.T * D.k);
+        // two workgroups of eight waves fill a CU, four of four: more than the first hold would
+        // wait for a second round (5 tokens of the resident configuration, 960 workgroups: 20.5 us
+        // of eight waves, 15.4 of four), fewer are done sooner by more waves (1 token: 8.2, 9.0)
+        if (grid.x * grid.y > 512) {
+            e = lds_limit(&k_decode_pair_gate_up<kT, 4>, lds);
+            if (e != hipSuccess) return e;
+            hipLaunchKernelGGL((k_decode_pair_gate_up<kT, 4>), grid, dim3(64 * 4), lds, st, gate_up_args(D));
+        } else {
+            e = lds_limit(&k_decode_pair_gate_up<kT, 8>, lds);
+            if (e != hipSuccess) return e;
+            hipLaunchKernelGGL((k_decode_pair_gate_up<kT, 8>), grid, dim3(64 * 8), lds, st, gate_up_args(D));
+        }
     } else {
-        const int64_t items = (int64_t)D.L.max_chunks * (D.f / 32);
-        const int lds = Limbs<NL>::kTokens * (D.d / 32) * 4;
-        e = lds_limit(&k_decode_chunk_gate_up<NL>, lds);
+        e = launch_chunk<NL, true>(D, D.L.max_chunks, D.d, D.f / 32, st);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(k_decode_chunk_gate_up<NL>, dim3((unsigned)(items < 768 ? items : 768)), dim3(64 * kChunkWaves), lds, st,
-                           gate_up_args(D));
     }
     e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -978,9 +951,7 @@ hipError_t products_typed(const DecodeLaunch& D, hipStream_t st)
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL(k_decode_pair_down<kT>, dim3(D.d / 32), dim3(64 * kPairDownWaves), lds, st, g);
     } else {
-        const int64_t units = (int64_t)(by_pairs(D) ? D.T * D.k : D.L.max_chunks) * ((D.d / 32 + 1) / 2);
-        const unsigned grid = nblk(units, kDownWaves);
-        hipLaunchKernelGGL(k_decode_chunk_down<NL>, dim3(grid < 768 ? grid : 768), dim3(64 * kDownWaves), 0, st, g);
+        return launch_chunk<NL, false>(D, by_pairs(D) ? D.T * D.k : D.L.max_chunks, D.f, (D.d / 32 + 1) / 2, st);
     }
     return hipGetLastError();
 }
