@@ -749,39 +749,36 @@ __global__ __launch_bounds__(64 * kPairDownWaves) void k_decode_pair_down(DownAr
 }
 
 // ------------------------------------------------------------------ combine ---
-// y[t] = sum over j of w[t, j] dm[t, j].  Four slots' rows are loaded together; a slot without
-// an expert reads the row of slot 0 (present if any is) and adds nothing.
+// y[t] = sum over j of w[t, j] dm[t, j].  Eight slots' rows, weights and experts are loaded
+// together, none of them waiting for another: a slot without an expert reads its row too (it
+// holds what the workspace held) and drops it.
 template <int kT>
 __global__ __launch_bounds__(256) void k_decode_combine(const float* __restrict__ dm,
                                                         const float* __restrict__ wts,
-                                                        const int32_t* __restrict__ eidx, int T, int k,
+                                                        const int32_t* __restrict__ eidx, int k,
                                                         int d, void* __restrict__ y, int64_t y_stride)
 {
-    const int d4 = d >> 2;
     const int t = blockIdx.y, c = ((int)blockIdx.x * 256 + (int)threadIdx.x) * 4;
-    if (c >= d4 * 4) return;
-    const int32_t* te = eidx + t * k;
-    const float* tw = wts + t * k;
+    if (c >= d) return;
     float acc[4] = {};
-    if (te[0] >= 0) {                                     // available experts come first
-        for (int j0 = 0; j0 < k; j0 += 4) {
-            float4 v[4];
-            float w[4];
+    for (int j0 = 0; j0 < k; j0 += 8) {
+        float4 v[8];
+        float w[8];
+        int e[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = j0 + i < k ? j0 + i : k - 1;
-                const bool live = j0 + i < k && te[j] >= 0;
-                w[i] = live ? tw[j] : 0.0f;
-                v[i] = *reinterpret_cast<const float4*>(dm + (int64_t)(t * k + (live ? j : 0)) * d + c);
-                if (!live) v[i] = float4{0.0f, 0.0f, 0.0f, 0.0f};
-            }
+        for (int i = 0; i < 8; ++i) {
+            const int p = t * k + (j0 + i < k ? j0 + i : k - 1);
+            v[i] = *reinterpret_cast<const float4*>(dm + (int64_t)p * d + c);
+            w[i] = wts[p];
+            e[i] = eidx[p];
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                acc[0] = __builtin_fmaf(w[i], v[i].x, acc[0]);
-                acc[1] = __builtin_fmaf(w[i], v[i].y, acc[1]);
-                acc[2] = __builtin_fmaf(w[i], v[i].z, acc[2]);
-                acc[3] = __builtin_fmaf(w[i], v[i].w, acc[3]);
-            }
+        for (int i = 0; i < 8; ++i) {
+            if (j0 + i >= k || e[i] < 0) continue;        // uniform
+            acc[0] = __builtin_fmaf(w[i], v[i].x, acc[0]);
+            acc[1] = __builtin_fmaf(w[i], v[i].y, acc[1]);
+            acc[2] = __builtin_fmaf(w[i], v[i].z, acc[2]);
+            acc[3] = __builtin_fmaf(w[i], v[i].w, acc[3]);
         }
     }
     store_n<kT, 4>(static_cast<uint8_t*>(y) + ((int64_t)t * y_stride + c) * dtype_bytes(kT), acc);
@@ -961,8 +958,8 @@ hipError_t combine_typed(const DecodeLaunch& D, hipStream_t st)
 {
     if (down_fused(D)) return hipSuccess;
     const DownArgs g = down_args(D);
-    hipLaunchKernelGGL(k_decode_combine<kT>, dim3(nblk(D.d / 4, 256), D.T), dim3(256), 0, st, g.dm, g.wts, g.eidx, D.T, D.k, D.d,
-                       D.y, D.y_stride);
+    hipLaunchKernelGGL(k_decode_combine<kT>, dim3(nblk(D.d / 4, 256), D.T), dim3(256), 0, st, g.dm, g.wts, g.eidx, D.k, D.d, D.y,
+                       D.y_stride);
     return hipGetLastError();
 }
 

@@ -676,7 +676,7 @@ hipError_t launch_shape(const MxGemm& g, hipStream_t st)
         return hipGetLastError();
     }
     if (rows >= 192 && tiles(256, 256) >= 192) return launch_tile<Tile256, kT, kSwiglu, kMode>(g, st);
-    if (rows >= 96 && tiles(128, 128) >= 192) return launch_tile<Tile128, kT, kSwiglu, kMode>(g, st);
+    if (rows >= 48 && tiles(128, 128) >= 192) return launch_tile<Tile128, kT, kSwiglu, kMode>(g, st);
     return launch_tile<Tile64, kT, kSwiglu, kMode>(g, st);
 }
 
