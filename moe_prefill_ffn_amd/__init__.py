@@ -72,6 +72,10 @@ class moe_mxfp4_gemm_args_t(ctypes.Structure):
                 ("out", _vp), ("out_stride", _i64)]
 
 
+_DECODE_IO_SIZE = ctypes.sizeof(moe_decode_io_t)
+_MX_MATRIX_SIZE = ctypes.sizeof(moe_mxfp4_matrix_t)
+_MX_GEMM_SIZE = ctypes.sizeof(moe_mxfp4_gemm_args_t)
+
 MOE_F32, MOE_BF16, MOE_F16 = 0, 1, 2
 _DTYPE_ID = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
 MOE_DECODE_MAX_PAIRS = 1024
@@ -384,26 +388,33 @@ def moe_prefill_run_layer_noalloc(d_model: int, d_ff: int, n_experts: int, top_k
 
 # ---------------------------------------------------- a few tokens' layer ---
 
-def _stream_of(stream: Optional[torch.cuda.Stream], device: torch.device) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    if s.device_index != device.index:
-        raise ValueError(f"stream is on device {s.device_index}, the tensors are on {device}")
-    return s.cuda_stream
+# the raw handle of torch's current stream, without the Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _rows_of(t: torch.Tensor, name: str, rows: int, cols: int, device: torch.device) -> int:
-    """Row stride of a [rows, cols] device matrix whose rows are contiguous."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+def _stream_of(stream: Optional[torch.cuda.Stream], index: int) -> int:
+    if stream is None:
+        return _raw_stream(index)
+    if stream.device_index != index:
+        raise ValueError(f"stream is on device {stream.device_index}, the tensors are on device {index}")
+    return stream.cuda_stream
+
+
+def _rows_of(t: torch.Tensor, name: str, rows: int, cols: int, index: int) -> int:
+    """Row stride of a [rows, cols] matrix on device `index` whose rows are contiguous."""
+    if t.shape != (rows, cols):
         raise ValueError(f"{name}: expected shape ({rows}, {cols}), got {tuple(t.shape)}")
-    if not t.is_cuda or t.device != device:
-        raise TypeError(f"{name}: expected a tensor on {device}, got {t.device}")
-    if cols > 1 and t.stride(1) != 1:
+    if t.get_device() != index:
+        raise TypeError(f"{name}: expected a tensor on device {index}, got {t.device}")
+    stride, unit = t.stride()
+    if unit != 1 and cols > 1:
         raise ValueError(f"{name}: rows must be contiguous")
     if rows <= 1:
         return cols
-    if t.stride(0) < cols:
+    if stride < cols:
         raise ValueError(f"{name}: rows overlap")
-    return t.stride(0)
+    return stride
 
 
 def moe_decode_workspace_size(d_model: int, d_ff: int, n_experts: int, top_k: int, max_tokens: int) -> int:
@@ -427,86 +438,75 @@ def moe_decode_run_layer(handle: Handle, x: torch.Tensor, logits: torch.Tensor, 
     without one the call takes it from torch's allocator.  exports: "eidx" int32 and
     "weights" fp32, [T, top_k] each."""
     P = handle.params
-    d, E, k = P["d_model"], P["n_experts"], P["top_k"]
+    d, E, k, index = P["d_model"], P["n_experts"], P["top_k"], P["device"]
     T = x.shape[0]
-    if x.dtype not in _DTYPE_ID or y.dtype != x.dtype:
+    dtype = _DTYPE_ID.get(x.dtype)
+    if dtype is None or y.dtype != x.dtype:
         raise TypeError("x and y: expected the same of float32, bfloat16, float16")
     if logits.dtype != torch.float32:
         raise TypeError("logits: expected float32")
-    dev = x.device
-    if not x.is_cuda or dev.index != P["device"]:
-        raise TypeError(f"x: expected a tensor on the handle's device cuda:{P['device']}")
-    io = moe_decode_io_t()
-    io.struct_size = ctypes.sizeof(io)
-    io.layer = layer
-    io.n_tokens = T
-    io.dtype = _DTYPE_ID[x.dtype]
-    io.x_stride = _rows_of(x, "x", T, d, dev)
-    io.logits_stride = _rows_of(logits, "logits", T, E, dev)
-    io.y_stride = _rows_of(y, "y", T, d, dev)
-    io.x, io.logits, io.y = x.data_ptr(), logits.data_ptr(), y.data_ptr()
+    if x.get_device() != index:
+        raise TypeError(f"x: expected a tensor on the handle's device cuda:{index}")
+    x_stride = _rows_of(x, "x", T, d, index)
+    l_stride = _rows_of(logits, "logits", T, E, index)
+    y_stride = _rows_of(y, "y", T, d, index)
+    blob = None
     if layer < 0:
         if weights is None:
             raise ValueError("layer=-1 needs a resident weight blob")
-        if weights.device != dev:
-            raise TypeError(f"weights: expected a tensor on {dev}")
-        io.weights_dev = _dev_ptr(weights, torch.uint8, "weights", handle.layer_bytes)
-    for name, t in (exports or {}).items():
-        if name not in ("eidx", "weights"):
-            raise KeyError(name)
-        if t.device != dev:
-            raise TypeError(f"{name}: expected a tensor on {dev}")
-        setattr(io, name, _dev_ptr(t, torch.int32 if name == "eidx" else torch.float32, name, T * k))
-    s = _stream_of(stream, dev)
+        if weights.get_device() != index:
+            raise TypeError(f"weights: expected a tensor on device {index}")
+        blob = _dev_ptr(weights, torch.uint8, "weights", handle.layer_bytes)
+    raw = _stream_of(stream, index)
     if workspace is None:
         if 0 < T * k <= MOE_DECODE_MAX_PAIRS:
-            workspace = torch.empty(moe_decode_workspace_size(d, P["d_ff"], E, k, T), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(moe_decode_workspace_size(d, P["d_ff"], E, k, T), dtype=torch.uint8, device=x.device)
             if stream is not None:
                 workspace.record_stream(stream)
-    elif workspace.device != dev:
-        raise TypeError(f"workspace: expected a tensor on {dev}")
-    if workspace is not None:
-        io.workspace = _dev_ptr(workspace, torch.uint8, "workspace")
-        io.workspace_bytes = workspace.numel()
-    rc = lib().moe_decode_run_layer(handle.ptr, io, s)
+    elif workspace.get_device() != index:
+        raise TypeError(f"workspace: expected a tensor on device {index}")
+    ws, ws_bytes = (_dev_ptr(workspace, torch.uint8, "workspace"), workspace.numel()) if workspace is not None else (None, 0)
+    io = moe_decode_io_t(_DECODE_IO_SIZE, layer, blob, T, dtype, x.data_ptr(), x_stride, logits.data_ptr(), l_stride,
+                         y.data_ptr(), y_stride, ws, ws_bytes)
+    if exports:
+        for name, t in exports.items():
+            if name not in ("eidx", "weights"):
+                raise KeyError(name)
+            if t.get_device() != index:
+                raise TypeError(f"{name}: expected a tensor on device {index}")
+            setattr(io, name, _dev_ptr(t, torch.int32 if name == "eidx" else torch.float32, name, T * k))
+    rc = lib().moe_decode_run_layer(handle.ptr, io, raw)
     if rc:
         _check(rc, handle.ptr)
 
 
 # ----------------------------------------------------------------- MXFP4 ---
 
-def _mx_device(t: torch.Tensor, name: str) -> torch.device:
-    if not t.is_cuda:
+def _mx_device(t: torch.Tensor, name: str) -> int:
+    index = t.get_device()
+    if index < 0 or not t.is_cuda:
         raise TypeError(f"{name}: expected a device tensor")
-    return t.device
+    return index
 
 
-def _mx_bytes(t: torch.Tensor, name: str, shape, device) -> int:
+def _mx_bytes(t: torch.Tensor, name: str, shape, index: int) -> int:
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != torch.uint8 or t.device != device or not t.is_contiguous():
-        raise TypeError(f"{name}: expected a contiguous uint8 tensor on {device}")
+    if t.dtype != torch.uint8 or t.get_device() != index or not t.is_contiguous():
+        raise TypeError(f"{name}: expected a contiguous uint8 tensor on device {index}")
     return t.data_ptr()
 
 
-def _mx_matrix(values, codes, scales, dev) -> moe_mxfp4_matrix_t:
-    if values.dtype not in _DTYPE_ID:
+def _mx_matrix(values, codes, scales, M, K, index) -> moe_mxfp4_matrix_t:
+    dtype = _DTYPE_ID.get(values.dtype)
+    if dtype is None:
         raise TypeError("expected float32, bfloat16 or float16 values")
-    M, K = values.shape
-    m = moe_mxfp4_matrix_t()
-    m.struct_size = ctypes.sizeof(m)
-    m.device = dev.index
-    m.dtype = _DTYPE_ID[values.dtype]
-    m.M, m.K = M, K
-    m.stride = _rows_of(values, "values", M, K, dev)
-    m.values = values.data_ptr()
-    m.codes = _mx_bytes(codes, "codes", (M, K // 2), dev)
-    m.scales = _mx_bytes(scales, "scales", (M, K // 32), dev)
-    return m
+    return moe_mxfp4_matrix_t(_MX_MATRIX_SIZE, index, dtype, K, M, values.data_ptr(), _rows_of(values, "values", M, K, index),
+                              _mx_bytes(codes, "codes", (M, K // 2), index), _mx_bytes(scales, "scales", (M, K // 32), index))
 
 
-def _new(shape, dtype, dev, stream) -> torch.Tensor:
-    t = torch.empty(shape, dtype=dtype, device=dev)
+def _new(shape, dtype, index, stream) -> torch.Tensor:
+    t = torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
     if stream is not None:
         t.record_stream(stream)
     return t
@@ -516,16 +516,15 @@ def moe_mxfp4_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
                        scales: Optional[torch.Tensor] = None,
                        stream: Optional[torch.cuda.Stream] = None):
     """x [M, K] (fp32, bf16 or fp16; K a multiple of 32) -> MXFP4 (codes [M, K/2] uint8, scales [M, K/32] uint8)."""
-    dev = _mx_device(x, "x")
+    index = _mx_device(x, "x")
     if x.dim() != 2:
         raise ValueError("x: expected a matrix")
     M, K = x.shape
     if codes is None:
-        codes = _new((M, K // 2), torch.uint8, dev, stream)
+        codes = _new((M, K // 2), torch.uint8, index, stream)
     if scales is None:
-        scales = _new((M, K // 32), torch.uint8, dev, stream)
-    m = _mx_matrix(x, codes, scales, dev)
-    rc = lib().moe_mxfp4_quantize(m, _stream_of(stream, dev))
+        scales = _new((M, K // 32), torch.uint8, index, stream)
+    rc = lib().moe_mxfp4_quantize(_mx_matrix(x, codes, scales, M, K, index), _stream_of(stream, index))
     if rc:
         _check(rc)
     return codes, scales
@@ -535,16 +534,14 @@ def moe_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, out: Optiona
                          dtype: torch.dtype = torch.float32,
                          stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """MXFP4 (codes [M, K/2], scales [M, K/32]) -> values [M, K] in ``out`` (or a new tensor of ``dtype``)."""
-    dev = _mx_device(codes, "codes")
+    index = _mx_device(codes, "codes")
     if codes.dim() != 2:
         raise ValueError("codes: expected a matrix")
-    M, K = codes.shape[0], codes.shape[1] * 2
+    M, K = codes.shape
+    K *= 2
     if out is None:
-        out = _new((M, K), dtype, dev, stream)
-    elif out.dim() != 2 or tuple(out.shape) != (M, K):
-        raise ValueError(f"out: expected shape {(M, K)}, got {tuple(out.shape)}")
-    m = _mx_matrix(out, codes, scales, dev)
-    rc = lib().moe_mxfp4_dequantize(m, _stream_of(stream, dev))
+        out = _new((M, K), dtype, index, stream)
+    rc = lib().moe_mxfp4_dequantize(_mx_matrix(out, codes, scales, M, K, index), _stream_of(stream, index))
     if rc:
         _check(rc)
     return out
@@ -561,48 +558,40 @@ def moe_mxfp4_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch
     2N rows a group, gate then up.  bounds: int32 [G + 1], group g's rows of out; rows: int32 [M],
     src(r) = rows[r] // top_k (the row table moe_prefill_run_layer exports); without rows
     src(r) = r // top_k and M = A * top_k.  Rows of out in no group are left as they were."""
-    dev = _mx_device(a_codes, "a_codes")
-    if a_codes.dim() != 2 or b_codes.dim() not in (2, 3):
+    index = _mx_device(a_codes, "a_codes")
+    b_shape = b_codes.shape
+    if a_codes.dim() != 2 or len(b_shape) not in (2, 3):
         raise ValueError("a_codes: expected a matrix; b_codes: a matrix, or one per group")
     if top_k < 1:
         raise ValueError("top_k must be at least 1")
     A, K2 = a_codes.shape
     K = K2 * 2
-    G = b_codes.shape[0] if b_codes.dim() == 3 else 1
-    NB = b_codes.shape[-2]
+    G = b_shape[0] if len(b_shape) == 3 else 1
+    NB = b_shape[-2]
     if swiglu and NB % 2:
         raise ValueError("b_codes: swiglu needs gate and up rows, an even number")
     N = NB // 2 if swiglu else NB
     M = rows.shape[0] if rows is not None else A * top_k
     if out is None:
-        out = _new((M, N), dtype, dev, stream)
-    if out.dtype not in _DTYPE_ID:
+        out = _new((M, N), dtype, index, stream)
+    out_dtype = _DTYPE_ID.get(out.dtype)
+    if out_dtype is None:
         raise TypeError("out: expected float32, bfloat16 or float16")
     if bounds is None and G != 1:
         raise ValueError("b_codes of several groups need bounds")
-    if bounds is not None and (bounds.dim() != 1 or bounds.shape[0] != G + 1):
+    if bounds is not None and bounds.shape != (G + 1,):
         raise ValueError(f"bounds: expected shape ({G + 1},)")
     if rows is not None and rows.dim() != 1:
         raise ValueError("rows: expected a vector")
     for name, t in (("bounds", bounds), ("rows", rows)):
-        if t is not None and (t.device != dev or t.dtype != torch.int32 or not t.is_contiguous()):
-            raise TypeError(f"{name}: expected a contiguous int32 tensor on {dev}")
-    a = moe_mxfp4_gemm_args_t()
-    a.struct_size = ctypes.sizeof(a)
-    a.device = dev.index
-    a.a_codes = _mx_bytes(a_codes, "a_codes", (A, K2), dev)
-    a.a_scales = _mx_bytes(a_scales, "a_scales", (A, K // 32), dev)
-    a.a_rows = A
-    a.b_codes = _mx_bytes(b_codes, "b_codes", b_codes.shape[:-1] + (K2,), dev)
-    a.b_scales = _mx_bytes(b_scales, "b_scales", b_codes.shape[:-1] + (K // 32,), dev)
-    a.bounds = bounds.data_ptr() if bounds is not None else None
-    a.rows = rows.data_ptr() if rows is not None else None
-    a.n_groups, a.top_k, a.M, a.N, a.K = G, top_k, M, N, K
-    a.swiglu = 1 if swiglu else 0
-    a.dtype = _DTYPE_ID[out.dtype]
-    a.out_stride = _rows_of(out, "out", M, N, dev)
-    a.out = out.data_ptr()
-    rc = lib().moe_mxfp4_gemm(a, _stream_of(stream, dev))
+        if t is not None and (t.get_device() != index or t.dtype != torch.int32 or not t.is_contiguous()):
+            raise TypeError(f"{name}: expected a contiguous int32 tensor on device {index}")
+    a = moe_mxfp4_gemm_args_t(
+        _MX_GEMM_SIZE, index, _mx_bytes(a_codes, "a_codes", (A, K2), index), _mx_bytes(a_scales, "a_scales", (A, K // 32), index),
+        A, _mx_bytes(b_codes, "b_codes", (*b_shape[:-1], K2), index), _mx_bytes(b_scales, "b_scales", (*b_shape[:-1], K // 32), index),
+        bounds.data_ptr() if bounds is not None else None, rows.data_ptr() if rows is not None else None, G, top_k, M, N, K,
+        1 if swiglu else 0, out_dtype, out.data_ptr(), _rows_of(out, "out", M, N, index))
+    rc = lib().moe_mxfp4_gemm(a, _stream_of(stream, index))
     if rc:
         _check(rc)
     return out

@@ -160,12 +160,43 @@ struct Tile {
 };
 
 template <int BM>
+__device__ __forceinline__ Tile tile_of_group(const MxGemm& a, int g, int64_t slot)
+{
+    const int64_t b0 = a.bounds[g], b1 = a.bounds[g + 1];
+    int64_t m0 = b0 + (slot - (b0 / BM + g)) * BM, m1 = m0 + BM < b1 ? m0 + BM : b1;
+    // sound bounds ascend within [0, M]; this only keeps others from reaching outside
+    if (m0 < b0 || m0 < 0) m0 = m1;
+    if (m1 > a.M) m1 = a.M;
+    return {g, m0, m1};
+}
+template <int BM>
+__device__ __forceinline__ Tile tile_of_rows(const MxGemm& a, int64_t slot)
+{
+    const int64_t m0 = slot * BM;
+    return {0, m0, m0 + BM < a.M ? m0 + BM : a.M};
+}
+
+// The tile of a slot, by each lane for a slot of its own.
+template <int BM>
+__device__ __forceinline__ Tile tile_of_slot_lane(const MxGemm& a, int64_t slot)
+{
+    if (!a.bounds) return tile_of_rows<BM>(a, slot);
+    int lo = 0, hi = a.G - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((int64_t)(a.bounds[mid] / BM) + mid <= slot)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return tile_of_group<BM>(a, lo, slot);
+}
+
+// The tile of a slot, the same on all lanes, by the wave together.
+template <int BM>
 __device__ __forceinline__ Tile tile_of_slot(const MxGemm& a, int64_t slot)
 {
-    if (!a.bounds) {
-        const int64_t m0 = slot * BM;
-        return {0, m0, m0 + BM < a.M ? m0 + BM : a.M};
-    }
+    if (!a.bounds) return tile_of_rows<BM>(a, slot);
     // 64 groups are compared at a time, one per lane: two rounds of loads up to 4096 groups
     int g = 0, span = a.G;
     const int lane = threadIdx.x & 63;
@@ -177,13 +208,7 @@ __device__ __forceinline__ Tile tile_of_slot(const MxGemm& a, int64_t slot)
         g += skip;
         span = span - skip < step ? span - skip : step;
     }
-    g = __builtin_amdgcn_readfirstlane(g);
-    const int64_t b0 = a.bounds[g], b1 = a.bounds[g + 1];
-    int64_t m0 = b0 + (slot - (b0 / BM + g)) * BM, m1 = m0 + BM < b1 ? m0 + BM : b1;
-    // sound bounds ascend within [0, M]; this only keeps others from reaching outside
-    if (m0 < b0 || m0 < 0) m0 = m1;
-    if (m1 > a.M) m1 = a.M;
-    return {g, m0, m1};
+    return tile_of_group<BM>(a, __builtin_amdgcn_readfirstlane(g), slot);
 }
 
 // A row of the product reads this row of A.
@@ -203,7 +228,18 @@ __device__ __forceinline__ v16f mfma_fp4(v4i w, v4i x, v16f c, int sw, int sx)
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, x8, c, 4, 4, step, sw, step, sx);   // 4: E2M1
 }
 
-__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + exp_cw(-g)) * u; }
+// silu(g) u by the hardware's exp2 and reciprocal (an ulp each).  exp(-g) = 2^t (1 + ln2 r), t the
+// rounded -g log2(e) and r what the rounding left, so that a large |g| costs no bits.
+__device__ __forceinline__ float silu_mul(float g, float u)
+{
+    const float log2e = 0x1.715476p+0f, log2e_lo = 0x1.4ae0c0p-26f;   // the fp32 nearest log2(e), and the rest
+    const float t = -g * log2e;
+    const float r = __builtin_fmaf(-g, log2e, -t) - g * log2e_lo;
+    const float p = __builtin_amdgcn_exp2f(t);
+    // past the range of exp (p = 0 or infinity) there is nothing to correct
+    const float e = t > -126.0f && t < 128.0f ? __builtin_fmaf(p, 0x1.62e430p-1f * r, p) : p;
+    return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
+}
 
 // ------------------------------------------------------------- tiled kernel ---
 // Direct global->LDS loads, lane i's bytes at wave_base + size * i; inline asm so that the
@@ -246,6 +282,12 @@ struct MxShape {
 // bytes at any address.
 enum ScaleMode { kScale16, kScale4, kScale1 };
 
+constexpr int kListMost = 256;                            // tiles a workgroup lists at a time
+
+struct ListedTile {
+    int g, m0, m1, nt;
+};
+
 template <class S, int kMode>
 struct MxLds {
     static constexpr int kRowBytes = kMode == kScale16 ? 16 : kMode == kScale4 ? 8 : 12;
@@ -254,9 +296,16 @@ struct MxLds {
     static constexpr int kDataBytes = S::kRows * 128;
     static constexpr int kScaleBytes = NS * S::NW * kPerLoad;
     static constexpr int kScaleOff = 2 * kDataBytes;
-    static constexpr int kBytes = 2 * kDataBytes + 2 * kScaleBytes;
+    static constexpr int kRowsOff = kScaleOff + 2 * kScaleBytes;            // row indices of two tiles
+    static constexpr int kListOff = kRowsOff + 2 * S::BM * 4;
+    static constexpr int kBytes = kListOff + kListMost * (int)sizeof(ListedTile) + 16;
 };
 
+// Persistent workgroups: each takes every so-many-th tile of its XCD's run (workgroups go
+// round-robin over the 8 XCDs), one after the other without a pause in its stages -- the last two
+// stages of a tile issue the first two of the next, whose pointers are made under the products,
+// and the epilogue's stores drain under them.  (A workgroup a tile spent 14 us of 43 a tile of
+// 8192 x 4096 x 4096 on its start, its first loads and its stores.)
 template <class S, int kT, bool kSwiglu, int kMode>
 __global__ __launch_bounds__(64 * S::NW) void k_mx_tile(MxGemm a, int n_tiles, int64_t n_slots)
 {
@@ -265,134 +314,133 @@ __global__ __launch_bounds__(64 * S::NW) void k_mx_tile(MxGemm a, int n_tiles, i
     const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, j = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / S::WN, wn = wave % S::WN;
-
-    // Workgroups go round-robin over the 8 XCDs: XCD x takes a contiguous run of tiles, and
-    // inside a run bands of 8 slots by all column tiles, so that what an XCD runs at once
-    // shares rows of A and of B in its L2.
-    Tile t;
-    int nt;
-    {
-        const int64_t total = n_slots * n_tiles, per = (total + 7) >> 3;
-        const int64_t id = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
-        if ((blockIdx.x >> 3) >= per || id >= total) return;
-        const uint32_t band = (uint32_t)id / (uint32_t)(8 * n_tiles), first = band * 8;   // total < 2^31
-        const uint32_t high = n_slots - first < 8 ? (uint32_t)(n_slots - first) : 8;
-        const uint32_t in = (uint32_t)id - first * n_tiles;
-        nt = (int)(in / high);
-        t = tile_of_slot<S::BM>(a, first + in % high);
-    }
-    if (t.m0 >= t.m1) return;                             // uniform
-    const int nb = a.K / 32, nst = (nb + 7) >> 3;
+    const int nb = a.K / 32;
+    // at least two stages (a stage past the end of K adds 0): a stage issues the one two further,
+    // which is then in this tile or the next
+    const int nst = nb > 8 ? (nb + 7) >> 3 : 2;
     const int NB = kSwiglu ? 2 * a.N : a.N;
     constexpr int kOutCols = kSwiglu ? S::BN / 2 : S::BN;
-    const int n0 = nt * kOutCols;
+    int32_t* s_rows = reinterpret_cast<int32_t*>(lds + L::kRowsOff);
+    ListedTile* s_list = reinterpret_cast<ListedTile*>(lds + L::kListOff);
+    int* s_count = reinterpret_cast<int*>(lds + L::kListOff + kListMost * sizeof(ListedTile));
+    const uint32_t lds0 = lds_addr(lds);
 
-    // row q of the stage: rows of A, then rows of B (SwiGLU: 32 gate rows and their 32 up rows in turn)
-    auto src_row = [&](int q, bool& is_a) -> int64_t {
-        is_a = q < S::BM;
-        if (is_a) {
-            const int64_t r = t.m0 + q < t.m1 ? t.m0 + q : t.m1 - 1;
-            return a_row(a, r);
-        }
-        q -= S::BM;
-        int n = kSwiglu ? n0 + (q >> 6) * 32 + (q & 31) : n0 + q;
-        n = n < a.N ? n : a.N - 1;
-        if (kSwiglu && (q & 32)) n += a.N;
-        return (int64_t)t.g * NB + n;
-    };
-
-    const uint8_t* dsrc[S::NL];                           // this lane's row, per load
-    const int dchunk = lane & 7;                          // ... and slot in it
-    int dswz[S::NL];
-#pragma unroll
-    for (int l = 0; l < S::NL; ++l) {
-        const int q = (wave * S::NL + l) * 8 + (lane >> 3);
-        bool is_a;
-        const int64_t r = src_row(q, is_a);
-        dswz[l] = dchunk ^ swz(q);
-        dsrc[l] = (is_a ? a.a_codes : a.b_codes) + r * (a.K / 2);
-        if (kMode == kScale16) dsrc[l] += dswz[l] * 16;   // K is a multiple of 512: no clamp below
-    }
-    const uint8_t* ssrc[L::NS];                           // where this lane's scale loads start
-    const uint8_t* slast[L::NS];                          // kScale1: the last aligned word that holds one of the row's bytes
-#pragma unroll
-    for (int l = 0; l < L::NS; ++l) {
-        int i = (wave * L::NS + l) * 64 + lane;
-        constexpr int kParts = kMode == kScale16 ? 1 : L::kRowBytes / 4;
-        i = i < S::kRows * kParts ? i : 0;
-        const int q = i / kParts, part = i % kParts;
-        bool is_a;
-        const int64_t r = src_row(q, is_a);
-        const uint8_t* p = (is_a ? a.a_scales : a.b_scales) + r * nb;
-        if constexpr (kMode == kScale1) {
-            // a word that holds a valid byte lies in that byte's page
-            slast[l] = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(p + nb - 1) & ~(uintptr_t)3);
-            p = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)3);
-        } else {
-            slast[l] = p + nb - 4;
-        }
-        ssrc[l] = p + 4 * part;
-    }
+    const uint8_t* dsrc[S::NL];                           // this lane's row (kScale16: and chunk) per data load
+    const uint8_t* ssrc[L::NS];                           // where its scale loads start
+    const uint8_t* slast[L::NS];                          // the last word it may read there
     constexpr int kOps = S::TM + S::TN, kProd = S::TM * S::TN;
     const int sa_base = wm * S::TM * 32 + j, sb_base = S::BM + wn * S::TN * 32 + j;
     auto op_row = [&](int i) { return i < S::TM ? sa_base + i * 32 : sb_base + (i - S::TM) * 32; };
-    int mis[kOps];                                        // kScale1: where the row's first byte is in its word
-    if constexpr (kMode == kScale1) {
-#pragma unroll
-        for (int i = 0; i < kOps; ++i) {
-            bool is_a;
-            const int64_t r = src_row(op_row(i), is_a);
-            mis[i] = (int)(reinterpret_cast<uintptr_t>((is_a ? a.a_scales : a.b_scales) + r * nb) & 3);
-        }
-    }
+    int mis[kOps];                                        // kScale1: where an operand row's first byte is in its word
 
-    const uint32_t lds0 = lds_addr(lds);
-    // data load l of stage s (clamped: a load past the last stage repeats it) into slot s % 2
-    auto issue_data = [&](int l, int s) {
-        const uint32_t to = lds0 + (s & 1) * L::kDataBytes + (wave * S::NL + l) * 1024;
-        const int sc = s < nst ? s : nst - 1;
+    // row q of a stage of tile t: rows of A (indices in s_rows[buf]), then rows of B (SwiGLU: 32
+    // gate rows and their 32 up rows in turn)
+    auto src_row = [&](const ListedTile& t, int buf, int q, bool is_a) -> uint32_t {
+        if (is_a) {
+            const int last = t.m1 - 1 - t.m0;
+            const int at = q < last ? q : last;
+            int r = a.rows ? s_rows[buf * S::BM + at] : t.m0 + at;
+            if (a.row_div > 1) r /= a.row_div;
+            return (uint32_t)(r < 0 ? 0 : (r >= a.a_rows ? (int)(a.a_rows - 1) : r));
+        }
+        q -= S::BM;
+        int n = t.nt * kOutCols + (kSwiglu ? (q >> 6) * 32 + (q & 31) : q);
+        n = n < a.N ? n : a.N - 1;
+        if (kSwiglu && (q & 32)) n += a.N;
+        return (uint32_t)n;
+    };
+    auto point_data = [&](const ListedTile& t, int buf) {
+        const uint8_t* bc = a.b_codes + (int64_t)t.g * NB * (a.K / 2);
+        const uint8_t* bsc = a.b_scales + (int64_t)t.g * NB * nb;
+#pragma unroll
+        for (int l = 0; l < S::NL; ++l) {
+            const int q = (wave * S::NL + l) * 8 + (lane >> 3);
+            const bool is_a = (wave * S::NL + l) * 8 < S::BM;     // uniform: BM is a multiple of 8
+            const uint32_t r = src_row(t, buf, q, is_a);
+            dsrc[l] = (is_a ? a.a_codes : bc) + (uint64_t)r * (uint32_t)(a.K / 2);
+            if (kMode == kScale16) dsrc[l] += ((lane & 7) ^ swz(q)) * 16;   // K is a multiple of 512: no clamp below
+        }
+#pragma unroll
+        for (int l = 0; l < L::NS; ++l) {
+            int i = (wave * L::NS + l) * 64 + lane;
+            constexpr int kParts = kMode == kScale16 ? 1 : L::kRowBytes / 4;
+            i = i < S::kRows * kParts ? i : S::kRows * kParts - 1;     // the last rows are B's
+            const int q = i / kParts, part = i % kParts;
+            // uniform where a load's 64 or 32 rows lie on one side
+            const bool is_a = kMode == kScale1 ? q < S::BM : (wave * L::NS + l) * 64 / kParts < S::BM;
+            const uint32_t r = src_row(t, buf, q, is_a);
+            const uint8_t* p = (is_a ? a.a_scales : bsc) + (uint64_t)r * (uint32_t)nb;
+            if constexpr (kMode == kScale1) {
+                // a word that holds a valid byte lies in that byte's page
+                slast[l] = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(p + nb - 1) & ~(uintptr_t)3);
+                p = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)3);
+            } else {
+                slast[l] = p + nb - 4;
+            }
+            ssrc[l] = p + 4 * part;
+        }
+    };
+    auto point_mis = [&](const ListedTile& t, int buf) {
+        if constexpr (kMode == kScale1) {
+            const uint8_t* bsc = a.b_scales + (int64_t)t.g * NB * nb;
+#pragma unroll
+            for (int i = 0; i < kOps; ++i) {
+                const bool is_a = i < S::TM;
+                const uint32_t r = src_row(t, buf, op_row(i), is_a);
+                mis[i] = (int)((reinterpret_cast<uintptr_t>(is_a ? a.a_scales : bsc) + r * (uint32_t)nb) & 3);
+            }
+        }
+    };
+    // Stages are counted through a list's tiles; a stage sits in slot gs % 2 (kScale16: scales of
+    // the stages gs, gs + 1 of an even gs in buffer gs / 2 % 2; a tile then has an even number).
+    auto issue_data = [&](int l, int gs, int s) {
+        const uint32_t to = lds0 + (gs & 1) * L::kDataBytes + (wave * S::NL + l) * 1024;
         if constexpr (kMode == kScale16) {
-            g2lds16(dsrc[l] + sc * 128, to);
+            g2lds16(dsrc[l] + s * 128, to);
         } else {
-            const int c = sc * 8 + dswz[l];
+            const int q = (wave * S::NL + l) * 8 + (lane >> 3);
+            const int c = s * 8 + ((lane & 7) ^ swz(q));
             g2lds16(dsrc[l] + (c < nb ? c : nb - 1) * 16, to);
         }
     };
-    // scale load l of stage s (kScale16: of the stages s, s + 1 for an even s, buffer s / 2 % 2)
-    auto issue_scales = [&](int l, int s) {
-        const int sc = s < nst ? s : (kMode == kScale16 ? (nst - 1) & ~1 : nst - 1);
-        const int buf = kMode == kScale16 ? (s >> 1) & 1 : s & 1;
+    auto issue_scales = [&](int l, int gs, int s) {
+        const int buf = kMode == kScale16 ? (gs >> 1) & 1 : gs & 1;
         const uint32_t to = lds0 + L::kScaleOff + buf * L::kScaleBytes + (wave * L::NS + l) * L::kPerLoad;
-        const uint8_t* p = ssrc[l] + sc * 8;
+        const uint8_t* p = ssrc[l] + s * 8;
         if constexpr (kMode == kScale16) {
             g2lds16(p, to);
         } else {
             g2lds4(p < slast[l] ? p : slast[l], to);
         }
     };
+    // the row indices of tile t into s_rows[buf] (past its end: the last one again)
+    auto issue_rows = [&](const ListedTile& t, int buf) {
+        if (!a.rows || wave * 64 >= S::BM) return;
+        static_assert(S::BM <= 64 * S::NW, "one index a thread");
+        const int at = wave * 64 + lane, last = t.m1 - 1 - t.m0;
+        g2lds4(a.rows + t.m0 + (at < last ? at : last), lds0 + L::kRowsOff + (buf * S::BM + wave * 64) * 4);
+    };
 
-    // Operands of one step: tiles of the activations, then of the weights.  Tile rows are 32
-    // apart, so the swizzle is that of row j.
     struct Ops {
         v4i v[kOps];
     };
     struct Scales {
         int v[kOps];
     };
-    auto read_op = [&](int i, int s, int step, Ops& o) {
-        o.v[i] = *reinterpret_cast<const v4i*>(lds + (s & 1) * L::kDataBytes + op_row(i) * 128 +
+    auto read_op = [&](int i, int gs, int step, Ops& o) {
+        o.v[i] = *reinterpret_cast<const v4i*>(lds + (gs & 1) * L::kDataBytes + op_row(i) * 128 +
                                                (((4 * h + step) ^ swz(j)) << 4));
     };
     // the scale bytes of this lane half's four blocks of stage s: 0 past the end of K
-    auto read_scale = [&](int i, int s, Scales& o) {
+    auto read_scale = [&](int i, int gs, int s, Scales& o) {
         const uint8_t* base = lds + L::kScaleOff;
         if constexpr (kMode == kScale16) {
-            o.v[i] = *reinterpret_cast<const int*>(base + ((s >> 1) & 1) * L::kScaleBytes + op_row(i) * 16 + (s & 1) * 8 + 4 * h);
+            o.v[i] = *reinterpret_cast<const int*>(base + ((gs >> 1) & 1) * L::kScaleBytes + op_row(i) * 16 + (gs & 1) * 8 + 4 * h);
         } else if constexpr (kMode == kScale4) {
-            const int v = *reinterpret_cast<const int*>(base + (s & 1) * L::kScaleBytes + op_row(i) * 8 + 4 * h);
+            const int v = *reinterpret_cast<const int*>(base + (gs & 1) * L::kScaleBytes + op_row(i) * 8 + 4 * h);
             o.v[i] = 8 * s + 4 * h < nb ? v : 0;
         } else {
-            const uint32_t* p = reinterpret_cast<const uint32_t*>(base + (s & 1) * L::kScaleBytes + op_row(i) * 12 + 4 * h);
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(base + (gs & 1) * L::kScaleBytes + op_row(i) * 12 + 4 * h);
             const uint32_t v = __builtin_amdgcn_alignbyte(p[1], p[0], mis[i]);
             const int left = nb - (8 * s + 4 * h);
             o.v[i] = (int)(left >= 4 ? v : left <= 0 ? 0u : v & ((1u << (8 * left)) - 1u));
@@ -400,18 +448,14 @@ __global__ __launch_bounds__(64 * S::NW) void k_mx_tile(MxGemm a, int n_tiles, i
     };
 
     v16f acc[S::TM][S::TN];
+    auto clear = [&] {
 #pragma unroll
-    for (int i = 0; i < S::TM; ++i)
+        for (int i = 0; i < S::TM; ++i)
 #pragma unroll
-        for (int n = 0; n < S::TN; ++n)
+            for (int n = 0; n < S::TN; ++n)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) acc[i][n][e] = 0.0f;
-
-    // Stage s, four steps of kProd products.  Steps 0 and 1 read the operands of steps 1 to 3;
-    // then every wave has read its share of slot s % 2, and the barrier frees it for stage
-    // s + 2 and admits stage s + 1 (its loads, the only ones out, have had a stage's time).
-    // Step 2 issues the loads of stage s + 2, step 3 reads step 0 of stage s + 1.  Each memory
-    // instruction is placed behind a product of its own, in whose 32 cycles it issues.
+                for (int e = 0; e < 16; ++e) acc[i][n][e] = 0.0f;
+    };
     auto products = [&](auto step_c, const Ops& o, const Scales& sc, auto between) {
 #pragma unroll
         for (int i = 0; i < S::TM; ++i)
@@ -422,105 +466,216 @@ __global__ __launch_bounds__(64 * S::NW) void k_mx_tile(MxGemm a, int n_tiles, i
                 __builtin_amdgcn_sched_barrier(0);
             }
     };
-    Ops o0, o1, o2, o3;
-    Scales sc0, sc1;
-    auto stage = [&](int s) {
-        products(std::integral_constant<int, 0>{}, o0, sc0, [&](int at) {
-#pragma unroll
-            for (int i = at * 2 * kOps / kProd; i < (at + 1) * 2 * kOps / kProd; ++i) {
-                if (i < kOps)
-                    read_op(i, s, 1, o1);
-                else
-                    read_op(i - kOps, s, 2, o2);
-            }
-        });
-        products(std::integral_constant<int, 1>{}, o1, sc0, [&](int at) {
-#pragma unroll
-            for (int i = at * kOps / kProd; i < (at + 1) * kOps / kProd; ++i) read_op(i, s, 3, o3);
-        });
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        products(std::integral_constant<int, 2>{}, o2, sc0, [&](int at) {
-            if (kMode != kScale16 || (s & 1) == 0) {
-#pragma unroll
-                for (int l = at * L::NS / kProd; l < (at + 1) * L::NS / kProd; ++l) issue_scales(l, s + 2);
-            }
-#pragma unroll
-            for (int l = at * S::NL / kProd; l < (at + 1) * S::NL / kProd; ++l) issue_data(l, s + 2);
-        });
-        products(std::integral_constant<int, 3>{}, o3, sc0, [&](int at) {
-            // past the last stage: a repeated one, not used
-#pragma unroll
-            for (int i = at * kOps / kProd; i < (at + 1) * kOps / kProd; ++i) {
-                read_op(i, s + 1, 0, o0);
-                read_scale(i, s + 1, sc1);
-            }
-        });
-    };
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        if (kMode != kScale16 || u == 0) {
-#pragma unroll
-            for (int l = 0; l < L::NS; ++l) issue_scales(l, u);
-        }
-#pragma unroll
-        for (int l = 0; l < S::NL; ++l) issue_data(l, u);
-    }
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(S::NL + (kMode == kScale16 ? 0 : L::NS)) : "memory");
-#pragma unroll
-    for (int i = 0; i < kOps; ++i) {
-        read_op(i, 0, 0, o0);
-        read_scale(i, 0, sc0);
-    }
-    for (int s = 0; s < nst; ++s) {
-        stage(s);
-        sc0 = sc1;
-    }
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");   // the slots are dead: the epilogue takes them
 
-    // Epilogue: each wave turns its tile, 32 rows at a time, through LDS of its own into
-    // row-major order and writes 16 bytes a lane, whole runs of a row at a time.
+    // Stores straight from the result registers.  A lane holds 4 consecutive columns of row j per
+    // register quad g: columns 8 g + 4 h.  Exchanges between lanes make 16 bytes a lane and 64
+    // consecutive bytes a row of them (32 at a time took the L2 twice the requests): of 16-bit
+    // types quads 2 p and 2 p + 1 between the lane halves (each then has 8 columns, of quad
+    // 2 p + h), and of all types two such vectors between lanes 16 apart, so that the first store
+    // takes rows 0-15 of the tile and the second rows 16-31, lane group j / 16 the first or the
+    // second vector.
     typedef typename Elem<kT>::type T;
-    constexpr int kCols = (kSwiglu ? S::TN / 2 : S::TN) * 32;
-    constexpr int kStride = kCols * (int)sizeof(T) + 16;
-    constexpr int kVec = 16 / (int)sizeof(T), kLanes = kCols / kVec;   // lanes a row
-    static_assert(32 * kStride * S::NW <= L::kBytes, "the waves' turning space fits the ring");
-    static_assert(64 % kLanes == 0, "whole rows a pass");
-    uint8_t* mine = lds + wave * 32 * kStride;
-    const int c0 = n0 + wn * kCols;
-    const bool vec = (reinterpret_cast<uintptr_t>(a.out) | (uint64_t)(a.out_stride * (int64_t)sizeof(T))) % 16 == 0;
+    constexpr int kVec = 16 / (int)sizeof(T), kTiles = kSwiglu ? S::TN / 2 : S::TN;
+    constexpr int kStores = S::TM * kTiles * (sizeof(T) == 4 ? 4 : 2);
+    const bool vec = (reinterpret_cast<uintptr_t>(a.out) | (uint64_t)(a.out_stride * (int64_t)sizeof(T))) % 16 == 0 &&
+                     a.N % kVec == 0;
+    auto value = [&](int i, int n, int x) -> float {
+        if constexpr (kSwiglu)
+            return silu_mul(acc[i][2 * n][x], acc[i][2 * n + 1][x]);
+        else
+            return acc[i][n][x];
+    };
+    // vector p of tile (i, n): fp32 quad p, 16-bit quads 2 p and 2 p + 1
+    auto vector = [&](int i, int n, int p, uint32_t(&w)[4]) {
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < S::TM; ++i) {
+            for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(value(i, n, 4 * p + e));
+        } else {
+            typedef T T2 __attribute__((ext_vector_type(2)));
+            uint32_t q[2][2];
 #pragma unroll
-        for (int n = 0; n < (kSwiglu ? S::TN / 2 : S::TN); ++n)
+            for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                float v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if constexpr (kSwiglu)
-                        v[e] = silu_mul(acc[i][2 * n][4 * g + e], acc[i][2 * n + 1][4 * g + e]);
-                    else
-                        v[e] = acc[i][n][4 * g + e];
+                for (int e = 0; e < 2; ++e) {
+                    const T2 v = {from_f32<kT>(value(i, n, 4 * (2 * p + b) + 2 * e)),
+                                  from_f32<kT>(value(i, n, 4 * (2 * p + b) + 2 * e + 1))};
+                    q[b][e] = __builtin_bit_cast(uint32_t, v);
                 }
-                store_n<kT, 4>(mine + j * kStride + (n * 32 + 8 * g + 4 * h) * sizeof(T), v);
-            }
-        __builtin_amdgcn_wave_barrier();
+            const auto s0 = __builtin_amdgcn_permlane32_swap(q[0][0], q[1][0], false, false);
+            const auto s1 = __builtin_amdgcn_permlane32_swap(q[0][1], q[1][1], false, false);
+            w[0] = s0[0], w[1] = s1[0], w[2] = s0[1], w[3] = s1[1];
+        }
+    };
+    auto store_tile = [&](const ListedTile& t, auto whole_c) {
+        constexpr bool kWhole = decltype(whole_c)::value;  // every row and column of the tile exists
 #pragma unroll
-        for (int p = 0; p < 32 * kLanes / 64; ++p) {
-            const int row = p * (64 / kLanes) + lane / kLanes, col = (lane % kLanes) * kVec;
-            const int64_t r = t.m0 + (wm * S::TM + i) * 32 + row;
-            const uint8_t* from = mine + row * kStride + col * sizeof(T);
-            if (r < t.m1 && c0 + col < a.N) {
-                T* o = static_cast<T*>(a.out) + r * a.out_stride + c0 + col;
-                if (vec && c0 + col + kVec <= a.N) {
-                    *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(from);
-                } else {
-                    const T* f = reinterpret_cast<const T*>(from);
-                    for (int e = 0; e < kVec && c0 + col + e < a.N; ++e) o[e] = f[e];
+        for (int i = 0; i < S::TM; ++i) {
+#pragma unroll
+            for (int n = 0; n < kTiles; ++n) {
+                const int64_t r0 = t.m0 + (wm * S::TM + i) * 32 + (j & 15);
+                const int c0 = t.nt * kOutCols + (wn * kTiles + n) * 32 + kVec * h + (j >> 4) * 2 * kVec;
+                T* o = static_cast<T*>(a.out) + r0 * a.out_stride + c0;
+#pragma unroll
+                for (int p = 0; p < (sizeof(T) == 4 ? 4 : 2); p += 2) {
+                    uint32_t w[2][4];
+                    vector(i, n, p, w[0]);
+                    vector(i, n, p + 1, w[1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const auto x = __builtin_amdgcn_permlane16_swap(w[0][e], w[1][e], false, false);
+                        w[0][e] = x[0];
+                        w[1][e] = x[1];
+                    }
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const uint4 v = {w[q][0], w[q][1], w[q][2], w[q][3]};
+                        const int c = c0 + 2 * kVec * p;
+                        T* at = o + 16 * q * a.out_stride + 2 * kVec * p;
+                        if (kWhole || (vec && r0 + 16 * q < t.m1 && c < a.N)) {
+                            *reinterpret_cast<uint4*>(at) = v;
+                        } else if (r0 + 16 * q < t.m1) {
+#pragma unroll
+                            for (int e = 0; e < kVec; ++e) {
+                                if (c + e >= a.N) break;
+                                if constexpr (sizeof(T) == 4)
+                                    at[e] = __uint_as_float(w[q][e]);
+                                else
+                                    at[e] = __builtin_bit_cast(T, (uint16_t)(w[q][e >> 1] >> (16 * (e & 1))));
+                            }
+                        }
+                    }
                 }
             }
         }
-        __builtin_amdgcn_wave_barrier();
+    };
+
+    // this workgroup's tiles: bands of 8 slots by all column tiles, so that what an XCD runs at
+    // once shares rows of A and of B in its L2
+    const int64_t total = n_slots * n_tiles, per = (total + 7) >> 3;
+    const int64_t run0 = (int64_t)(blockIdx.x & 7) * per, run1 = run0 + per < total ? run0 + per : total;
+    const int nq = gridDim.x >> 3;
+    for (int64_t list0 = run0 + (blockIdx.x >> 3); list0 < run1; list0 += (int64_t)nq * kListMost) {
+        // list the next kListMost tiles that hold rows
+        __syncthreads();                                  // the previous list is done
+        if (tid == 0) *s_count = 0;
+        __syncthreads();
+#pragma unroll 1
+        for (int w0 = 0; w0 < kListMost; w0 += 64) {      // wave 0: in order
+            if (wave != 0) break;
+            const int64_t id = list0 + (int64_t)(w0 + lane) * nq;
+            ListedTile t = {0, 0, 0, 0};
+            if (id < run1) {
+                const uint32_t band = (uint32_t)id / (uint32_t)(8 * n_tiles), first = band * 8;   // total < 2^31
+                const uint32_t high = n_slots - first < 8 ? (uint32_t)(n_slots - first) : 8;
+                const uint32_t in = (uint32_t)id - first * n_tiles;
+                const Tile f = tile_of_slot_lane<S::BM>(a, first + in % high);
+                t = {f.g, (int)f.m0, (int)(f.m0 < f.m1 ? f.m1 : f.m0), (int)(in / high)};
+            }
+            const bool keep = t.m0 < t.m1;
+            const uint64_t mask = __ballot(keep);
+            const int base = *s_count;
+            if (keep) s_list[base + __popcll(mask & ((1ull << lane) - 1))] = t;
+            if (lane == 0) *s_count = base + __popcll(mask);
+        }
+        __syncthreads();
+        const int count = *s_count;
+        if (count == 0) continue;                         // uniform
+        auto listed = [&](int i) -> ListedTile {
+            const ListedTile t = s_list[i < count ? i : count - 1];
+            return {__builtin_amdgcn_readfirstlane(t.g), __builtin_amdgcn_readfirstlane(t.m0),
+                    __builtin_amdgcn_readfirstlane(t.m1), __builtin_amdgcn_readfirstlane(t.nt)};
+        };
+        ListedTile cur = listed(0);
+        issue_rows(cur, 0);
+        issue_rows(listed(1), 1);
+        asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+        point_data(cur, 0);
+        point_mis(cur, 0);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if (kMode != kScale16 || u == 0) {
+#pragma unroll
+                for (int l = 0; l < L::NS; ++l) issue_scales(l, u, u);
+            }
+#pragma unroll
+            for (int l = 0; l < S::NL; ++l) issue_data(l, u, u);
+        }
+        asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+        Ops o0, o1, o2, o3;
+        Scales sc0, sc1;
+#pragma unroll
+        for (int i = 0; i < kOps; ++i) {
+            read_op(i, 0, 0, o0);
+            read_scale(i, 0, 0, sc0);
+        }
+        clear();
+        int gs = 0;
+        bool stored = false;                              // the last tile's kStores stores are out, nothing else behind the loads
+        for (int ti = 0; ti < count; ++ti) {
+            ListedTile next = cur;
+            for (int s = 0; s < nst; ++s, ++gs) {
+                // Stage gs, four steps of kProd products.  Steps 0 and 1 read the operands of steps 1
+                // to 3; then every wave has read its share of slot gs % 2, and the barrier frees it for
+                // stage gs + 2 and admits stage gs + 1 (its loads, the only ones out but for stores,
+                // have had a stage's time).  Step 2 issues the loads of stage gs + 2, step 3 reads step
+                // 0 of stage gs + 1.  Each memory instruction is placed behind a product of its own, in
+                // whose 32 cycles it issues.
+                products(std::integral_constant<int, 0>{}, o0, sc0, [&](int at) {
+#pragma unroll
+                    for (int i = at * 2 * kOps / kProd; i < (at + 1) * 2 * kOps / kProd; ++i) {
+                        if (i < kOps)
+                            read_op(i, gs, 1, o1);
+                        else
+                            read_op(i - kOps, gs, 2, o2);
+                    }
+                });
+                products(std::integral_constant<int, 1>{}, o1, sc0, [&](int at) {
+#pragma unroll
+                    for (int i = at * kOps / kProd; i < (at + 1) * kOps / kProd; ++i) read_op(i, gs, 3, o3);
+                });
+                if (stored) {
+                    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kStores < 63 ? kStores : 63) : "memory");
+                    stored = false;
+                } else {
+                    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                }
+                // past the list's last tile: its first stages again, not used
+                const int s2 = s + 2 < nst ? s + 2 : s + 2 - nst;
+                if (s + 2 == nst && ti + 1 < count) {     // this tile's loads are all issued: on to the next
+                    next = listed(ti + 1);
+                    point_data(next, (ti + 1) & 1);
+                    if (ti + 2 < count) issue_rows(listed(ti + 2), ti & 1);   // its buffer: this tile's, pointed long ago
+                }
+                products(std::integral_constant<int, 2>{}, o2, sc0, [&](int at) {
+                    if (at == 0 && (kMode != kScale16 || (s & 1) == 0)) {
+#pragma unroll
+                        for (int l = 0; l < L::NS; ++l) issue_scales(l, gs + 2, s2);
+                    }
+#pragma unroll
+                    for (int l = at * S::NL / kProd; l < (at + 1) * S::NL / kProd; ++l) issue_data(l, gs + 2, s2);
+                });
+                const bool last = s + 1 == nst;
+                if (last && ti + 1 < count) point_mis(next, (ti + 1) & 1);
+                products(std::integral_constant<int, 3>{}, o3, sc0, [&](int at) {
+                    // past the list's last stage: an old one, not used
+#pragma unroll
+                    for (int i = at * kOps / kProd; i < (at + 1) * kOps / kProd; ++i) {
+                        read_op(i, gs + 1, 0, o0);
+                        read_scale(i, gs + 1, last ? 0 : s + 1, sc1);
+                    }
+                });
+                sc0 = sc1;
+            }
+            const bool whole = vec && cur.m0 + S::BM <= cur.m1 && (cur.nt + 1) * kOutCols <= a.N;   // uniform
+            if (whole)
+                store_tile(cur, std::true_type{});
+            else
+                store_tile(cur, std::false_type{});
+            stored = whole;
+            clear();
+            cur = next;
+        }
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     }
 }
 
@@ -660,8 +815,11 @@ hipError_t launch_tile(const MxGemm& g, hipStream_t st)
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_mx_tile<S, kT, kSwiglu, kMode>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_mx_tile<S, kT, kSwiglu, kMode>), dim3(8 * nblk(total, 8)), dim3(64 * S::NW), lds, st, g,
-                       n_tiles, slots);
+    // as many workgroups as the chip holds at once: 256 CUs, 160 KiB of LDS each
+    constexpr int kGrid = 256 * (163840 / lds);
+    const unsigned grid = 8 * nblk(total, 8);
+    hipLaunchKernelGGL((k_mx_tile<S, kT, kSwiglu, kMode>), dim3(grid < (unsigned)kGrid ? grid : (unsigned)kGrid), dim3(64 * S::NW), lds,
+                       st, g, n_tiles, slots);
     return hipGetLastError();
 }
 

@@ -9,6 +9,7 @@
 
 #include <algorithm>
 #include <array>
+#include <atomic>
 #include <chrono>
 #include <mutex>
 #include <string>
@@ -138,7 +139,8 @@ struct DevGuard {
     explicit DevGuard(int d)
     {
         if (hipGetDevice(&prev) != hipSuccess) prev = -1;
-        (void)hipSetDevice(d);
+        if (prev == d) prev = -1;                        // current already: nothing to set or restore
+        else (void)hipSetDevice(d);
     }
     ~DevGuard()
     {
@@ -304,11 +306,13 @@ hipError_t export_copies(const moe_layer_io_t& io, const uint8_t* ws, const WsLa
     return hipSuccess;
 }
 
-// The allocation-free entry point's device check (gfx950), once per device.
+// The handle-free entry points' device check (gfx950), once per device.
 int noalloc_device_ok(int dev)
 {
     static std::mutex mu;
     static std::vector<signed char> ok;                  // -1 unknown, 0 refused, 1 accepted
+    static std::atomic<bool> accepted[64];               // the devices found good, without the lock
+    if (dev >= 0 && dev < 64 && accepted[dev].load(std::memory_order_acquire)) return MOE_OK;
     std::lock_guard<std::mutex> lock(mu);
     int ndev = 0;
     if (hipGetDeviceCount(&ndev) != hipSuccess || ndev < 1) return fail(nullptr, MOE_EUNSUPPORTED, "no HIP device");
@@ -321,6 +325,7 @@ int noalloc_device_ok(int dev)
         ok[dev] = strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : 0;
     }
     if (!ok[dev]) return fail(nullptr, MOE_EUNSUPPORTED, "device is not gfx950");
+    if (dev < 64) accepted[dev].store(true, std::memory_order_release);
     return MOE_OK;
 }
 

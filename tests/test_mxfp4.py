@@ -193,7 +193,7 @@ def test_dense_product(M, N, K, dtype, swiglu):
 @gpu
 @pytest.mark.parametrize("K", [128, 384, 480, 512, 1536])  # scale rows 16-byte aligned, 4-byte aligned, and not
 @pytest.mark.parametrize("swiglu,dtype", [(False, torch.bfloat16), (True, torch.float32), (False, torch.float32)])
-@pytest.mark.parametrize("M,N", [(3500, 3600), (1200, 2500), (4100, 1030)])
+@pytest.mark.parametrize("M,N", [(3500, 3600), (1200, 2500), (4100, 1030), (5000, 7000)])
 def test_large_products_take_the_wider_tiles(M, N, K, swiglu, dtype):
     """Row and column counts of no tile's multiple, at which each of the wider tiles is chosen."""
     g = gen(M + N + K)
