@@ -357,7 +357,7 @@ typedef struct moe_mxfp4_gemm_args {
     int32_t n_groups;          /* 1..65535 (1 if dense) */
     int32_t top_k;             /* >= 1 */
     int64_t M;                 /* rows of out, >= 0 (0 is a no-op), < 2^31 */
-    int32_t N, K;              /* N >= 1, K a multiple of 32, >= 32 */
+    int32_t N, K;              /* N in 1..2^20, K a multiple of 32 in 32..2^20 */
     int32_t swiglu;            /* 0 or 1 */
     int32_t dtype;             /* type of out */
     void* out;                 /* device [M, N], rows out_stride elements apart */

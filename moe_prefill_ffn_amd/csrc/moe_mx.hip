@@ -253,6 +253,11 @@ __device__ __forceinline__ void g2lds16(const void* g, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(lds) : "memory", "m0");
 }
+// the same from a wave-uniform base and 32 bits of offset a lane
+__device__ __forceinline__ void g2lds16_at(const uint8_t* base, uint32_t off, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory", "m0");
+}
 __device__ __forceinline__ void g2lds4(const void* g, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(lds) : "memory", "m0");
@@ -273,8 +278,9 @@ template <int WM_, int WN_, int TM_, int TN_>
 struct MxShape {
     static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_;
     static constexpr int NW = WM * WN, BM = 32 * WM * TM, BN = 32 * WN * TN, kRows = BM + BN;
-    static constexpr int NL = kRows / 8 / NW;             // 1 KiB data loads per wave and stage
-    static_assert(NL * NW * 8 == kRows, "whole loads");
+    // 1 KiB data loads per wave and stage: of A's rows, of B's
+    static constexpr int NLA = BM / 8 / NW, NLB = BN / 8 / NW, NL = NLA + NLB;
+    static_assert(NLA * NW * 8 == BM && NLB * NW * 8 == BN, "whole loads");
 };
 
 // How the scale bytes come in, by the alignment of the rows of both scale matrices: 16 bytes
@@ -325,51 +331,59 @@ __global__ __launch_bounds__(64 * S::NW) void k_mx_tile(MxGemm a, int n_tiles, i
     int* s_count = reinterpret_cast<int*>(lds + L::kListOff + kListMost * sizeof(ListedTile));
     const uint32_t lds0 = lds_addr(lds);
 
-    const uint8_t* dsrc[S::NL];                           // this lane's row (kScale16: and chunk) per data load
-    const uint8_t* ssrc[L::NS];                           // where its scale loads start
+    // Data: a base per operand and tile, an offset per lane and load (kScale16: to its chunk, else
+    // to its row).  32 bits of offset: a tile's rows of B span at most BN K / 2 bytes, A's at most
+    // what the host checked.
+    const uint8_t* a_at;
+    const uint8_t* b_at;
+    uint32_t dofs[S::NL];
+    const uint8_t* ssrc[L::NS];                           // where this lane's scale loads start
     const uint8_t* slast[L::NS];                          // the last word it may read there
     constexpr int kOps = S::TM + S::TN, kProd = S::TM * S::TN;
     const int sa_base = wm * S::TM * 32 + j, sb_base = S::BM + wn * S::TN * 32 + j;
     auto op_row = [&](int i) { return i < S::TM ? sa_base + i * 32 : sb_base + (i - S::TM) * 32; };
     int mis[kOps];                                        // kScale1: where an operand row's first byte is in its word
 
-    // row q of a stage of tile t: rows of A (indices in s_rows[buf]), then rows of B (SwiGLU: 32
-    // gate rows and their 32 up rows in turn)
-    auto src_row = [&](const ListedTile& t, int buf, int q, bool is_a) -> uint32_t {
-        if (is_a) {
-            const int last = t.m1 - 1 - t.m0;
-            const int at = q < last ? q : last;
-            int r = a.rows ? s_rows[buf * S::BM + at] : t.m0 + at;
-            if (a.row_div > 1) r /= a.row_div;
-            return (uint32_t)(r < 0 ? 0 : (r >= a.a_rows ? (int)(a.a_rows - 1) : r));
-        }
-        q -= S::BM;
-        int n = t.nt * kOutCols + (kSwiglu ? (q >> 6) * 32 + (q & 31) : q);
-        n = n < a.N ? n : a.N - 1;
-        if (kSwiglu && (q & 32)) n += a.N;
-        return (uint32_t)n;
+    // row q of tile t's rows of A, relative to a_at's row: from the row table (indices in
+    // s_rows[buf]) relative to A, else to the tile's first
+    const bool by_table = a.rows != nullptr || a.row_div > 1;
+    auto a_ofs = [&](const ListedTile& t, int buf, int q) -> uint32_t {
+        const int last = t.m1 - 1 - t.m0, at = q < last ? q : last;
+        if (!by_table) return (uint32_t)at;
+        int r = a.rows ? s_rows[buf * S::BM + at] : t.m0 + at;
+        if (a.row_div > 1) r /= a.row_div;
+        return (uint32_t)(r < 0 ? 0 : (r >= a.a_rows ? (int)(a.a_rows - 1) : r));
     };
+    auto a_first = [&](const ListedTile& t) -> int64_t { return by_table ? 0 : t.m0; };
+    // row q of its rows of B, relative to the tile's first (SwiGLU: 32 gate rows and their 32 up
+    // rows in turn, the up rows relative to the first up row)
+    auto b_ofs = [&](const ListedTile& t, int q) -> uint32_t {
+        const int n = kSwiglu ? (q >> 6) * 32 + (q & 31) : q, last = a.N - 1 - t.nt * kOutCols;
+        return (uint32_t)(n < last ? n : last);
+    };
+    auto b_first = [&](const ListedTile& t) -> int64_t { return (int64_t)t.g * NB + t.nt * kOutCols; };
+    const int64_t up = kSwiglu ? (int64_t)a.N * (a.K / 2) : 0;      // bytes from a gate row to its up row
     auto point_data = [&](const ListedTile& t, int buf) {
-        const uint8_t* bc = a.b_codes + (int64_t)t.g * NB * (a.K / 2);
-        const uint8_t* bsc = a.b_scales + (int64_t)t.g * NB * nb;
+        a_at = a.a_codes + a_first(t) * (a.K / 2);
+        b_at = a.b_codes + b_first(t) * (a.K / 2);
+        const uint32_t half = (uint32_t)(a.K / 2);
 #pragma unroll
         for (int l = 0; l < S::NL; ++l) {
-            const int q = (wave * S::NL + l) * 8 + (lane >> 3);
-            const bool is_a = (wave * S::NL + l) * 8 < S::BM;     // uniform: BM is a multiple of 8
-            const uint32_t r = src_row(t, buf, q, is_a);
-            dsrc[l] = (is_a ? a.a_codes : bc) + (uint64_t)r * (uint32_t)(a.K / 2);
-            if (kMode == kScale16) dsrc[l] += ((lane & 7) ^ swz(q)) * 16;   // K is a multiple of 512: no clamp below
+            const bool is_a = l < S::NLA;
+            const int q = (is_a ? wave * S::NLA + l : wave * S::NLB + l - S::NLA) * 8 + (lane >> 3);
+            dofs[l] = (is_a ? a_ofs(t, buf, q) : b_ofs(t, q)) * half;
+            if (kMode == kScale16) dofs[l] += ((lane & 7) ^ swz(q)) * 16;   // K is a multiple of 512: no clamp below
         }
 #pragma unroll
         for (int l = 0; l < L::NS; ++l) {
             int i = (wave * L::NS + l) * 64 + lane;
             constexpr int kParts = kMode == kScale16 ? 1 : L::kRowBytes / 4;
             i = i < S::kRows * kParts ? i : S::kRows * kParts - 1;     // the last rows are B's
-            const int q = i / kParts, part = i % kParts;
+            const int q = i / kParts, part = i % kParts, qb = q - S::BM;
             // uniform where a load's 64 or 32 rows lie on one side
             const bool is_a = kMode == kScale1 ? q < S::BM : (wave * L::NS + l) * 64 / kParts < S::BM;
-            const uint32_t r = src_row(t, buf, q, is_a);
-            const uint8_t* p = (is_a ? a.a_scales : bsc) + (uint64_t)r * (uint32_t)nb;
+            const uint8_t* p = is_a ? a.a_scales + (a_first(t) + a_ofs(t, buf, q)) * nb
+                                    : a.b_scales + (b_first(t) + b_ofs(t, qb) + (kSwiglu && (qb & 32) ? a.N : 0)) * nb;
             if constexpr (kMode == kScale1) {
                 // a word that holds a valid byte lies in that byte's page
                 slast[l] = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(p + nb - 1) & ~(uintptr_t)3);
@@ -382,25 +396,27 @@ __global__ __launch_bounds__(64 * S::NW) void k_mx_tile(MxGemm a, int n_tiles, i
     };
     auto point_mis = [&](const ListedTile& t, int buf) {
         if constexpr (kMode == kScale1) {
-            const uint8_t* bsc = a.b_scales + (int64_t)t.g * NB * nb;
 #pragma unroll
             for (int i = 0; i < kOps; ++i) {
-                const bool is_a = i < S::TM;
-                const uint32_t r = src_row(t, buf, op_row(i), is_a);
-                mis[i] = (int)((reinterpret_cast<uintptr_t>(is_a ? a.a_scales : bsc) + r * (uint32_t)nb) & 3);
+                const int q = op_row(i), qb = q - S::BM;
+                const int64_t r = i < S::TM ? a_first(t) + a_ofs(t, buf, q) : b_first(t) + b_ofs(t, qb) + (kSwiglu && (qb & 32) ? a.N : 0);
+                mis[i] = (int)((reinterpret_cast<uintptr_t>(i < S::TM ? a.a_scales : a.b_scales) + (uintptr_t)(r * nb)) & 3);
             }
         }
     };
     // Stages are counted through a list's tiles; a stage sits in slot gs % 2 (kScale16: scales of
     // the stages gs, gs + 1 of an even gs in buffer gs / 2 % 2; a tile then has an even number).
     auto issue_data = [&](int l, int gs, int s) {
-        const uint32_t to = lds0 + (gs & 1) * L::kDataBytes + (wave * S::NL + l) * 1024;
+        const bool is_a = l < S::NLA;
+        const int ql = is_a ? wave * S::NLA + l : wave * S::NLB + l - S::NLA;       // load of the operand: 8 rows
+        const uint32_t to = lds0 + (gs & 1) * L::kDataBytes + ((is_a ? 0 : S::BM / 8) + ql) * 1024;
+        const uint8_t* base = (is_a ? a_at : b_at + (kSwiglu && (ql & 4) ? up : 0)) + s * 128;
         if constexpr (kMode == kScale16) {
-            g2lds16(dsrc[l] + s * 128, to);
+            g2lds16_at(base, dofs[l], to);
         } else {
-            const int q = (wave * S::NL + l) * 8 + (lane >> 3);
-            const int c = s * 8 + ((lane & 7) ^ swz(q));
-            g2lds16(dsrc[l] + (c < nb ? c : nb - 1) * 16, to);
+            const int q = ql * 8 + (lane >> 3), c = (lane & 7) ^ swz(q), left = nb - 1 - s * 8;
+            // past the end of K: the last block again; a stage past it altogether starts before its base
+            g2lds16(base + dofs[l] + (int64_t)(c < left ? c : left) * 16, to);
         }
     };
     auto issue_scales = [&](int l, int gs, int s) {
@@ -544,6 +560,7 @@ __global__ __launch_bounds__(64 * S::NW) void k_mx_tile(MxGemm a, int n_tiles, i
                             }
                         }
                     }
+                    __builtin_amdgcn_sched_barrier(0);    // two vectors at a time in registers
                 }
             }
         }
@@ -827,8 +844,10 @@ template <int kT, bool kSwiglu, int kMode>
 hipError_t launch_shape(const MxGemm& g, hipStream_t st)
 {
     const int64_t rows = g.M / g.G;       // rows a group has on average
+    // the tiled kernel reaches A through the row table by 32 bits of offset
+    const bool far = (g.rows || g.row_div > 1) && g.a_rows * (g.K / 2) > (int64_t)UINT32_MAX;
     auto tiles = [&](int BM, int BN) { return (g.bounds ? g.M / BM + 1 : (g.M + BM - 1) / BM) * nblk(g.N, kSwiglu ? BN / 2 : BN); };
-    if (rows <= 32) {
+    if (rows <= 32 || far) {
         hipLaunchKernelGGL((k_mx_few<kT, kSwiglu, kMode != kScale1>), dim3((unsigned)slots_of(g, 32), nblk(g.N, 32)),
                            dim3(64 * kFewWaves), 0, st, g);
         return hipGetLastError();

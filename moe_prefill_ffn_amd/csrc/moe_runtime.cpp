@@ -1152,7 +1152,7 @@ int moe_mxfp4_gemm(const moe_mxfp4_gemm_args_t* in, void* stream)
         if (!read_struct(in, &a, &why)) return fail(nullptr, MOE_EINVAL, why);
         if (!dtype_ok(a.dtype)) return fail(nullptr, MOE_EINVAL, "mxfp4: dtype must be MOE_F32, MOE_BF16 or MOE_F16");
         if (a.swiglu != 0 && a.swiglu != 1) return fail(nullptr, MOE_EINVAL, "mxfp4: swiglu must be 0 or 1");
-        if (a.K < 32 || a.K % 32) return fail(nullptr, MOE_EINVAL, "mxfp4: K must be a multiple of 32, at least 32");
+        if (a.K < 32 || a.K % 32 || a.K > (1 << 20)) return fail(nullptr, MOE_EINVAL, "mxfp4: K must be a multiple of 32 in [32, 2^20]");
         if (a.N < 1 || a.N > (1 << 20)) return fail(nullptr, MOE_EINVAL, "mxfp4: N must be in [1, 2^20]");
         if (a.M < 0 || a.M > INT32_MAX) return fail(nullptr, MOE_EINVAL, "mxfp4: M must be in [0, 2^31)");
         if (a.n_groups < 1 || a.n_groups > 65535 || (!a.bounds && a.n_groups != 1))

@@ -62,7 +62,7 @@ def gemm_args(**kw):
 
 
 @pytest.mark.parametrize("bad", [
-    dict(struct_size=0), dict(dtype=7), dict(swiglu=2), dict(K=0), dict(K=48), dict(N=0), dict(N=1 << 21), dict(M=-1),
+    dict(struct_size=0), dict(dtype=7), dict(swiglu=2), dict(K=0), dict(K=48), dict(K=(1 << 20) + 32), dict(N=0), dict(N=1 << 21), dict(M=-1),
     dict(M=1 << 31), dict(n_groups=0), dict(n_groups=2), dict(n_groups=65536, bounds=128), dict(top_k=0),
     dict(a_codes=None), dict(a_scales=None), dict(b_codes=None), dict(b_scales=None), dict(out=None),
     dict(a_rows=0), dict(a_rows=3), dict(a_rows=1, top_k=3), dict(a_rows=0, rows=128), dict(out_stride=7),
