@@ -844,16 +844,26 @@ template <int kT, bool kSwiglu, int kMode>
 hipError_t launch_shape(const MxGemm& g, hipStream_t st)
 {
     const int64_t rows = g.M / g.G;       // rows a group has on average
+    // tiles of a shape: what a grouped product has at most
+    auto tiles = [&](int BM, int BN) { return slots_of(g, BM) * (int64_t)nblk(g.N, kSwiglu ? BN / 2 : BN); };
     // the tiled kernel reaches A through the row table by 32 bits of offset
     const bool far = (g.rows || g.row_div > 1) && g.a_rows * (g.K / 2) > (int64_t)UINT32_MAX;
-    auto tiles = [&](int BM, int BN) { return (g.bounds ? g.M / BM + 1 : (g.M + BM - 1) / BM) * nblk(g.N, kSwiglu ? BN / 2 : BN); };
-    if (rows <= 32 || far) {
+    // Fewer tiles than a quarter of the CUs: the few-row kernel's workgroups are narrower and their
+    // waves share K.  64 x 4096 x 4096: 8.3 us against 10.9; 128 rows (64 tiles): 13.6 against 11.1;
+    // 64 groups of 8 rows, N = K = 2048 (more than 1024 tiles): 47 against 34.
+    if (far || (rows <= 64 && tiles(64, 128) < 64)) {
         hipLaunchKernelGGL((k_mx_few<kT, kSwiglu, kMode != kScale1>), dim3((unsigned)slots_of(g, 32), nblk(g.N, 32)),
                            dim3(64 * kFewWaves), 0, st, g);
         return hipGetLastError();
     }
-    if (rows >= 192 && tiles(256, 256) >= 192) return launch_tile<Tile256, kT, kSwiglu, kMode>(g, st);
-    if (rows >= 48 && tiles(128, 128) >= 192) return launch_tile<Tile128, kT, kSwiglu, kMode>(g, st);
+    // 256 x 256 tiles move the fewest bytes a product but start and end slowest: worth it over
+    // several stages and tiles that fill the chip more than once.  8192 x 4096 at K = 4096: 96 us
+    // against 104 of 128 x 128 tiles, K = 1024: 42 against 33; 4096 x 4096 x 4096 (256 tiles): 51, 50.
+    if (rows >= 320 && g.K >= 2048 && tiles(256, 256) >= 384) return launch_tile<Tile256, kT, kSwiglu, kMode>(g, st);
+    // 128 x 128 tiles where they fill the chip's two workgroups a CU and the rows fill a good part of
+    // a tile: 2048 x 4096 x 4096 28 us against 33 of 64 x 128, 64 groups of 64 rows (N = K = 2048)
+    // 46 against 53; 512 x 4096 x 4096 (128 tiles) 18 against 15.5, 64 groups of 24 rows 38 against 36.
+    if (rows >= 40 && tiles(128, 128) >= 512) return launch_tile<Tile128, kT, kSwiglu, kMode>(g, st);
     return launch_tile<Tile64, kT, kSwiglu, kMode>(g, st);
 }
 

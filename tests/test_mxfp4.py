@@ -208,7 +208,22 @@ def test_large_products_take_the_wider_tiles(M, N, K, swiglu, dtype):
 
 
 @gpu
-@pytest.mark.parametrize("M,G,k,N,K,swiglu", [(9000, 20, 3, 1500, 96, False), (6000, 40, 2, 1100, 256, True), (5000, 70, 1, 900, 160, False)])
+@pytest.mark.parametrize("K", [2048, 2080, 2176])         # scale rows 16-byte aligned, not at all, 4-byte aligned
+@pytest.mark.parametrize("M,N,swiglu,dtype", [(5000, 6100, False, torch.float32), (5001, 3050, True, torch.bfloat16)])
+def test_products_of_the_widest_tiles(M, N, K, swiglu, dtype):
+    g = gen(M + K)
+    a = [t.cuda() for t in random_mx(g, M, K, hi=118)]
+    b = [t.cuda() for t in random_mx(g, 2 * N if swiglu else N, K, hi=118)]
+    out = torch.full((M + 2, N), 77.0, dtype=dtype, device="cuda")
+    mp.moe_mxfp4_gemm(*a, *b, out[:M], swiglu=swiglu)
+    want, err = ref.mx_product(ref.mx_values(*a).cuda(), ref.mx_values(*b)[None].cuda(), swiglu=swiglu)
+    check_product(out[:M], dtype, want.cpu(), err.cpu())
+    assert (out[M:] == 77).all()
+
+
+@gpu
+@pytest.mark.parametrize("M,G,k,N,K,swiglu", [(9000, 20, 3, 1500, 96, False), (6000, 40, 2, 1100, 256, True), (5000, 70, 1, 900, 160, False),
+                                              (4001, 4, 1, 7001, 2048, False)])
 def test_large_grouped_products(M, G, k, N, K, swiglu):
     g = gen(M + G)
     ac, asc = random_mx(g, M // k, K, hi=122)
