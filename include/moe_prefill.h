@@ -313,7 +313,7 @@ typedef struct moe_mxfp4_matrix {
     int32_t device;            /* HIP device ordinal */
     int32_t dtype;             /* MOE_F32 / MOE_BF16 / MOE_F16: the type of values */
     int32_t K;                 /* multiple of 32, >= 32 */
-    int64_t M;                 /* rows, >= 0 (0 is a no-op); M * K / 32 < 2^31 */
+    int64_t M;                 /* rows, >= 0 (0 is a no-op); M * K / 32 < 2^30 */
     void* values;              /* device [M, K], rows `stride` elements apart; rows 16-byte aligned */
     int64_t stride;            /* >= K */
     uint8_t* codes;            /* device [M, K/2], 16-byte aligned */
@@ -349,14 +349,15 @@ typedef struct moe_mxfp4_gemm_args {
     int32_t device;
     const uint8_t* a_codes;    /* device [a_rows, K/2], 16-byte aligned */
     const uint8_t* a_scales;   /* device [a_rows, K/32] */
-    int64_t a_rows;            /* >= 1 if M > 0 */
+    int64_t a_rows;            /* >= 1 if M > 0, < 2^31 */
     const uint8_t* b_codes;    /* device [n_groups, N or 2N, K/2], 16-byte aligned */
     const uint8_t* b_scales;   /* device [n_groups, N or 2N, K/32] */
     const int32_t* bounds;     /* device [n_groups + 1], ascending within [0, M]; NULL: dense */
     const int32_t* rows;       /* device [M]; NULL: in order */
     int32_t n_groups;          /* 1..65535 (1 if dense) */
     int32_t top_k;             /* >= 1 */
-    int64_t M;                 /* rows of out, >= 0 (0 is a no-op), < 2^31 */
+    int64_t M;                 /* rows of out, 0 (a no-op) .. 2^27, and
+                                  (M / 64 + n_groups) * ceil(N / 64) <= 2^30 */
     int32_t N, K;              /* N in 1..2^20, K a multiple of 32 in 32..2^20 */
     int32_t swiglu;            /* 0 or 1 */
     int32_t dtype;             /* type of out */

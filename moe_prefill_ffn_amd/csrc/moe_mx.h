@@ -8,6 +8,12 @@
 
 namespace moe {
 
+// What one launch takes: a launch has fewer than 2^32 threads (four a block of 32; 512 for 32 rows
+// and a group's last ones), and the tiled kernel counts its tiles in 32 bits.
+constexpr int64_t kMxMostBlocks = (1 << 30) - 1;      // M * K / 32 of quantise and dequantise
+constexpr int64_t kMxMostRows = 1 << 27;              // M of a product
+constexpr int64_t kMxMostTiles = 1 << 30;             // its tiles, the smallest being 64 x 64
+
 struct MxQuant {
     const void* x;            // quantise: [M, K] in; dequantise: out
     void* y;
@@ -19,7 +25,7 @@ struct MxQuant {
 };
 
 struct MxGemm {
-    const uint8_t* a_codes;   // [a_rows, K / 2]
+    const uint8_t* a_codes;   // [a_rows, K / 2], a_rows < 2^31
     const uint8_t* a_scales;  // [a_rows, K / 32]
     int64_t a_rows;
     const int32_t* rows;      // row r of the product reads A row rows[r] / row_div (null: r / row_div)

@@ -43,7 +43,7 @@ struct BlockAt {
 };
 __device__ __forceinline__ BlockAt block_at(int64_t blk, int nb)
 {
-    const uint32_t row = (uint32_t)blk / (uint32_t)nb;    // fewer than 2^31 blocks
+    const uint32_t row = (uint32_t)blk / (uint32_t)nb;    // fewer than 2^30 blocks
     return {(int64_t)row, (int)((uint32_t)blk - row * (uint32_t)nb)};
 }
 
@@ -214,7 +214,7 @@ __device__ __forceinline__ Tile tile_of_slot(const MxGemm& a, int64_t slot)
 // A row of the product reads this row of A.
 __device__ __forceinline__ int64_t a_row(const MxGemm& a, int64_t r)
 {
-    int src = a.rows ? a.rows[r] : (int)r;                // r < 2^31
+    int src = a.rows ? a.rows[r] : (int)r;                // r < 2^27
     if (a.row_div > 1) src /= a.row_div;
     return src < 0 ? 0 : (src >= a.a_rows ? a.a_rows - 1 : src);
 }
@@ -582,7 +582,7 @@ __global__ __launch_bounds__(64 * S::NW) void k_mx_tile(MxGemm a, int n_tiles, i
             const int64_t id = list0 + (int64_t)(w0 + lane) * nq;
             ListedTile t = {0, 0, 0, 0};
             if (id < run1) {
-                const uint32_t band = (uint32_t)id / (uint32_t)(8 * n_tiles), first = band * 8;   // total < 2^31
+                const uint32_t band = (uint32_t)id / (uint32_t)(8 * n_tiles), first = band * 8;   // total <= 2^30
                 const uint32_t high = n_slots - first < 8 ? (uint32_t)(n_slots - first) : 8;
                 const uint32_t in = (uint32_t)id - first * n_tiles;
                 const Tile f = tile_of_slot_lane<S::BM>(a, first + in % high);
@@ -826,8 +826,7 @@ hipError_t launch_tile(const MxGemm& g, hipStream_t st)
 {
     constexpr int lds = MxLds<S, kMode>::kBytes;
     const int n_tiles = (int)nblk(g.N, kSwiglu ? S::BN / 2 : S::BN);
-    const int64_t slots = slots_of(g, S::BM), total = slots * n_tiles;
-    if (total > INT32_MAX - 8) return hipErrorInvalidValue;
+    const int64_t slots = slots_of(g, S::BM), total = slots * n_tiles;   // at most 2^30 (kMxMostTiles)
     // more than the default limit of dynamic LDS
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_mx_tile<S, kT, kSwiglu, kMode>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);

@@ -1111,8 +1111,8 @@ static int mx_matrix(const moe_mxfp4_matrix_t* in, bool quantize, void* stream)
         if (!read_struct(in, &m, &why)) return fail(nullptr, MOE_EINVAL, why);
         if (!dtype_ok(m.dtype)) return fail(nullptr, MOE_EINVAL, "mxfp4: dtype must be MOE_F32, MOE_BF16 or MOE_F16");
         if (m.K < 32 || m.K % 32) return fail(nullptr, MOE_EINVAL, "mxfp4: K must be a multiple of 32, at least 32");
-        if (m.M < 0 || m.M > INT32_MAX / (m.K / 32))
-            return fail(nullptr, MOE_EINVAL, "mxfp4: M < 0 or M * K / 32 not below 2^31");
+        if (m.M < 0 || m.M > kMxMostBlocks / (m.K / 32))
+            return fail(nullptr, MOE_EINVAL, "mxfp4: M < 0 or M * K / 32 not below 2^30");
         if (m.M == 0) {
             g_err.clear();
             return (int)MOE_OK;
@@ -1154,9 +1154,11 @@ int moe_mxfp4_gemm(const moe_mxfp4_gemm_args_t* in, void* stream)
         if (a.swiglu != 0 && a.swiglu != 1) return fail(nullptr, MOE_EINVAL, "mxfp4: swiglu must be 0 or 1");
         if (a.K < 32 || a.K % 32 || a.K > (1 << 20)) return fail(nullptr, MOE_EINVAL, "mxfp4: K must be a multiple of 32 in [32, 2^20]");
         if (a.N < 1 || a.N > (1 << 20)) return fail(nullptr, MOE_EINVAL, "mxfp4: N must be in [1, 2^20]");
-        if (a.M < 0 || a.M > INT32_MAX) return fail(nullptr, MOE_EINVAL, "mxfp4: M must be in [0, 2^31)");
+        if (a.M < 0 || a.M > kMxMostRows) return fail(nullptr, MOE_EINVAL, "mxfp4: M must be in [0, 2^27]");
         if (a.n_groups < 1 || a.n_groups > 65535 || (!a.bounds && a.n_groups != 1))
             return fail(nullptr, MOE_EINVAL, "mxfp4: n_groups must be in [1, 65535], and 1 without bounds");
+        if ((a.M / 64 + a.n_groups) * ((a.N + 63) / 64) > kMxMostTiles)
+            return fail(nullptr, MOE_EINVAL, "mxfp4: (M / 64 + n_groups) * N / 64 above 2^30; take the rows in parts");
         if (a.top_k < 1) return fail(nullptr, MOE_EINVAL, "mxfp4: top_k must be at least 1");
         if (a.M == 0) {
             g_err.clear();
@@ -1164,8 +1166,8 @@ int moe_mxfp4_gemm(const moe_mxfp4_gemm_args_t* in, void* stream)
         }
         if (!a.a_codes || !a.a_scales || !a.b_codes || !a.b_scales || !a.out)
             return fail(nullptr, MOE_EINVAL, "mxfp4: a_codes, a_scales, b_codes, b_scales and out are required");
-        if (a.a_rows < 1 || (!a.rows && a.a_rows < (a.M + a.top_k - 1) / a.top_k))
-            return fail(nullptr, MOE_EINVAL, "mxfp4: A has fewer rows than the product reads");
+        if (a.a_rows < 1 || a.a_rows > INT32_MAX || (!a.rows && a.a_rows < (a.M + a.top_k - 1) / a.top_k))
+            return fail(nullptr, MOE_EINVAL, "mxfp4: A has 2^31 rows or more, or fewer than the product reads");
         if (!stride_ok(a.out_stride, a.N)) return fail(nullptr, MOE_EINVAL, "mxfp4: out_stride below N, or above 2^40");
         if ((addr(a.a_codes) | addr(a.b_codes)) % 16)
             return fail(nullptr, MOE_EINVAL, "mxfp4: a_codes and b_codes must be 16-byte aligned");

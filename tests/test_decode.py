@@ -296,6 +296,40 @@ def test_two_graphs_with_their_own_workspaces_and_an_eager_call_between(layers):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,d,f", [(1, 16384, 32), (1, 32, 16384), (7, 16384, 32), (7, 32, 16384), (2, 16384, 1024)])
+def test_longest_rows(layers, T, d, f, dtype):
+    L, h, blob = layers(d, f, 2, 1)
+    x, lg = inputs(T, L, dtype, seed=T)
+    y, ex = run(L, h, x, lg, blob)
+    check(y, ex, L, x, lg)
+
+
+@gpu
+def test_calls_at_once_on_two_streams(layers):
+    """One handle, a workspace per call: the calls of each path (few pairs, chunks) run into each other."""
+    L, h, blob = layers(2048, 768, 9, 8)
+    calls = []
+    for T in (1, 5, 16, 100):
+        x, lg = (t.cuda() for t in inputs(T, L, torch.bfloat16, seed=T))
+        want = torch.empty_like(x)
+        mp.moe_decode_run_layer(h, x, lg, want, weights=blob)
+        calls.append((x, lg, want))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    outs = []
+    for _ in range(5):
+        for (x, lg, want), s in zip(calls, streams):
+            y = torch.full_like(want, 77.0)
+            s.wait_stream(torch.cuda.current_stream())
+            y.record_stream(s)
+            mp.moe_decode_run_layer(h, x, lg, y, weights=blob, stream=s)
+            outs.append((y, want))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, w) for y, w in outs)
+
+
+@gpu
 def test_on_another_stream_than_the_current_one(layers):
     L, h, blob = layers(2048, 768, 9, 8)
     x, lg = inputs(4, L, torch.float16)

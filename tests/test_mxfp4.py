@@ -38,7 +38,7 @@ def matrix(**kw):
 
 @pytest.mark.parametrize("bad", [
     dict(struct_size=4), dict(dtype=3), dict(dtype=-1), dict(K=0), dict(K=33), dict(K=-32), dict(M=-1),
-    dict(M=1 << 31), dict(values=None), dict(codes=None), dict(scales=None), dict(stride=63), dict(stride=-64),
+    dict(M=1 << 31), dict(M=1 << 29), dict(K=1 << 20, M=1 << 15, stride=1 << 20), dict(values=None), dict(codes=None), dict(scales=None), dict(stride=63), dict(stride=-64),
     dict(stride=1 << 41), dict(values=4100), dict(codes=8200), dict(stride=66), dict(stride=68, dtype=mp.MOE_BF16)])
 def test_matrix_refusals(bad):
     for fn in (mp.lib().moe_mxfp4_quantize, mp.lib().moe_mxfp4_dequantize):
@@ -63,7 +63,8 @@ def gemm_args(**kw):
 
 @pytest.mark.parametrize("bad", [
     dict(struct_size=0), dict(dtype=7), dict(swiglu=2), dict(K=0), dict(K=48), dict(K=(1 << 20) + 32), dict(N=0), dict(N=1 << 21), dict(M=-1),
-    dict(M=1 << 31), dict(n_groups=0), dict(n_groups=2), dict(n_groups=65536, bounds=128), dict(top_k=0),
+    dict(M=1 << 31), dict(M=(1 << 27) + 1, a_rows=1 << 28), dict(M=1 << 24, a_rows=1 << 24, N=1 << 20, out_stride=1 << 20),
+    dict(a_rows=1 << 31), dict(n_groups=0), dict(n_groups=2), dict(n_groups=65536, bounds=128), dict(top_k=0),
     dict(a_codes=None), dict(a_scales=None), dict(b_codes=None), dict(b_scales=None), dict(out=None),
     dict(a_rows=0), dict(a_rows=3), dict(a_rows=1, top_k=3), dict(a_rows=0, rows=128), dict(out_stride=7),
     dict(a_codes=4104), dict(b_codes=16400 - 8), dict(out=65538), dict(out=65537, dtype=mp.MOE_BF16),
@@ -385,3 +386,133 @@ def test_binding_refusals_on_the_device():
         mp.moe_mxfp4_quantize(torch.zeros(64, 4, device="cuda").t())
     with pytest.raises(TypeError):
         mp.moe_mxfp4_quantize(torch.zeros(2, 64, device="cuda", dtype=torch.float64))
+
+
+@gpu
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_many_empty_groups(swiglu):
+    """More tile slots than a workgroup lists at a time, nearly all of groups without rows."""
+    g = gen(11)
+    G, M, N, K = 65535, 900, 150, 32
+    ac, asc = random_mx(g, M, K, hi=120)
+    bc, bsc = random_mx(g, G, 2 * N if swiglu else N, K, hi=120)
+    held = sorted(torch.randperm(G, generator=g)[:12].tolist())
+    held[0], held[-1] = 0, G - 1
+    cuts = [0] + sorted(torch.randint(0, M + 1, (11,), generator=g).tolist()) + [M]
+    bounds = torch.zeros(G + 1, dtype=torch.int32)
+    for i, e in enumerate(held):
+        bounds[e + 1:] = cuts[i + 1]
+    out = torch.full((M, N), 77.0, device="cuda")
+    mp.moe_mxfp4_gemm(ac.cuda(), asc.cuda(), bc.cuda(), bsc.cuda(), out, bounds=bounds.cuda(), swiglu=swiglu)
+    want, err = ref.mx_product(ref.mx_values(ac, asc), ref.mx_values(bc[held], bsc[held]), torch.tensor(cuts), swiglu=swiglu)
+    check_product(out, torch.float32, want, err)
+
+
+@gpu
+@pytest.mark.parametrize("far,M", [("a", 5), ("a just below", 130), ("a", 130), ("b", 3), ("b", 70), ("out", 70)])
+def test_offsets_past_32_bits(far, M):
+    """Codes of A (reached by a row table) or of B that span more than 2^32 bytes, or just fewer, and an
+    output that does: all zero but for the rows that count."""
+    g = gen(M)
+    K = 64 if far == "out" else 1 << 18
+    A = {"a": 32800, "a just below": 32767}.get(far, M)
+    N = 33000 if far == "b" else 40
+    a = [torch.zeros(A, K // 2, dtype=torch.uint8, device="cuda"), torch.full((A, K // 32), 127, dtype=torch.uint8, device="cuda")]
+    b = [torch.zeros(N, K // 2, dtype=torch.uint8, device="cuda"), torch.full((N, K // 32), 127, dtype=torch.uint8, device="cuda")]
+    ar = sorted({0, A // 2, A - 2, A - 1}) if A > M else list(range(M))
+    br = [0, N // 2, N - 1]
+    for t, rows in ((a, ar), (b, br)):
+        for m, v in zip(t, random_mx(g, len(rows), K, hi=118)):
+            m[rows] = v.cuda()
+    rows = torch.tensor(ar)[torch.randint(0, len(ar), (M,), generator=g)].int().cuda() if A > M else None
+    stride = 1 << 26 if far == "out" else N
+    buf = torch.empty((M - 1) * stride + N, device="cuda")
+    out = buf.as_strided((M, N), (stride, 1))
+    mp.moe_mxfp4_gemm(*a, *b, out, rows=rows)
+    near = torch.searchsorted(torch.tensor(ar), rows.cpu().long()).int() if rows is not None else None
+    want, err = ref.mx_product(ref.mx_values(a[0][ar], a[1][ar]), ref.mx_values(b[0][br], b[1][br])[None], rows=near)
+    check_product(out[:, br], torch.float32, want, err)
+    zero = torch.ones(N, dtype=torch.bool)
+    zero[br] = False
+    assert (out[:, zero.cuda()] == 0).all()
+
+
+@gpu
+def test_quantise_of_more_than_2_to_the_31_elements():
+    M, K = 66000, 32768
+    x = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    codes, scales = mp.moe_mxfp4_quantize(x.fill_(1.5))
+    for r0, r1 in ((0, 3), (40000, 40002), (M - 3, M)):
+        assert (codes[r0:r1] == 0x77).all() and (scales[r0:r1] == 125).all()       # 1.5 = 6 * 2^-2
+    tail = torch.randn(5, K, generator=gen(1)).bfloat16()
+    x[-5:] = tail.cuda()
+    mp.moe_mxfp4_quantize(x, codes, scales)
+    check_quantised(tail, codes[-5:], scales[-5:], torch.bfloat16)
+    back = mp.moe_mxfp4_dequantize(codes, scales, out=x)
+    assert_same(back[-5:], ref.mx_values(codes[-5:], scales[-5:]).bfloat16())
+    assert (back[:-5] == 1.5).all()
+
+
+@gpu
+def test_layer_of_the_operators_after_the_routing_of_a_prompt():
+    """The products of a MoE layer on MXFP4 weights, with the row table, bounds and weights that the
+    prompt path exports: quantise, gate/up with SwiGLU, quantise, down."""
+    d, f, E, k, T = 256, 192, 10, 3, 150
+    g = gen(5)
+    R = T * k
+    x = torch.randn(T, d, generator=g)
+    logits = torch.randn(T, E, generator=g)
+    logits[:, 7] = -50.0                                  # an expert without rows
+    wgu = mp.moe_mxfp4_quantize((torch.randn(E * 2 * f, d, generator=g) / 16).cuda())
+    wd = mp.moe_mxfp4_quantize((torch.randn(E * d, f, generator=g) / 16).cuda())
+    wgu, wd = [t.view(E, 2 * f, -1) for t in wgu], [t.view(E, d, -1) for t in wd]
+    ex = dict(rows=torch.empty(R, dtype=torch.int32, device="cuda"), bounds=torch.empty(E + 1, dtype=torch.int32, device="cuda"),
+              weights=torch.empty(T, k, device="cuda"))
+    h = mp.moe_prefill_create(d, f, E, k, T)
+    blob = torch.zeros(mp.moe_prefill_layer_bytes(d, f, E), dtype=torch.uint8, device="cuda")
+    y = torch.empty(T, d, device="cuda")
+    mp.moe_prefill_run_layer(h, x.cuda(), logits.cuda(), y, weights=blob, exports=ex)
+    xq = mp.moe_mxfp4_quantize(x.cuda())
+    hh = mp.moe_mxfp4_gemm(*xq, *wgu, bounds=ex["bounds"], rows=ex["rows"], top_k=k, swiglu=True, dtype=torch.bfloat16)
+    hq = mp.moe_mxfp4_quantize(hh)
+    dm = mp.moe_mxfp4_gemm(*hq, *wd, bounds=ex["bounds"])
+    pair = ex["rows"].long()
+    y.zero_().index_add_(0, pair // k, dm * ex["weights"].view(-1)[pair, None])
+    torch.cuda.synchronize()
+    h.close()
+    bounds, rows = ex["bounds"].cpu(), ex["rows"].cpu()
+    assert bounds[0] == 0 and bounds[-1] == R and bounds[7] == bounds[8]
+    want, err = ref.mx_product(ref.mx_values(*xq), ref.mx_values(*wgu), bounds, rows, k, True)
+    check_product(hh, torch.bfloat16, want, err)
+    check_quantised(hh, *hq, torch.bfloat16)
+    want, err = ref.mx_product(ref.mx_values(*hq), ref.mx_values(*wd), bounds, torch.arange(R).int(), 1)
+    check_product(dm, torch.float32, want, err)
+    # by the dense formula: the 4-bit roundings of x, h and both weights (an element of a block of 32
+    # normal values is off by about a tenth of its rms) make it a fifth to a third of the output's norm
+    full, wg, wdn = torch.zeros(T, d, dtype=torch.float64), ref.mx_values(*wgu), ref.mx_values(*wd)
+    wt = torch.softmax(logits.double().topk(k, -1).values, -1)
+    for t in range(T):
+        for j, e in enumerate(logits[t].topk(k).indices.tolist()):
+            z = wg[e] @ x[t].double()
+            full[t] += wt[t, j] * (wdn[e] @ (z[:f] * torch.sigmoid(z[:f]) * z[f:]))
+    assert float((y.cpu() - full).norm() / full.norm()) < 0.4
+
+
+@gpu
+def test_products_on_two_streams_at_once():
+    g = gen(6)
+    sets = []
+    for M, N, K in ((700, 900, 1024), (2500, 4200, 512)):
+        a, b = ([t.cuda() for t in random_mx(g, n, K)] for n in (M, N))
+        sets.append((a, b, mp.moe_mxfp4_gemm(*a, *b)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = []
+    for _ in range(4):
+        for (a, b, want), s in zip(sets, streams):
+            o = torch.full_like(want, 77.0)
+            s.wait_stream(torch.cuda.current_stream())
+            mp.moe_mxfp4_gemm(*a, *b, o, stream=s)
+            outs.append((o, want))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in outs)
