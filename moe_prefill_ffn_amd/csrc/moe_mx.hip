@@ -147,69 +147,7 @@ __global__ __launch_bounds__(kQuantThreads) void k_mx_dequantize(MxQuant q, int6
 //
 // A block past the end of K is read from the last block (in bounds, any finite codes) with
 // scale byte 0 on both sides: 2^-254 of a product below 2^11 is 0 in fp32.
-//
-// Groups of a row table: tile slot s belongs to the last group g whose first slot
-// bounds[g] / BM + g is <= s (a group of c rows never needs more than the
-// bounds[g + 1] / BM + 1 - bounds[g] / BM slots up to the next group's first), so a
-// workgroup finds its rows from the bounds alone, without a list of tiles.
 typedef int v4i __attribute__((ext_vector_type(4)));
-
-struct Tile {
-    int g;
-    int64_t m0, m1;           // rows [m0, m1) of the tile; m0 >= m1: nothing to do
-};
-
-template <int BM>
-__device__ __forceinline__ Tile tile_of_group(const MxGemm& a, int g, int64_t slot)
-{
-    const int64_t b0 = a.bounds[g], b1 = a.bounds[g + 1];
-    int64_t m0 = b0 + (slot - (b0 / BM + g)) * BM, m1 = m0 + BM < b1 ? m0 + BM : b1;
-    // sound bounds ascend within [0, M]; this only keeps others from reaching outside
-    if (m0 < b0 || m0 < 0) m0 = m1;
-    if (m1 > a.M) m1 = a.M;
-    return {g, m0, m1};
-}
-template <int BM>
-__device__ __forceinline__ Tile tile_of_rows(const MxGemm& a, int64_t slot)
-{
-    const int64_t m0 = slot * BM;
-    return {0, m0, m0 + BM < a.M ? m0 + BM : a.M};
-}
-
-// The tile of a slot, by each lane for a slot of its own.
-template <int BM>
-__device__ __forceinline__ Tile tile_of_slot_lane(const MxGemm& a, int64_t slot)
-{
-    if (!a.bounds) return tile_of_rows<BM>(a, slot);
-    int lo = 0, hi = a.G - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if ((int64_t)(a.bounds[mid] / BM) + mid <= slot)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    return tile_of_group<BM>(a, lo, slot);
-}
-
-// The tile of a slot, the same on all lanes, by the wave together.
-template <int BM>
-__device__ __forceinline__ Tile tile_of_slot(const MxGemm& a, int64_t slot)
-{
-    if (!a.bounds) return tile_of_rows<BM>(a, slot);
-    // 64 groups are compared at a time, one per lane: two rounds of loads up to 4096 groups
-    int g = 0, span = a.G;
-    const int lane = threadIdx.x & 63;
-    while (span > 1) {
-        const int step = (span + 63) >> 6, at = g + lane * step;
-        const bool le = lane * step < span && (int64_t)(a.bounds[at] / BM) + at <= slot;
-        const int n = __popcll(__ballot(le));             // a run of lanes from 0 for sound bounds
-        const int skip = (n > 0 ? n - 1 : 0) * step;
-        g += skip;
-        span = span - skip < step ? span - skip : step;
-    }
-    return tile_of_group<BM>(a, __builtin_amdgcn_readfirstlane(g), slot);
-}
 
 // A row of the product reads this row of A.
 __device__ __forceinline__ int64_t a_row(const MxGemm& a, int64_t r)
@@ -304,7 +242,7 @@ struct MxLds {
     static constexpr int kScaleOff = 2 * kDataBytes;
     static constexpr int kRowsOff = kScaleOff + 2 * kScaleBytes;            // row indices of two tiles
     static constexpr int kListOff = kRowsOff + 2 * S::BM * 4;
-    static constexpr int kBytes = kListOff + kListMost * (int)sizeof(ListedTile) + 16;
+    static constexpr int kBytes = kListOff + kListMost * (int)sizeof(ListedTile);
 };
 
 // Persistent workgroups: each takes every so-many-th tile of its XCD's run (workgroups go
@@ -328,7 +266,6 @@ __global__ __launch_bounds__(64 * S::NW) void k_mx_tile(MxGemm a, int n_tiles, i
     constexpr int kOutCols = kSwiglu ? S::BN / 2 : S::BN;
     int32_t* s_rows = reinterpret_cast<int32_t*>(lds + L::kRowsOff);
     ListedTile* s_list = reinterpret_cast<ListedTile*>(lds + L::kListOff);
-    int* s_count = reinterpret_cast<int*>(lds + L::kListOff + kListMost * sizeof(ListedTile));
     const uint32_t lds0 = lds_addr(lds);
 
     // Data: a base per operand and tile, an offset per lane and load (kScale16: to its chunk, else
@@ -566,37 +503,100 @@ __global__ __launch_bounds__(64 * S::NW) void k_mx_tile(MxGemm a, int n_tiles, i
         }
     };
 
-    // this workgroup's tiles: bands of 8 slots by all column tiles, so that what an XCD runs at
-    // once shares rows of A and of B in its L2
-    const int64_t total = n_slots * n_tiles, per = (total + 7) >> 3;
-    const int64_t run0 = (int64_t)(blockIdx.x & 7) * per, run1 = run0 + per < total ? run0 + per : total;
-    const int nq = gridDim.x >> 3;
-    for (int64_t list0 = run0 + (blockIdx.x >> 3); list0 < run1; list0 += (int64_t)nq * kListMost) {
-        // list the next kListMost tiles that hold rows
-        __syncthreads();                                  // the previous list is done
-        if (tid == 0) *s_count = 0;
+    // The tiles of BM rows that hold any, in the groups' order.  scan: those of the kWin groups from
+    // base on, and in s_pre how many of them lie before each group's.
+    constexpr int kPer = 4, kWin = 64 * S::NW * kPer;
+    uint32_t* s_pre = reinterpret_cast<uint32_t*>(lds);   // nothing else is in the stages' slots then
+    uint32_t* s_wave = s_pre + kWin;
+    static_assert((kWin + S::NW) * 4 <= 2 * L::kDataBytes, "inside the stages' slots");
+    auto bound = [&](int g) -> int {                      // sound bounds lie within [0, M]
+        const int64_t b = a.bounds[g < a.G ? g : a.G];
+        return (int)(b < 0 ? 0 : b > a.M ? a.M : b);
+    };
+    auto scan = [&](int base) -> uint32_t {
+        int b[kPer + 1];
+        uint32_t n[kPer], sum = 0;
+#pragma unroll
+        for (int i = 0; i <= kPer; ++i) b[i] = bound(base + tid * kPer + i);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            n[i] = b[i + 1] > b[i] ? (uint32_t)(b[i + 1] - b[i] + S::BM - 1) / S::BM : 0u;
+            sum += n[i];                                  // at most 2^21 a group, 2^31 a window
+        }
+        uint32_t upto = sum;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const uint32_t y = (uint32_t)__shfl_up((int)upto, o);
+            if (lane >= o) upto += y;
+        }
+        __syncthreads();                                  // the last scan's, or list's, readers are done
+        if (lane == 63) s_wave[wave] = upto;
         __syncthreads();
-#pragma unroll 1
-        for (int w0 = 0; w0 < kListMost; w0 += 64) {      // wave 0: in order
-            if (wave != 0) break;
-            const int64_t id = list0 + (int64_t)(w0 + lane) * nq;
-            ListedTile t = {0, 0, 0, 0};
-            if (id < run1) {
-                const uint32_t band = (uint32_t)id / (uint32_t)(8 * n_tiles), first = band * 8;   // total <= 2^30
-                const uint32_t high = n_slots - first < 8 ? (uint32_t)(n_slots - first) : 8;
-                const uint32_t in = (uint32_t)id - first * n_tiles;
-                const Tile f = tile_of_slot_lane<S::BM>(a, first + in % high);
-                t = {f.g, (int)f.m0, (int)(f.m0 < f.m1 ? f.m1 : f.m0), (int)(in / high)};
-            }
-            const bool keep = t.m0 < t.m1;
-            const uint64_t mask = __ballot(keep);
-            const int base = *s_count;
-            if (keep) s_list[base + __popcll(mask & ((1ull << lane) - 1))] = t;
-            if (lane == 0) *s_count = base + __popcll(mask);
+        uint32_t before = upto - sum, all = 0;
+#pragma unroll
+        for (int w = 0; w < S::NW; ++w) {
+            before += w < wave ? s_wave[w] : 0u;
+            all += s_wave[w];
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            s_pre[tid * kPer + i] = before;
+            before += n[i];
         }
         __syncthreads();
-        const int count = *s_count;
-        if (count == 0) continue;                         // uniform
+        return (uint32_t)__builtin_amdgcn_readfirstlane((int)all);
+    };
+    int64_t slots = n_slots;
+    uint32_t first_window = 0;
+    if (a.bounds) {
+        slots = 0;
+        for (int base = 0; base < a.G; base += kWin) slots += first_window = scan(base);
+        if (slots > n_slots) slots = n_slots;             // bounds that do not ascend
+    }
+
+    // this workgroup's tiles: bands of 8 row tiles by all column tiles, so that what an XCD runs at
+    // once shares rows of A and of B in its L2; each XCD a run of as many tiles as the others, each of
+    // its workgroups as many of them.  (Empty tiles numbered along, at most one a group, left the
+    // fullest workgroup of 24576 rows in 256 groups 28 tiles of 19 on average.)
+    const int64_t total = slots * n_tiles, per = (total + 7) >> 3;
+    const int64_t run0 = (int64_t)(blockIdx.x & 7) * per, run1 = run0 + per < total ? run0 + per : total;
+    const int nq = gridDim.x >> 3;
+    static_assert(kListMost == 64 * S::NW, "a listed tile a thread");
+    for (int64_t list0 = run0 + (blockIdx.x >> 3); list0 < run1; list0 += (int64_t)nq * kListMost) {
+        const int64_t id = list0 + (int64_t)tid * nq;
+        const bool want = id < run1;
+        const uint32_t band = (uint32_t)id / (uint32_t)(8 * n_tiles), first = band * 8;   // total <= 2^30
+        const uint32_t high = slots - first < 8 ? (uint32_t)(slots - first) : 8;
+        const uint32_t in = (uint32_t)id - first * n_tiles;
+        const int64_t at = first + (want ? in % high : 0);
+        const int nt = want ? (int)(in / high) : 0;
+        __syncthreads();                                  // the previous list is done
+        if (!a.bounds) {
+            const int64_t end = (at + 1) * S::BM;
+            if (want) s_list[tid] = {0, (int)(at * S::BM), (int)(end < a.M ? end : a.M), nt};
+        }
+        int64_t before = 0;                               // tiles before the window's
+        for (int base = 0; a.bounds && base < a.G; base += kWin) {
+            const bool have = a.G <= kWin && list0 < run0 + nq;          // scanned above, uniform
+            const uint32_t n = have ? first_window : scan(base);
+            const int64_t x = at - before;
+            before += n;
+            if (want && x >= 0 && x < n) {
+                int lo = 0, hi = kWin - 1;                // the last group with s_pre <= x
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (s_pre[mid] <= (uint32_t)x)
+                        lo = mid;
+                    else
+                        hi = mid - 1;
+                }
+                const int g = base + lo, m0 = bound(g) + (int)((uint32_t)x - s_pre[lo]) * S::BM, end = bound(g + 1);
+                s_list[tid] = {g, m0, m0 + S::BM < end ? m0 + S::BM : end, nt};
+            }
+        }
+        __syncthreads();
+        const int64_t left = (run1 - list0 + nq - 1) / nq;
+        const int count = left < kListMost ? (int)left : kListMost;
         auto listed = [&](int i) -> ListedTile {
             const ListedTile t = s_list[i < count ? i : count - 1];
             return {__builtin_amdgcn_readfirstlane(t.g), __builtin_amdgcn_readfirstlane(t.m0),
@@ -701,14 +701,50 @@ __global__ __launch_bounds__(64 * S::NW) void k_mx_tile(MxGemm a, int n_tiles, i
 // workgroup; its waves take every eighth run of 256 codes of K, fed straight from memory,
 // and add up through LDS in wave order.  What bounds it is B's bytes, read once: lane half
 // h takes blocks 4 h + s of a run, 64 consecutive bytes of a row in four loads.
-constexpr int kFewWaves = 8;
+constexpr int kFewWaves = 8, kFewRows = 32;
+
+// Groups of a row table: row slot s belongs to the last group g whose first slot
+// bounds[g] / 32 + g is <= s (a group of c rows never needs more than the
+// bounds[g + 1] / 32 + 1 - bounds[g] / 32 slots up to the next group's first), so a
+// workgroup finds its rows from the bounds alone, and where there is nothing to do it ends.
+struct Rows {
+    int g;
+    int64_t m0, m1;           // rows [m0, m1); m0 >= m1: nothing to do
+};
+
+// The rows of a slot, the same on all lanes, by the wave together.
+__device__ __forceinline__ Rows rows_of_slot(const MxGemm& a, int64_t slot)
+{
+    if (!a.bounds) {
+        const int64_t m0 = slot * kFewRows;
+        return {0, m0, m0 + kFewRows < a.M ? m0 + kFewRows : a.M};
+    }
+    // 64 groups are compared at a time, one per lane: two rounds of loads up to 4096 groups
+    int g = 0, span = a.G;
+    const int lane = threadIdx.x & 63;
+    while (span > 1) {
+        const int step = (span + 63) >> 6, at = g + lane * step;
+        const bool le = lane * step < span && (int64_t)(a.bounds[at] / kFewRows) + at <= slot;
+        const int n = __popcll(__ballot(le));             // a run of lanes from 0 for sound bounds
+        const int skip = (n > 0 ? n - 1 : 0) * step;
+        g += skip;
+        span = span - skip < step ? span - skip : step;
+    }
+    g = __builtin_amdgcn_readfirstlane(g);
+    const int64_t b0 = a.bounds[g], b1 = a.bounds[g + 1];
+    int64_t m0 = b0 + (slot - (b0 / kFewRows + g)) * kFewRows, m1 = m0 + kFewRows < b1 ? m0 + kFewRows : b1;
+    // sound bounds ascend within [0, M]; this only keeps others from reaching outside
+    if (m0 < b0 || m0 < 0) m0 = m1;
+    if (m1 > a.M) m1 = a.M;
+    return {g, m0, m1};
+}
 
 template <int kT, bool kSwiglu, bool kAligned>
 __global__ __launch_bounds__(64 * kFewWaves) void k_mx_few(MxGemm a)
 {
     constexpr int NT = kSwiglu ? 2 : 1;
     __shared__ float red[kFewWaves][NT][32][33];
-    const Tile t = tile_of_slot<32>(a, blockIdx.x);
+    const Rows t = rows_of_slot(a, blockIdx.x);
     if (t.m0 >= t.m1) return;                             // uniform
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, j = lane & 31;
     const int nb = a.K / 32, NB = kSwiglu ? 2 * a.N : a.N;
@@ -818,7 +854,7 @@ using Tile256 = MxShape<2, 2, 4, 4>;      // 256 x 256
 using Tile128 = MxShape<2, 2, 2, 2>;      // 128 x 128
 using Tile64 = MxShape<2, 2, 1, 2>;       // 64 x 128
 
-// Slots of BM rows: see tile_of_slot.
+// The most tiles of BM rows that the groups can have, and the few-row kernel's slots.
 int64_t slots_of(const MxGemm& g, int BM) { return g.bounds ? g.M / BM + g.G : (g.M + BM - 1) / BM; }
 
 template <class S, int kT, bool kSwiglu, int kMode>
@@ -851,7 +887,7 @@ hipError_t launch_shape(const MxGemm& g, hipStream_t st)
     // waves share K.  64 x 4096 x 4096: 8.3 us against 10.9; 128 rows (64 tiles): 13.6 against 11.1;
     // 64 groups of 8 rows, N = K = 2048 (more than 1024 tiles): 47 against 34.
     if (far || (rows <= 64 && tiles(64, 128) < 64)) {
-        hipLaunchKernelGGL((k_mx_few<kT, kSwiglu, kMode != kScale1>), dim3((unsigned)slots_of(g, 32), nblk(g.N, 32)),
+        hipLaunchKernelGGL((k_mx_few<kT, kSwiglu, kMode != kScale1>), dim3((unsigned)slots_of(g, kFewRows), nblk(g.N, 32)),
                            dim3(64 * kFewWaves), 0, st, g);
         return hipGetLastError();
     }
