@@ -12,10 +12,9 @@
 // two operations per weight, far below the matrix cores' rate.  So the activations are
 // carried with more bits than a quantised product would need: a block of 32 values is held
 // as integers times one power of two, split into signed bytes ("limbs"), and the int8
-// matrix instruction multiplies the limbs with the 4-bit codes exactly.  The limbs of
-// several tokens fill the 32 rows of one instruction, which at these row counts would idle
-// otherwise.  Per 32-block the limb sums are joined exactly in integers and scaled into an
-// fp32 accumulator.
+// matrix instruction multiplies the limbs with the 4-bit codes exactly.  The limbs of a
+// few tokens share the rows of one instruction, which would idle otherwise.  Per 32-block the
+// limb sums are joined exactly in integers and scaled into an fp32 accumulator.
 //   fp32 activations: 24 bits, three limbs (error at most 2^-23 of the block's largest value)
 //   bf16 and fp16: 16 bits, two limbs (2^-15 of the block's largest value: an eighth of an
 //   fp16's own last place there; a third limb costs the sums half as much again and the
@@ -459,6 +458,10 @@ __device__ __forceinline__ void store_h(const GateUpArgs& g, int p, int fb, floa
 // registers -- and turns the token's x into fixed point in LDS, so that no launch comes before
 // it.  Pairs of the same expert each read its weights (from a cache).  The workgroups of
 // f-block 0 and slot 0 leave the token's routing for the next kernel.
+//
+// One token, 8 experts of d = 2048, f = 768 (14 MB): 7.7 us, of which the weights' bytes are 3;
+// the rest is the launch, the logits' way and eight slots' routing, the sums.  d = 4096,
+// f = 1536 (57 MB): 14.9 us, 3.8 TB/s.
 template <int kT, int kPairWaves>
 __global__ __launch_bounds__(64 * kPairWaves) void k_decode_pair_gate_up(GateUpArgs g)
 {
@@ -576,6 +579,9 @@ constexpr int chunk_lds(int K) { return Limbs<NL>::kTokens * (NL * (K + kActPad)
 // fixed number of workgroups goes through the items, since only the device knows how many there
 // are; the chunks of an expert follow each other at a multiple of 8 workgroups, so that one XCD
 // reads a tile for all of them (the first from memory, the others from its L2).
+//
+// 24 tokens of d = 4096, f = 1536, some 35 of 256 experts reached, bf16 (370 MB): gate/up 75 us, down
+// 46; what bounds it is memory (3 TB/s) with the expansion of the codes and the sums' join close behind.
 constexpr int kChunkWaves = 4;
 
 template <int NL, bool kGateUp>
@@ -671,8 +677,10 @@ __global__ __launch_bounds__(64 * kChunkWaves) __attribute__((amdgpu_waves_per_e
 // ------------------------------------------- few pairs: down and combine in one ---
 // A workgroup owns 32 columns of y for all tokens.  Its 16 waves take the (pair, K split) units
 // in turn, the pairs' h in LDS, and leave the units' rows there, where each token's slots are
-// added up in slot order.
+// added up in slot order.  One token, 8 experts of d = 2048, f = 768 (7 MB): 7.3 us; d = 4096,
+// f = 1536 (28 MB): 10.5 us.
 constexpr int kPairDownWaves = 16;
+constexpr int kFusedPairs = 8;                            // pairs, at most
 
 struct PairDownLds {
     int hl, hs, dm, bytes;
@@ -689,9 +697,8 @@ template <int kT>
 __global__ __launch_bounds__(64 * kPairDownWaves) void k_decode_pair_down(DownArgs g)
 {
     constexpr int NL = limbs_of(kT);
-    constexpr int kMost = 64;                             // pairs, at most
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    __shared__ float s_w[kMost];
+    __shared__ float s_w[kFusedPairs];
     const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, j32 = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int R = g.T * g.k, nb = g.f / 32, npairs = k_pairs(g.f), nt = blockIdx.x;
@@ -791,16 +798,31 @@ unsigned nblk(int64_t n, int per) { return (unsigned)((n + per - 1) / per); }
 // ----------------------------------------------------------------- launches ---
 namespace {
 
-// Tokens from which the route kernel pays: below it every pair's workgroups route for
-// themselves and pairs that share an expert read its weights again.
-constexpr int kPairTokens = 6;
-// Column tiles from which one workgroup a tile fills enough of the chip, and the pairs up to
-// which it does so faster than a wave for every (pair, two tiles) and a combine.
-constexpr int kPairDownTiles = 64;
-constexpr int kPairDownPairs = 16;
-constexpr int kPairDownLds = 96 << 10;
+// Pairs by themselves need no route kernel, but those that share an expert read its weights again,
+// from a cache.  With experts drawn alike the re-reads are (R - D) experts' bytes, D = E (1 - (1 - k / E)^T)
+// the experts reached; about 100 MB of them cost what the route kernel does, whatever the sizes.  Chunks
+// against pairs: 4096 x 1536, 8 of 256 experts, 8 tokens (63 MB) 125 us, 118, 12 tokens (160 MB) 162, 170; 8 of
+// 32, 4 tokens (107 MB) 52, 55; 2048 x 768, 8 of 16, 6 tokens (85 MB) 27, 25, 7 tokens (106 MB) 27.6, 28.3;
+// 1024 x 512, 2 of 8, 16 tokens (21 MB) 19, 13.
+constexpr double kPairReread = 100e6;
+constexpr int kPairMost = 128;                            // as far as that was measured
 
-bool by_pairs(const DecodeLaunch& D) { return D.T <= kPairTokens && !D.need_counts; }
+// The fused down and combine (a workgroup a column tile) against a wave for every (pair, K split) of two
+// tiles and a combine: it saves a launch and wins while its workgroups fill some of the chip and have little
+// to do each.  Fused, not: 1024 x 512, 2 pairs 9.3 us, 11.0, 10 pairs 11.9, 11.5; 4096 x 1536, 8 pairs 23.7,
+// 24.6, 24 pairs 45, 39; 512 x 256 (16 tiles), 6 pairs 10.7, 10.6; 4096 x 4096, 6 pairs (56 KB of h) 33, 36, 8
+// pairs (74 KB) 41, 37.
+constexpr int kFusedTiles = 32;
+constexpr int kFusedLds = 64 << 10;
+
+bool by_pairs(const DecodeLaunch& D)
+{
+    const int R = D.T * D.k;
+    if (R > kPairMost || D.need_counts) return false;
+    double missed = 1.0;                                  // the share of experts no token reaches
+    for (int t = 0; t < D.T; ++t) missed *= 1.0 - (double)D.k / D.E;
+    return (R - D.E * (1.0 - missed)) * (double)D.expert_stride <= kPairReread;
+}
 
 // K splits that give every wave of the fused down kernel a unit
 int down_ksplit(const DecodeLaunch& D)
@@ -814,8 +836,8 @@ int down_ksplit(const DecodeLaunch& D)
 bool down_fused(const DecodeLaunch& D)
 {
     const int R = D.T * D.k;
-    return by_pairs(D) && D.d / 32 >= kPairDownTiles && R <= kPairDownPairs &&
-           PairDownLds(R, D.f, limbs_of(D.dtype), down_ksplit(D)).bytes <= kPairDownLds;
+    return by_pairs(D) && D.d / 32 >= kFusedTiles && R <= kFusedPairs &&
+           PairDownLds(R, D.f, limbs_of(D.dtype), down_ksplit(D)).bytes <= kFusedLds;
 }
 
 RouteArgs route_args(const DecodeLaunch& D)

@@ -33,7 +33,9 @@ __device__ __forceinline__ float e8m0(uint32_t s)
 }
 
 // ---------------------------------------------------- quantise, dequantise ---
-// Four lanes per block, eight values each; a wave takes 16 consecutive blocks.
+// Four lanes per block, eight values each; a wave takes 16 consecutive blocks.  One pass, one read
+// and one write of everything, so memory bounds it: 8192 x 4096 fp32 (152 MB) 28 us either way,
+// 5.5 TB/s, next to the 5.2 of a copy kernel over a gigabyte; one row 1.5 us, a launch's time.
 constexpr int kQuantThreads = 256;
 constexpr int kQuantBlocks = kQuantThreads / 4;           // blocks per workgroup
 
@@ -250,6 +252,11 @@ struct MxLds {
 // stages of a tile issue the first two of the next, whose pointers are made under the products,
 // and the epilogue's stores drain under them.  (A workgroup a tile spent 14 us of 43 a tile of
 // 8192 x 4096 x 4096 on its start, its first loads and its stores.)
+//
+// What bounds it: large dense products the matrix cores -- 8192 x 4096 x 4096, bf16 out, 91 us or
+// 3.0 PFLOP/s, 4.4 as K grows; the instruction alone on random codes reaches 5.6 to 6.7 on all CUs,
+// where power holds the clock (10 on zeros).  Grouped ones memory, in latency more than in rate --
+// 24576 rows in 256 groups (N = 4096, K = 1536, fp32 out) move 1.0 GB in 337 us, 3.0 TB/s.
 template <class S, int kT, bool kSwiglu, int kMode>
 __global__ __launch_bounds__(64 * S::NW) void k_mx_tile(MxGemm a, int n_tiles, int64_t n_slots)
 {
@@ -700,7 +707,9 @@ __global__ __launch_bounds__(64 * S::NW) void k_mx_tile(MxGemm a, int n_tiles, i
 // Up to 32 rows of a group by 32 columns (SwiGLU: 32 gate and 32 up rows of B) per
 // workgroup; its waves take every eighth run of 256 codes of K, fed straight from memory,
 // and add up through LDS in wave order.  What bounds it is B's bytes, read once: lane half
-// h takes blocks 4 h + s of a run, 64 consecutive bytes of a row in four loads.
+// h takes blocks 4 h + s of a run, 64 consecutive bytes of a row in four loads.  At 1 row of
+// 4096 x 4096 (8.9 MB, 1.9 us at a copy's rate) its 5.6 us are mostly latency: a launch, the
+// operands' first bytes, the waves' sums.
 constexpr int kFewWaves = 8, kFewRows = 32;
 
 // Groups of a row table: row slot s belongs to the last group g whose first slot
@@ -885,7 +894,7 @@ hipError_t launch_shape(const MxGemm& g, hipStream_t st)
     const bool far = (g.rows || g.row_div > 1) && g.a_rows * (g.K / 2) > (int64_t)UINT32_MAX;
     // Fewer tiles than a quarter of the CUs: the few-row kernel's workgroups are narrower and their
     // waves share K.  64 x 4096 x 4096: 8.3 us against 10.9; 128 rows (64 tiles): 13.6 against 11.1;
-    // 64 groups of 8 rows, N = K = 2048 (more than 1024 tiles): 47 against 34.
+    // 64 groups of 8 rows, N = K = 2048 (more than 1024 tiles): 48 against 30.
     if (far || (rows <= 64 && tiles(64, 128) < 64)) {
         hipLaunchKernelGGL((k_mx_few<kT, kSwiglu, kMode != kScale1>), dim3((unsigned)slots_of(g, kFewRows), nblk(g.N, 32)),
                            dim3(64 * kFewWaves), 0, st, g);
@@ -893,11 +902,12 @@ hipError_t launch_shape(const MxGemm& g, hipStream_t st)
     }
     // 256 x 256 tiles move the fewest bytes a product but start and end slowest: worth it over
     // several stages and tiles that fill the chip more than once.  8192 x 4096 at K = 4096: 96 us
-    // against 104 of 128 x 128 tiles, K = 1024: 42 against 33; 4096 x 4096 x 4096 (256 tiles): 51, 50.
+    // against 104 of 128 x 128 tiles, K = 1024: 42 against 33; 4096 x 4096 x 4096 (256 tiles): 51, 50;
+    // 64 groups of 256 rows, N = K = 2048 (512 tiles): 91, 83.
     if (rows >= 320 && g.K >= 2048 && tiles(256, 256) >= 384) return launch_tile<Tile256, kT, kSwiglu, kMode>(g, st);
     // 128 x 128 tiles where they fill the chip's two workgroups a CU and the rows fill a good part of
-    // a tile: 2048 x 4096 x 4096 28 us against 33 of 64 x 128, 64 groups of 64 rows (N = K = 2048)
-    // 46 against 53; 512 x 4096 x 4096 (128 tiles) 18 against 15.5, 64 groups of 24 rows 38 against 36.
+    // a tile: 2048 x 4096 x 4096 28 us against 33 of 64 x 128, 64 groups of 96 rows (N = K = 2048)
+    // 49 against 53, of 48 37, 38; 512 x 4096 x 4096 (128 tiles) 18 against 15, 64 groups of 24 rows 36, 31.
     if (rows >= 40 && tiles(128, 128) >= 512) return launch_tile<Tile128, kT, kSwiglu, kMode>(g, st);
     return launch_tile<Tile64, kT, kSwiglu, kMode>(g, st);
 }

@@ -129,7 +129,29 @@ def test_many_rows_and_many_experts(layers, T, shape):
 
 
 @gpu
-@pytest.mark.parametrize("T", [1, 3, 8])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,shape", [(40, (64, 96, 4, 4)), (66, (96, 64, 5, 2)), (70, (224, 160, 3, 2)), (33, (1184, 352, 12, 4)), (17, (2048, 768, 9, 8)),
+                                     (140, (32, 32, 1, 1))])
+def test_more_than_128_pairs(layers, T, shape, dtype):
+    L, h, blob = layers(*shape)
+    x, lg = inputs(T, L, dtype, seed=T)
+    y, ex = run(L, h, x, lg, blob, pad=16)
+    check(y, ex, L, x, lg)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T", [3, 5])
+def test_wide_experts_shared_by_few_tokens(layers, T, dtype):
+    """Experts of 28 MB, 2 of 3 a token: read again for every token, or once for all."""
+    L, h, blob = layers(4096, 4096, 3, 2)
+    x, lg = inputs(T, L, dtype, seed=T)
+    y, ex = run(L, h, x, lg, blob)
+    check(y, ex, L, x, lg)
+
+
+@gpu
+@pytest.mark.parametrize("T", [1, 3, 8, 72])
 def test_masks_ties_and_extreme_logits(layers, T):
     L, h, blob = layers(96, 64, 5, 2)
     low = torch.finfo(torch.float32).min
@@ -147,9 +169,10 @@ def test_masks_ties_and_extreme_logits(layers, T):
 
 
 @gpu
-def test_infinities_and_nan_stay_in_their_token(layers):
+@pytest.mark.parametrize("T", [5, 80])
+def test_infinities_and_nan_stay_in_their_token(layers, T):
     L, h, blob = layers(96, 64, 5, 2)
-    x, lg = inputs(5, L, torch.float32)
+    x, lg = inputs(T, L, torch.float32)
     clean, _ = run(L, h, x, lg, blob)
     x2, lg2 = x.clone(), lg.clone()
     x2[1, 3], x2[3, 95] = math.nan, math.inf
@@ -157,7 +180,7 @@ def test_infinities_and_nan_stay_in_their_token(layers):
     x2[4] = math.nan                                      # an empty slot of a padded batch: whatever it holds
     y, _ = run(L, h, x2, lg2, blob)
     assert torch.isnan(y[[1, 3]]).all()
-    assert torch.equal(y[[0, 2]], clean[[0, 2]])
+    assert torch.equal(y[[0, 2]], clean[[0, 2]]) and torch.equal(y[5:], clean[5:])
     assert (y[4] == 0).all()
 
 
@@ -188,9 +211,10 @@ def test_a_block_of_mixed_magnitudes(layers):
 
 
 @gpu
-def test_y_may_be_x_and_runs_repeat_bit_for_bit(layers):
+@pytest.mark.parametrize("T", [1, 6, 30])
+def test_y_may_be_x_and_runs_repeat_bit_for_bit(layers, T):
     L, h, blob = layers(2048, 768, 9, 8)
-    x, lg = inputs(6, L, torch.bfloat16)
+    x, lg = inputs(T, L, torch.bfloat16)
     y, _ = run(L, h, x, lg, blob)
     for _ in range(3):
         xd = x.cuda()
@@ -258,9 +282,9 @@ def test_pool_layers_equal_resident_ones(active_only):
 
 
 @gpu
-def test_two_graphs_with_their_own_workspaces_and_an_eager_call_between(layers):
+def test_graphs_with_their_own_workspaces_and_an_eager_call_between(layers):
     L, h, blob = layers(1184, 352, 12, 4)
-    T = (1, 7)
+    T = (1, 7, 50)
     xs = [torch.empty(t, L.d, device="cuda") for t in T]
     ls = [torch.empty(t, L.E, device="cuda") for t in T]
     ys = [torch.empty(t, L.d, device="cuda") for t in T]
@@ -283,8 +307,8 @@ def test_two_graphs_with_their_own_workspaces_and_an_eager_call_between(layers):
         for ws in (w for _, w in graphs):
             ws.fill_(255)                                 # what a workspace holds does not matter
         torch.cuda.synchronize()
-        streams = [torch.cuda.Stream(), torch.cuda.Stream()]
-        for (g, _), s in zip(graphs, streams):            # both at once, on two streams
+        streams = [torch.cuda.Stream() for _ in T]
+        for (g, _), s in zip(graphs, streams):            # all at once, on streams of their own
             with torch.cuda.stream(s):
                 g.replay()
         torch.cuda.synchronize()
@@ -297,7 +321,7 @@ def test_two_graphs_with_their_own_workspaces_and_an_eager_call_between(layers):
 
 @gpu
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("T,d,f", [(1, 16384, 32), (1, 32, 16384), (7, 16384, 32), (7, 32, 16384), (2, 16384, 1024)])
+@pytest.mark.parametrize("T,d,f", [(1, 16384, 32), (1, 32, 16384), (7, 16384, 32), (7, 32, 16384), (129, 16384, 32), (129, 32, 16384), (2, 16384, 1024)])
 def test_longest_rows(layers, T, d, f, dtype):
     L, h, blob = layers(d, f, 2, 1)
     x, lg = inputs(T, L, dtype, seed=T)
