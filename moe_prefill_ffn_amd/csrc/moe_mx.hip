@@ -253,10 +253,10 @@ struct MxLds {
 // and the epilogue's stores drain under them.  (A workgroup a tile spent 14 us of 43 a tile of
 // 8192 x 4096 x 4096 on its start, its first loads and its stores.)
 //
-// What bounds it: large dense products the matrix cores -- 8192 x 4096 x 4096, bf16 out, 91 us or
-// 3.0 PFLOP/s, 4.4 as K grows; the instruction alone on random codes reaches 5.6 to 6.7 on all CUs,
-// where power holds the clock (10 on zeros).  Grouped ones memory, in latency more than in rate --
-// 24576 rows in 256 groups (N = 4096, K = 1536, fp32 out) move 1.0 GB in 337 us, 3.0 TB/s.
+// What bounds it: large dense products the matrix cores -- 8192 x 4096 x 4096, bf16 out, 85 to 92 us or
+// 3.1 PFLOP/s, 4.4 as K grows; the instruction alone on random codes reaches 5.6 to 6.7 on all CUs,
+// where power holds the clock (10 on zeros).  Grouped ones memory -- 24576 rows in 256 groups
+// (N = 4096, K = 1536, fp32 out) move 1.28 GB in 334 us, 3.8 TB/s.
 template <class S, int kT, bool kSwiglu, int kMode>
 __global__ __launch_bounds__(64 * S::NW) void k_mx_tile(MxGemm a, int n_tiles, int64_t n_slots)
 {
