@@ -65,6 +65,8 @@ struct DecodeLaunch {
 
 // Routing, the chunk table and x's fixed-point form; nothing where the products route themselves.
 hipError_t launch_decode_route(const DecodeLaunch& D, hipStream_t st);
+// The experts with rows from the pinned host blob into the slot that D reads, after a route with need_counts.
+hipError_t launch_decode_load(const DecodeLaunch& D, const uint8_t* src, uint8_t* dst, unsigned long long* stats, hipStream_t st);
 // Both expert products (the last reader of the weights), and the combine where they hold it.
 hipError_t launch_decode_products(const DecodeLaunch& D, hipStream_t st);
 // The combine, where the products left it.

@@ -30,6 +30,11 @@
 
 namespace moe {
 
+// The active-expert load of the prompt path (moe_kernels.hip).
+__global__ __launch_bounds__(256) void k_expert_load(const uint8_t* __restrict__ src, uint8_t* __restrict__ dst,
+                                                     const int32_t* __restrict__ counts, int E, uint64_t expert_bytes,
+                                                     unsigned long long* __restrict__ stats);
+
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v16i __attribute__((ext_vector_type(16)));
 
@@ -990,6 +995,13 @@ hipError_t combine_typed(const DecodeLaunch& D, hipStream_t st)
 hipError_t launch_decode_route(const DecodeLaunch& D, hipStream_t st)
 {
     return D.dtype == kF32 ? route_typed<kF32>(D, st) : D.dtype == kBF16 ? route_typed<kBF16>(D, st) : route_typed<kF16>(D, st);
+}
+
+hipError_t launch_decode_load(const DecodeLaunch& D, const uint8_t* src, uint8_t* dst, unsigned long long* stats, hipStream_t st)
+{
+    hipLaunchKernelGGL(k_expert_load, dim3(512), dim3(256), 0, st, src, dst, reinterpret_cast<const int32_t*>(D.ws + D.L.counts), D.E,
+                       D.expert_stride, stats);
+    return hipGetLastError();
 }
 
 hipError_t launch_decode_products(const DecodeLaunch& D, hipStream_t st)

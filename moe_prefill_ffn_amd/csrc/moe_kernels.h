@@ -76,9 +76,6 @@ enum KernelId { kRouteQuant, kGroup, kExpertLoad, kScatter, kGemmGateUp, kGemmDo
 // GU GEMM with SwiGLU+Q8, down GEMM (last reader of the weights) -- everything up to the combine.
 // The kExpertLoad mark is recorded whether or not that kernel runs.
 hipError_t launch_layer(const LayerLaunch& L, hipStream_t st);
-// the active-expert load alone: experts with counts[e] > 0 from the pinned host blob into the slot
-hipError_t launch_expert_load(const uint8_t* src, uint8_t* dst, const int32_t* counts, int E, uint64_t expert_bytes,
-                              unsigned long long* stats, hipStream_t st);
 // combine (and clear the membership mask for the next layer)
 hipError_t launch_combine(const LayerLaunch& L, hipStream_t st);
 hipError_t launch_fill_u32(uint32_t* p, int64_t n, uint32_t v, hipStream_t st);

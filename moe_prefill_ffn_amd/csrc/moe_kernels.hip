@@ -1022,13 +1022,6 @@ static inline void mark(const LayerLaunch& L, int i, hipStream_t st)
     if (L.marks) (void)hipEventRecord(L.marks[i], st);
 }
 
-hipError_t launch_expert_load(const uint8_t* src, uint8_t* dst, const int32_t* counts, int E, uint64_t expert_bytes,
-                              unsigned long long* stats, hipStream_t st)
-{
-    hipLaunchKernelGGL(k_expert_load, dim3(512), dim3(256), 0, st, src, dst, counts, E, expert_bytes, stats);
-    return hipGetLastError();
-}
-
 hipError_t launch_layer(const LayerLaunch& L, hipStream_t st)
 {
     const int64_t R = (int64_t)L.T * L.k;
@@ -1042,10 +1035,9 @@ hipError_t launch_layer(const LayerLaunch& L, hipStream_t st)
     hipLaunchKernelGGL(k_group, dim3(L.E), dim3(kGroupThreads), 0, st, L.mask, L.W, L.wprefix,
                        L.counts);
     mark(L, kExpertLoad, st);
-    if (L.load_src) {
-        const hipError_t e = launch_expert_load(L.load_src, L.load_dst, L.counts, L.E, L.expert_stride, L.load_stats, st);
-        if (e != hipSuccess) return e;
-    }
+    if (L.load_src)
+        hipLaunchKernelGGL(k_expert_load, dim3(512), dim3(256), 0, st, L.load_src, L.load_dst, L.counts,
+                           L.E, L.expert_stride, L.load_stats);
     mark(L, kScatter, st);
     hipLaunchKernelGGL(k_scatter, dim3(nblk(R, 256)), dim3(256), 0, st, L.eidx, R, L.k, L.mask,
                        L.wprefix, L.counts, L.E, L.W, L.bounds, L.tiles, L.ntiles, L.rows, L.pos,

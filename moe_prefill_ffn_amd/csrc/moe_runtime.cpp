@@ -1081,8 +1081,7 @@ int moe_decode_run_layer(moe_prefill_t* h, const moe_decode_io_t* io_in, void* s
         D.need_counts = W.sparse_slot >= 0;
         hipError_t e = launch_decode_route(D, st);
         if (e == hipSuccess && W.sparse_slot >= 0)
-            e = launch_expert_load(h->blobs_dev[io.layer], h->pool + (uint64_t)W.sparse_slot * h->slot_bytes,
-                                   reinterpret_cast<const int32_t*>(D.ws + D.L.counts), h->E, h->B.expert_bytes,
+            e = launch_decode_load(D, h->blobs_dev[io.layer], h->pool + (uint64_t)W.sparse_slot * h->slot_bytes,
                                    reinterpret_cast<unsigned long long*>(h->ws + h->L.load_stats), st);
         if (e == hipSuccess) e = launch_decode_products(D, st);
         if (e != hipSuccess) return hip_fail(h, e, "decode: launch");
