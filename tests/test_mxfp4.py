@@ -296,6 +296,47 @@ def test_indices_outside_are_clamped_and_stay_inside():
 
 
 @gpu
+@pytest.mark.parametrize("M,N", [(700, 64), (30000, 400)])
+def test_bounds_that_are_not_sound_stay_inside(M, N):
+    """Groups that overlap, run backwards or leave [0, M], in the tiled kernels: the rows before and behind
+    out[5:M + 5] and the columns beside it keep what they held."""
+    g = gen(8)
+    a, b = [t.cuda() for t in random_mx(g, M, 64)], [t.cuda() for t in random_mx(g, 5, N, 64)]
+    buf = torch.full((M + 10, N + 8), 77.0, device="cuda")
+    out = buf[5:M + 5, :N]
+    for bad in ([0, M, 0, M, 0, M], [-7, 2, M + 9, 4, M, M], [M, 300, 200, 100, 50, 0], [0, 1 << 30, -(1 << 30), 1 << 30, M, 2 * M],
+                [M // 2, M // 2, M + 1, 1 << 30, 1 << 30, 1 << 30], [-(1 << 31), (1 << 31) - 1, -(1 << 31), (1 << 31) - 1, 0, M]):
+        mp.moe_mxfp4_gemm(*a, *b, out, bounds=torch.tensor(bad).int().cuda())
+        torch.cuda.synchronize()
+        assert (buf[:5] == 77).all() and (buf[M + 5:] == 77).all() and (buf[:, N:] == 77).all()
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K,G", [(3000, 300, 512, 12), (9000, 1100, 288, 40), (60, 200, 256, 6)])
+def test_grouped_product_in_a_replayed_graph_with_other_bounds(M, N, K, G):
+    """What the rows are is read when the graph runs, not when it is captured."""
+    g = gen(M)
+    a, b = [t.cuda() for t in random_mx(g, M, K, hi=120)], [t.cuda() for t in random_mx(g, G, 2 * N, K, hi=120)]
+    bounds, rows = groups_of("even", G, M, g).cuda(), torch.arange(M).int().cuda()
+    out = torch.full((M, N), 77.0, dtype=torch.bfloat16, device="cuda")
+    run = lambda o: mp.moe_mxfp4_gemm(*a, *b, o, bounds=bounds, rows=rows, swiglu=True)  # noqa: E731
+    run(torch.empty_like(out))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(out)
+    for kind in ("random", "one", "part", "even"):
+        bounds.copy_(groups_of(kind, G, M, g))
+        rows.copy_(torch.randperm(M, generator=g).int())
+        out.fill_(77.0)
+        graph.replay()
+        want = torch.full_like(out, 77.0)
+        run(want)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), kind
+
+
+@gpu
 def test_nan_blocks_reach_their_rows_and_columns_only():
     g = gen(6)
     ac, asc = random_mx(g, 40, 128)
