@@ -401,6 +401,25 @@ def _stream_of(stream: Optional[torch.cuda.Stream], index: int) -> int:
     return stream.cuda_stream
 
 
+def _scratch(shape, dtype, index: int, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """Memory for work on ``stream``, from that stream's own pool: a block of the current stream's may
+    have been freed under kernels that are still queued there, and ``stream`` does not wait for them."""
+    device = torch.device("cuda", index)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _result(shape, dtype, index: int, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """_scratch() that is handed to the caller, who goes on with it on the current stream: freed there,
+    it is not used again before that stream's work on it is done."""
+    t = _scratch(shape, dtype, index, stream)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(index))
+    return t
+
+
 def _rows_of(t: torch.Tensor, name: str, rows: int, cols: int, index: int) -> int:
     """Row stride of a [rows, cols] matrix on device `index` whose rows are contiguous."""
     if t.shape != (rows, cols):
@@ -435,7 +454,7 @@ def moe_decode_run_layer(handle: Handle, x: torch.Tensor, logits: torch.Tensor, 
     x, y: [T, d_model] fp32, bf16 or fp16, the same type (rows may be strided, 16-byte aligned);
     logits: [T, n_experts] fp32, -inf where an expert is not available.  ``workspace``: device
     uint8 scratch of moe_decode_workspace_size() bytes that no other call in flight uses;
-    without one the call takes it from torch's allocator.  exports: "eidx" int32 and
+    without one the call takes it from torch's allocator, on ``stream``.  exports: "eidx" int32 and
     "weights" fp32, [T, top_k] each."""
     P = handle.params
     d, E, k, index = P["d_model"], P["n_experts"], P["top_k"], P["device"]
@@ -460,9 +479,7 @@ def moe_decode_run_layer(handle: Handle, x: torch.Tensor, logits: torch.Tensor, 
     raw = _stream_of(stream, index)
     if workspace is None:
         if 0 < T * k <= MOE_DECODE_MAX_PAIRS:
-            workspace = torch.empty(moe_decode_workspace_size(d, P["d_ff"], E, k, T), dtype=torch.uint8, device=x.device)
-            if stream is not None:
-                workspace.record_stream(stream)
+            workspace = _scratch(moe_decode_workspace_size(d, P["d_ff"], E, k, T), torch.uint8, index, stream)
     elif workspace.get_device() != index:
         raise TypeError(f"workspace: expected a tensor on device {index}")
     ws, ws_bytes = (_dev_ptr(workspace, torch.uint8, "workspace"), workspace.numel()) if workspace is not None else (None, 0)
@@ -505,13 +522,6 @@ def _mx_matrix(values, codes, scales, M, K, index) -> moe_mxfp4_matrix_t:
                               _mx_bytes(codes, "codes", (M, K // 2), index), _mx_bytes(scales, "scales", (M, K // 32), index))
 
 
-def _new(shape, dtype, index, stream) -> torch.Tensor:
-    t = torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
-    if stream is not None:
-        t.record_stream(stream)
-    return t
-
-
 def moe_mxfp4_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
                        scales: Optional[torch.Tensor] = None,
                        stream: Optional[torch.cuda.Stream] = None):
@@ -520,11 +530,12 @@ def moe_mxfp4_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
     if x.dim() != 2:
         raise ValueError("x: expected a matrix")
     M, K = x.shape
+    raw = _stream_of(stream, index)
     if codes is None:
-        codes = _new((M, K // 2), torch.uint8, index, stream)
+        codes = _result((M, K // 2), torch.uint8, index, stream)
     if scales is None:
-        scales = _new((M, K // 32), torch.uint8, index, stream)
-    rc = lib().moe_mxfp4_quantize(_mx_matrix(x, codes, scales, M, K, index), _stream_of(stream, index))
+        scales = _result((M, K // 32), torch.uint8, index, stream)
+    rc = lib().moe_mxfp4_quantize(_mx_matrix(x, codes, scales, M, K, index), raw)
     if rc:
         _check(rc)
     return codes, scales
@@ -539,9 +550,10 @@ def moe_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, out: Optiona
         raise ValueError("codes: expected a matrix")
     M, K = codes.shape
     K *= 2
+    raw = _stream_of(stream, index)
     if out is None:
-        out = _new((M, K), dtype, index, stream)
-    rc = lib().moe_mxfp4_dequantize(_mx_matrix(out, codes, scales, M, K, index), _stream_of(stream, index))
+        out = _result((M, K), dtype, index, stream)
+    rc = lib().moe_mxfp4_dequantize(_mx_matrix(out, codes, scales, M, K, index), raw)
     if rc:
         _check(rc)
     return out
@@ -572,8 +584,9 @@ def moe_mxfp4_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch
         raise ValueError("b_codes: swiglu needs gate and up rows, an even number")
     N = NB // 2 if swiglu else NB
     M = rows.shape[0] if rows is not None else A * top_k
+    raw = _stream_of(stream, index)
     if out is None:
-        out = _new((M, N), dtype, index, stream)
+        out = _result((M, N), dtype, index, stream)
     out_dtype = _DTYPE_ID.get(out.dtype)
     if out_dtype is None:
         raise TypeError("out: expected float32, bfloat16 or float16")
@@ -591,7 +604,7 @@ def moe_mxfp4_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch
         A, _mx_bytes(b_codes, "b_codes", (*b_shape[:-1], K2), index), _mx_bytes(b_scales, "b_scales", (*b_shape[:-1], K // 32), index),
         bounds.data_ptr() if bounds is not None else None, rows.data_ptr() if rows is not None else None, G, top_k, M, N, K,
         1 if swiglu else 0, out_dtype, out.data_ptr(), _rows_of(out, "out", M, N, index))
-    rc = lib().moe_mxfp4_gemm(a, _stream_of(stream, index))
+    rc = lib().moe_mxfp4_gemm(a, raw)
     if rc:
         _check(rc)
     return out
