@@ -244,11 +244,11 @@ enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 };
  *     are read for it.  A token with no expert available (an empty slot of a
  *     padded batch) gets y = 0.
  *   - Activations are not quantised to 8 bits: x and the SwiGLU output enter the
- *     products as integers per block of 32, 24 bits for fp32 x (error at most
- *     2^-23 of the block's largest magnitude), 16 bits for bf16 and fp16 x
- *     (2^-15), and all sums are fp32, so y is the layer of the 4-bit weights to
- *     about the rounding of its type.  moe_prefill_run_layer's y differs from it
- *     by that path's Q8 rounding of x and h.
+ *     products as 24-bit integers per block of 32 for every type of x (error at
+ *     most 1.01 * 2^-23 of the block's largest magnitude, 2^-127 where that is
+ *     below 2^-104), and all sums are fp32, so y is the layer of the 4-bit
+ *     weights to about the rounding of its type.  moe_prefill_run_layer's y
+ *     differs from it by that path's Q8 rounding of x and h.
  *   - A block of 32 values of x that holds an infinity or a NaN makes the
  *     token's y NaN; so does an h that leaves the fp32 range.
  *   - Deterministic: the same bits on every run.

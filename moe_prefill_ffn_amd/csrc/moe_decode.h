@@ -9,14 +9,16 @@
 namespace moe {
 
 constexpr int kDecodeMaxPairs = 1024;   // n_tokens * top_k of one call
-constexpr int kChunkRows = 4;           // most rows of one expert that share one read of its weights
-constexpr int kChunkRowsF32 = 2;        // ... of fp32 activations (three limbs a row instead of two)
+// Most rows of one expert that share one read of its weights.  Two fill one result register quad of
+// each lane half and 26 KB of LDS at 4096 columns; four cost a quad more and the LDS of a workgroup a CU:
+// 4096 x 1536, 8 of 256 experts, 16 tokens 201 us against 230 of four rows, 24 alike 278 against 302, 24
+// skewed 149, 146, 128 tokens 824, 762; at 16384 columns four do not fit.
+constexpr int kChunkRows = 2;
 
 // One work item of the expert products: (token, slot) pairs of one expert.
 struct DecodeChunk {
     int32_t expert, n;
-    int32_t pair[kChunkRows];
-    int32_t pad[2];            // 32 bytes
+    int32_t pair[kChunkRows];  // 16 bytes
 };
 
 struct DecodeWs {
@@ -28,8 +30,8 @@ static inline DecodeWs decode_ws(int d, int f, int E, int k, int T)
 {
     DecodeWs L;
     const uint64_t R = (uint64_t)T * k;
-    // sum over experts of ceil(rows / 2): at most one partial chunk per reached expert
-    L.max_chunks = (int)(R / kChunkRowsF32) + (int)(R < (uint64_t)E ? R : (uint64_t)E);
+    // sum over experts of ceil(rows / kChunkRows): at most one partial chunk per reached expert
+    L.max_chunks = (int)(R / kChunkRows) + (int)(R < (uint64_t)E ? R : (uint64_t)E);
     uint64_t o = 0;
     auto take = [&](uint64_t bytes) { uint64_t at = o; o = align_up(o + bytes, 256); return at; };
     L.eidx = take(R * 4);

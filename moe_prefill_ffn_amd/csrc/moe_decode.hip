@@ -11,14 +11,14 @@
 // What bounds it: the bytes of the experts reached (0.5625 per weight); a token brings
 // two operations per weight, far below the matrix cores' rate.  So the activations are
 // carried with more bits than a quantised product would need: a block of 32 values is held
-// as integers times one power of two, split into signed bytes ("limbs"), and the int8
-// matrix instruction multiplies the limbs with the 4-bit codes exactly.  The limbs of a
+// as 24-bit integers times one power of two, split into three signed bytes ("limbs"), and the
+// int8 matrix instruction multiplies the limbs with the 4-bit codes exactly.  The limbs of a
 // few tokens share the rows of one instruction, which would idle otherwise.  Per 32-block the
-// limb sums are joined exactly in integers and scaled into an fp32 accumulator.
-//   fp32 activations: 24 bits, three limbs (error at most 2^-23 of the block's largest value)
-//   bf16 and fp16: 16 bits, two limbs (2^-15 of the block's largest value: an eighth of an
-//   fp16's own last place there; a third limb costs the sums half as much again and the
-//   output's rounding hides it)
+// limb sums are joined and scaled into an fp32 accumulator.  A value is off by at most 1.01 * 2^-23 of
+// its block's largest: bf16 x down to 2^-15 of it and fp16 x down to 2^-12 is exact.  (Two limbs
+// for 16-bit types, 2^-15 of the largest: their error next to a large value is not hidden by the
+// output's rounding where that value's weight is small.  A block's value 300 times the others, its
+// weights smaller in proportion: 1e-3 of the output, six roundings of fp16.)
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -41,49 +41,39 @@ typedef int v16i __attribute__((ext_vector_type(16)));
 namespace {
 
 // -------------------------------------------------------------- fixed point ---
-// NL limbs: integers q of 8 NL bits.  Exponent field of the scale of a block whose largest
-// magnitude has the fp32 bits u: with E = that field, the value is q * 2^(E - 125 - 8 NL) and
-// |q| <= 0x7F7F7F (0x7F7F), so that signed bytes hold it.  2^17 added to the mantissa moves
-// the top 1/64 of a binade to the next one (q would pass that).  E >= 8 NL - 1 keeps the
-// scale normal.
-template <int NL>
+// Integers q of 24 bits in three limbs.  Exponent field of the scale of a block whose largest
+// magnitude has the fp32 bits u: with E = that field, the value is q * 2^(E - 149) and
+// |q| <= 0x7F7F7F, so that signed bytes hold it.  2^17 added to the mantissa moves the top 1/64
+// of a binade to the next one (q would pass that).  E >= 23 keeps the scale normal: below a
+// largest value of 2^-104 the last place stays at 2^-126.
+constexpr int kLimbs = 3;
 __device__ __forceinline__ int fix_exp(uint32_t u)
 {
     const int e = (int)((u + (1u << 17)) >> 23);
-    return e < 8 * NL - 1 ? 8 * NL - 1 : e;
+    return e < 8 * kLimbs - 1 ? 8 * kLimbs - 1 : e;
 }
 // the block scale; NaN for a block that holds an infinity or a NaN
-template <int NL>
 __device__ __forceinline__ float fix_scale(uint32_t u, int e)
 {
-    return u >= 0x7f800000u ? __builtin_nanf("") : __uint_as_float((uint32_t)(e - (8 * NL - 2)) << 23);
+    return u >= 0x7f800000u ? __builtin_nanf("") : __uint_as_float((uint32_t)(e - (8 * kLimbs - 2)) << 23);
 }
-template <int NL>
-__device__ __forceinline__ int fix_code(float v, int e) { return (int)__builtin_rintf(ldexpf(v, 125 + 8 * NL - e)); }
+__device__ __forceinline__ int fix_code(float v, int e) { return (int)__builtin_rintf(ldexpf(v, 125 + 8 * kLimbs - e)); }
 
-// q = l0 + 256 l1 (+ 65536 l2) with signed bytes
-template <int NL>
-__device__ __forceinline__ void limbs(int q, int (&l)[3])
+// q = l0 + 256 l1 + 65536 l2 with signed bytes
+__device__ __forceinline__ void limbs(int q, int (&l)[kLimbs])
 {
     l[0] = (int8_t)q;
     q = (q - l[0]) >> 8;
-    l[1] = NL == 2 ? q : (int)(int8_t)q;
-    l[2] = NL == 2 ? 0 : (q - l[1]) >> 8;
+    l[1] = (int8_t)q;
+    l[2] = (q - l[1]) >> 8;
 }
 
-// Limb l of token m is row kRowStep m + l of the instruction's 32 rows, so that a lane gets the
-// limb sums of a (token, column) in neighbouring result registers.  Only the first 8 rows are
-// used, the first register quad of both lane halves: half h holds rows 4 h .. 4 h + 3, that is
-// token h of three limbs, or tokens 2 h and 2 h + 1 of two.  (More rows a read cost registers,
-// and so waves in flight, and LDS for their activations: 24 tokens on the wide layer took 75 us
-// of gate/up with up to 16 rows.)
-template <int NL>
-struct Limbs {
-    static constexpr int kRowStep = NL == 2 ? 2 : 4;
-    static constexpr int kTokens = 8 / kRowStep;          // rows of a chunk
-    static constexpr int kPerHalf = 4 / kRowStep;         // tokens of a lane half
-};
-constexpr int limbs_of(int dtype) { return dtype == kF32 ? 3 : 2; }
+// Limb l of a chunk's token m is row 4 m + l of the instruction's 32 rows, so that a lane gets the
+// limb sums of a (token, column) in neighbouring result registers: register quad i of lane half h
+// holds rows 8 i + 4 h .. 8 i + 4 h + 3, token 2 i + h.
+constexpr int kRowStep = 4;
+constexpr int kPerHalf = kChunkRows / 2;                  // tokens of a lane half
+static_assert(kPerHalf * 2 == kChunkRows && kChunkRows * kRowStep <= 32, "rows of one instruction");
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
@@ -186,7 +176,6 @@ struct RouteArgs {
     const float* logits;
     int64_t logits_stride;
     int T, E, k;
-    int chunk_rows;
     int32_t* eidx;
     float* wts;
     int32_t* counts;
@@ -202,7 +191,7 @@ struct RouteArgs {
 };
 
 // Workgroup 0 routes every token (a token per wave at a time) and lists the chunks: per
-// expert its pairs in groups of chunk_rows.  A pair's row inside its chunk depends on
+// expert its pairs in groups of kChunkRows.  A pair's row inside its chunk depends on
 // the order of LDS atomics; nothing else does, since every row is computed by itself.
 __device__ __forceinline__ void route_all(const RouteArgs& a)
 {
@@ -243,7 +232,7 @@ __device__ __forceinline__ void route_all(const RouteArgs& a)
     }
     __syncthreads();
     const int c = tid < a.E ? s_cnt[tid] : 0;
-    const int nc = (c + a.chunk_rows - 1) / a.chunk_rows;
+    const int nc = (c + kChunkRows - 1) / kChunkRows;
     int incl = nc;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -263,56 +252,54 @@ __device__ __forceinline__ void route_all(const RouteArgs& a)
         a.counts[tid] = c;
         for (int i = 0; i < nc; ++i) {
             a.chunks[first + i].expert = tid;
-            a.chunks[first + i].n = c - i * a.chunk_rows < a.chunk_rows ? c - i * a.chunk_rows : a.chunk_rows;
+            a.chunks[first + i].n = c - i * kChunkRows < kChunkRows ? c - i * kChunkRows : kChunkRows;
         }
     }
     if (tid == 0) *a.nchunks = total;
     __syncthreads();
     if (e_of >= 0) {
         const int r = atomicAdd(&s_fill[e_of], 1);
-        a.chunks[s_first[e_of] + r / a.chunk_rows].pair[r % a.chunk_rows] = tid;
+        a.chunks[s_first[e_of] + r / kChunkRows].pair[r % kChunkRows] = tid;
     }
 }
 
 // Four values of a block of 32 by each of 8 lanes: their limbs as a word per plane, and the
 // block's scale.
-template <int NL>
-__device__ __forceinline__ void block_to_fixed(const float (&v)[4], uint32_t (&w)[3], float& scale)
+__device__ __forceinline__ void block_to_fixed(const float (&v)[4], uint32_t (&w)[kLimbs], float& scale)
 {
     uint32_t u = umax(umax(abs_bits(v[0]), abs_bits(v[1])), umax(abs_bits(v[2]), abs_bits(v[3])));
     u = umax(u, dpp0<0xB1>(u));                           // quad_perm: lane ^ 1
     u = umax(u, dpp0<0x4E>(u));                           // quad_perm: lane ^ 2
     u = umax(u, dpp0<0x141>(u));                          // row_half_mirror: the other quad of the 8
-    const int e = fix_exp<NL>(u);
+    const int e = fix_exp(u);
     w[0] = w[1] = w[2] = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        int l[3];
-        limbs<NL>(u >= 0x7f800000u ? 0 : fix_code<NL>(v[i], e), l);
+        int l[kLimbs];
+        limbs(u >= 0x7f800000u ? 0 : fix_code(v[i], e), l);
 #pragma unroll
-        for (int j = 0; j < NL; ++j) w[j] |= (uint32_t)(l[j] & 0xff) << (8 * i);
+        for (int j = 0; j < kLimbs; ++j) w[j] |= (uint32_t)(l[j] & 0xff) << (8 * i);
     }
-    scale = fix_scale<NL>(u, e);
+    scale = fix_scale(u, e);
 }
 
-// x in fixed point: 8 lanes per block of 32, limb plane l of token t at xl[(NL t + l) d].
+// x in fixed point: 8 lanes per block of 32, limb plane l of token t at xl[(3 t + l) d].
 template <int kT>
 __device__ __forceinline__ void x_to_fixed(const RouteArgs& a, int64_t first)
 {
-    constexpr int NL = limbs_of(kT);
     const int nb = a.d / 32;
     const int64_t blk = first + (threadIdx.x >> 3);
     if (blk >= (int64_t)a.T * nb) return;                 // uniform over the 8-lane group
     const int sub = threadIdx.x & 7;
     const int t = (int)((uint32_t)blk / (uint32_t)nb), b = (int)blk - t * nb;
     float v[4], scale;
-    uint32_t w[3];
+    uint32_t w[kLimbs];
     load_n<kT, 4>(static_cast<const uint8_t*>(a.x) +
                   ((int64_t)t * a.x_stride + b * 32 + sub * 4) * dtype_bytes(kT), v);
-    block_to_fixed<NL>(v, w, scale);
+    block_to_fixed(v, w, scale);
 #pragma unroll
-    for (int j = 0; j < NL; ++j)
-        *reinterpret_cast<uint32_t*>(a.xl + ((int64_t)t * NL + j) * a.d + b * 32 + sub * 4) = w[j];
+    for (int j = 0; j < kLimbs; ++j)
+        *reinterpret_cast<uint32_t*>(a.xl + ((int64_t)t * kLimbs + j) * a.d + b * 32 + sub * 4) = w[j];
     if (sub == 0) a.xs[(int64_t)t * nb + b] = scale;
 }
 
@@ -381,7 +368,7 @@ struct Ring {
 // block of ring slot u.
 //   a          the 16 bytes of the block that this lane feeds
 //   scl(i, b)  the scale of that token's block
-template <int NL, int kTok, int NT, int U, class Scl>
+template <int kTok, int NT, int U, class Scl>
 __device__ __forceinline__ void block_product(float (&acc)[NT][kTok], const Ring<NT, U>& r, int u, int q, v4i a, int b, Scl scl)
 {
     const v16i zero = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
@@ -400,8 +387,8 @@ __device__ __forceinline__ void block_product(float (&acc)[NT][kTok], const Ring
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             // 16 x the limb sums; s0 + 256 s1 is a multiple of 16 below 2^28: exact in fp32
-            float v = (float)(s[t][2 * i] + (s[t][2 * i + 1] << 8));
-            if (NL == 3) v = __builtin_fmaf((float)s[t][2], 65536.0f, v);
+            const float low = (float)(s[t][4 * i] + (s[t][4 * i + 1] << 8));
+            const float v = __builtin_fmaf((float)s[t][4 * i + 2], 65536.0f, low);
             acc[t][i] = __builtin_fmaf(v, ws[t] * x, acc[t][i]);
         }
     }
@@ -410,7 +397,7 @@ __device__ __forceinline__ void block_product(float (&acc)[NT][kTok], const Ring
 
 // K pairs [p0, p1) of a filled ring, the activations in LDS: act(b) gives the bytes of block b
 // that this lane feeds.
-template <int NL, int kTok, int NT, int U, class Act, class Scl>
+template <int kTok, int NT, int U, class Act, class Scl>
 __device__ __forceinline__ void ring_product(float (&acc)[NT][kTok], Ring<NT, U>& r, const WeightAt& w, int p0, int p1,
                                              int nb, Act act, Scl scl)
 {
@@ -419,9 +406,9 @@ __device__ __forceinline__ void ring_product(float (&acc)[NT][kTok], Ring<NT, U>
         for (int u = 0; u < U; ++u) {
             const int pr = pb + u;
             if (pr >= p1) break;                          // uniform
-            block_product<NL, kTok>(acc, r, u, 0, act(2 * pr), 2 * pr, scl);
+            block_product<kTok>(acc, r, u, 0, act(2 * pr), 2 * pr, scl);
             // the padded block of an odd count is left out
-            if (2 * pr + 1 < nb) block_product<NL, kTok>(acc, r, u, 1, act(2 * pr + 1), 2 * pr + 1, scl);
+            if (2 * pr + 1 < nb) block_product<kTok>(acc, r, u, 1, act(2 * pr + 1), 2 * pr + 1, scl);
             if (pr + U < p1) r.load(u, w, pr + U);
         }
     }
@@ -435,13 +422,12 @@ struct GateUpArgs {
     const DecodeChunk* chunks;
     const uint8_t* blob;
     uint64_t expert_stride, q_off, s_off;
-    int8_t* hl;               // h in fixed point: limb plane l of pair p at hl[(NL p + l) f]
+    int8_t* hl;               // h in fixed point: limb plane l of pair p at hl[(3 p + l) f]
     float* hs;                // its block scales [pairs][f / 32]
     int f;
 };
 
 // h = silu(gate) * up of pair p, 32 columns by a 32-lane half, in fixed point.
-template <int NL>
 __device__ __forceinline__ void store_h(const GateUpArgs& g, int p, int fb, float gate, float up)
 {
     const int j32 = threadIdx.x & 31;
@@ -449,13 +435,13 @@ __device__ __forceinline__ void store_h(const GateUpArgs& g, int p, int fb, floa
     uint32_t u = abs_bits(hv);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) u = umax(u, (uint32_t)__shfl_xor((int)u, o));
-    const int e = fix_exp<NL>(u);
-    int l[3];
-    limbs<NL>(u >= 0x7f800000u ? 0 : fix_code<NL>(hv, e), l);
-    int8_t* o = g.hl + (int64_t)p * NL * g.f + fb * 32 + j32;
+    const int e = fix_exp(u);
+    int l[kLimbs];
+    limbs(u >= 0x7f800000u ? 0 : fix_code(hv, e), l);
+    int8_t* o = g.hl + (int64_t)p * kLimbs * g.f + fb * 32 + j32;
 #pragma unroll
-    for (int i = 0; i < NL; ++i) o[i * g.f] = (int8_t)l[i];
-    if (j32 == 0) g.hs[(int64_t)p * (g.f / 32) + fb] = fix_scale<NL>(u, e);
+    for (int i = 0; i < kLimbs; ++i) o[i * g.f] = (int8_t)l[i];
+    if (j32 == 0) g.hs[(int64_t)p * (g.f / 32) + fb] = fix_scale(u, e);
 }
 
 // ------------------------------------------------------- few pairs: gate/up ---
@@ -470,8 +456,7 @@ __device__ __forceinline__ void store_h(const GateUpArgs& g, int p, int fb, floa
 template <int kT, int kPairWaves>
 __global__ __launch_bounds__(64 * kPairWaves) void k_decode_pair_gate_up(GateUpArgs g)
 {
-    constexpr int NL = limbs_of(kT);
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];   // xl [NL][d], then xs [d / 32]
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];   // xl [3][d], then xs [d / 32]
     __shared__ float s_red[kPairWaves][2][32];
     __shared__ int s_eidx[kMaxE];
     __shared__ float s_z[kMaxE];
@@ -481,7 +466,7 @@ __global__ __launch_bounds__(64 * kPairWaves) void k_decode_pair_gate_up(GateUpA
     const int p = blockIdx.y, t = p / r.k, j = p - t * r.k, fb = blockIdx.x;
     const int d = r.d, nb = d / 32, npairs = k_pairs(d);
     int8_t* xl = reinterpret_cast<int8_t*>(lds);
-    float* xs = reinterpret_cast<float*>(lds + NL * d);
+    float* xs = reinterpret_cast<float*>(lds + kLimbs * d);
     const bool record = fb == 0 && j == 0;                // uniform
     const float* lt = r.logits + (int64_t)t * r.logits_stride;
 
@@ -519,23 +504,23 @@ __global__ __launch_bounds__(64 * kPairWaves) void k_decode_pair_gate_up(GateUpA
     for (int blk = tid >> 3; blk < nb; blk += 64 * kPairWaves / 8) {
         const int sub = tid & 7;
         float v[4], scale;
-        uint32_t x[3];
+        uint32_t x[kLimbs];
         load_n<kT, 4>(static_cast<const uint8_t*>(r.x) +
                       ((int64_t)t * r.x_stride + blk * 32 + sub * 4) * dtype_bytes(kT), v);
-        block_to_fixed<NL>(v, x, scale);
+        block_to_fixed(v, x, scale);
 #pragma unroll
-        for (int l = 0; l < NL; ++l) *reinterpret_cast<uint32_t*>(xl + l * d + blk * 32 + sub * 4) = x[l];
+        for (int l = 0; l < kLimbs; ++l) *reinterpret_cast<uint32_t*>(xl + l * d + blk * 32 + sub * 4) = x[l];
         if (sub == 0) xs[blk] = scale;
     }
     __syncthreads();
 
     auto act = [&](int b) -> v4i {
         v4i a = {0, 0, 0, 0};
-        if (j32 < NL) a = *reinterpret_cast<const v4i*>(xl + j32 * d + b * 32 + 16 * h);
+        if (j32 < kLimbs) a = *reinterpret_cast<const v4i*>(xl + j32 * d + b * 32 + 16 * h);
         return a;
     };
     float acc[2][1] = {};
-    if (p0 < p1) ring_product<NL, 1>(acc, ring, w, p0, p1, nb, act, [&](int, int b) { return xs[b]; });
+    if (p0 < p1) ring_product<1>(acc, ring, w, p0, p1, nb, act, [&](int, int b) { return xs[b]; });
     if (h == 0) {
         s_red[wave][0][j32] = acc[0][0];
         s_red[wave][1][j32] = acc[1][0];
@@ -548,7 +533,7 @@ __global__ __launch_bounds__(64 * kPairWaves) void k_decode_pair_gate_up(GateUpA
         z[0] += s_red[v][0][j32];
         z[1] += s_red[v][1][j32];
     }
-    store_h<NL>(g, p, fb, z[0], z[1]);
+    store_h(g, p, fb, z[0], z[1]);
 }
 
 // ----------------------------------------------------- chunks: gate/up, down ---
@@ -575,26 +560,25 @@ struct ChunkArgs {
 // LDS of a chunk kernel: the rows' activations (rows kPad apart in bank groups), their block
 // scales.
 constexpr int kActPad = 32;
-template <int NL>
-constexpr int chunk_lds(int K) { return Limbs<NL>::kTokens * (NL * (K + kActPad) + K / 32 * 4); }
+constexpr int chunk_lds(int K) { return kChunkRows * (kLimbs * (K + kActPad) + K / 32 * 4); }
 
-// Rows that share an expert's weights: a chunk of the route kernel's list (up to kTokens), or a
+// Rows that share an expert's weights: a chunk of the route kernel's list (up to kChunkRows), or a
 // pair by itself.  A workgroup takes a chunk by two 32-column tiles -- the gate and the up tile of
 // an f-block, or two tiles of the down matrix -- its waves split K and add up through LDS.  A
 // fixed number of workgroups goes through the items, since only the device knows how many there
 // are; the chunks of an expert follow each other at a multiple of 8 workgroups, so that one XCD
 // reads a tile for all of them (the first from memory, the others from its L2).
 //
-// 24 tokens of d = 4096, f = 1536, some 35 of 256 experts reached, bf16 (370 MB): gate/up 75 us, down
-// 46; what bounds it is memory (3 TB/s) with the expansion of the codes and the sums' join close behind.
+// 24 tokens of d = 4096, f = 1536, skewed routing, some 36 of 256 experts reached (380 MB): 149 us the layer, of
+// alike routing, 137 experts (1.4 GB): 278.  The first is bound by the expansion of the codes and the sums' join, paid
+// again for every chunk of an expert, the second by memory (5.2 TB/s).
 constexpr int kChunkWaves = 4;
 
-template <int NL, bool kGateUp>
+template <bool kGateUp>
 __global__ __launch_bounds__(64 * kChunkWaves) __attribute__((amdgpu_waves_per_eu(4))) void k_decode_chunk(ChunkArgs a)
 {
-    using Lb = Limbs<NL>;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    __shared__ float s_red[kChunkWaves][2][Lb::kTokens][32];
+    __shared__ float s_red[kChunkWaves][2][kChunkRows][32];
     const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, j32 = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int K = kGateUp ? a.g.r.d : a.d.f, nb = K / 32, npairs = k_pairs(K);
@@ -603,7 +587,7 @@ __global__ __launch_bounds__(64 * kChunkWaves) __attribute__((amdgpu_waves_per_e
     const int items = (nchunks ? *nchunks : a.d.T * a.d.k) * stride;
     const int p0 = wave * npairs / kChunkWaves, p1 = (wave + 1) * npairs / kChunkWaves;
     int8_t* s_act = reinterpret_cast<int8_t*>(lds);
-    float* s_scale = reinterpret_cast<float*>(lds + Lb::kTokens * NL * (K + kActPad));
+    float* s_scale = reinterpret_cast<float*>(lds + kChunkRows * kLimbs * (K + kActPad));
     const int8_t* acts = kGateUp ? a.g.r.xl : a.d.hl;
     const float* scales = kGateUp ? a.g.r.xs : a.d.hs;
 
@@ -619,39 +603,39 @@ __global__ __launch_bounds__(64 * kChunkWaves) __attribute__((amdgpu_waves_per_e
         if (!two) w.q_step = w.s_step = 0;                // an odd count's last tile twice, stored once
         Ring<2, 4> ring;
         ring.fill(w, p0, p1);                             // in flight while the activations are staged
-        int pair[Lb::kTokens];
+        int pair[kChunkRows];
 #pragma unroll
-        for (int m = 0; m < Lb::kTokens; ++m) pair[m] = nchunks ? ch->pair[m < n ? m : 0] : ci;
+        for (int m = 0; m < kChunkRows; ++m) pair[m] = nchunks ? ch->pair[m < n ? m : 0] : ci;
         __syncthreads();                                  // the previous item's LDS is read
 #pragma unroll
-        for (int m = 0; m < Lb::kTokens; ++m) {
+        for (int m = 0; m < kChunkRows; ++m) {
             if (m >= n) break;                            // uniform
             const int64_t src = kGateUp ? pair[m] / a.g.r.k : pair[m];
-            for (int i = tid * 16; i < NL * K; i += 64 * kChunkWaves * 16) {
+            for (int i = tid * 16; i < kLimbs * K; i += 64 * kChunkWaves * 16) {
                 const int l = (i >= K) + (i >= 2 * K);    // K is a multiple of 32: a piece is in one plane
-                *reinterpret_cast<uint4*>(s_act + (m * NL + l) * (K + kActPad) + i - l * K) =
-                    *reinterpret_cast<const uint4*>(acts + src * NL * K + i);
+                *reinterpret_cast<uint4*>(s_act + (m * kLimbs + l) * (K + kActPad) + i - l * K) =
+                    *reinterpret_cast<const uint4*>(acts + src * kLimbs * K + i);
             }
             for (int i = tid; i < nb; i += 64 * kChunkWaves) s_scale[m * nb + i] = scales[src * nb + i];
         }
         __syncthreads();
-        const int m_a = j32 / Lb::kRowStep, l_a = j32 % Lb::kRowStep;   // the A row this lane feeds
-        const bool on = m_a < n && l_a < NL;
-        const int8_t* al = s_act + (m_a * NL + l_a) * (K + kActPad) + 16 * h;
+        const int m_a = j32 / kRowStep, l_a = j32 % kRowStep;           // the A row this lane feeds
+        const bool on = m_a < n && l_a < kLimbs;
+        const int8_t* al = s_act + (m_a * kLimbs + l_a) * (K + kActPad) + 16 * h;
         auto act = [&](int b) -> v4i {
             v4i v = {0, 0, 0, 0};
             if (on) v = *reinterpret_cast<const v4i*>(al + b * 32);
             return v;
         };
         // an absent token's column is not stored: whatever its place in the array holds will do
-        const float* xs = s_scale + Lb::kPerHalf * h * nb;
-        float acc[2][Lb::kPerHalf] = {};
+        const float* xs = s_scale + h * nb;
+        float acc[2][kPerHalf] = {};
         if (p0 < p1)
-            ring_product<NL, Lb::kPerHalf>(acc, ring, w, p0, p1, nb, act, [&](int i, int b) { return xs[i * nb + b]; });
+            ring_product<kPerHalf>(acc, ring, w, p0, p1, nb, act, [&](int i, int b) { return xs[2 * i * nb + b]; });
 #pragma unroll
-        for (int i = 0; i < Lb::kPerHalf; ++i) {
-            s_red[wave][0][Lb::kPerHalf * h + i][j32] = acc[0][i];
-            s_red[wave][1][Lb::kPerHalf * h + i][j32] = acc[1][i];
+        for (int i = 0; i < kPerHalf; ++i) {
+            s_red[wave][0][2 * i + h][j32] = acc[0][i];
+            s_red[wave][1][2 * i + h][j32] = acc[1][i];
         }
         __syncthreads();
         // gate/up: row m by a half wave; down: row m's tile t by a half wave
@@ -664,7 +648,7 @@ __global__ __launch_bounds__(64 * kChunkWaves) __attribute__((amdgpu_waves_per_e
                     z[0] += s_red[v][0][m][j32];
                     z[1] += s_red[v][1][m][j32];
                 }
-                store_h<NL>(a.g, nchunks ? ch->pair[m] : ci, nt >> 1, z[0], z[1]);
+                store_h(a.g, nchunks ? ch->pair[m] : ci, nt >> 1, z[0], z[1]);
             }
         } else {
             const int m = tid >> 6, t = (tid >> 5) & 1;
@@ -675,7 +659,7 @@ __global__ __launch_bounds__(64 * kChunkWaves) __attribute__((amdgpu_waves_per_e
                 a.d.dm[(int64_t)(nchunks ? ch->pair[m] : ci) * a.d.d + (nt + t) * 32 + j32] = z;
             }
         }
-        static_assert(Lb::kTokens <= kChunkWaves, "a wave per row");
+        static_assert(kChunkRows <= kChunkWaves, "a wave per row");
     }
 }
 
@@ -689,10 +673,10 @@ constexpr int kFusedPairs = 8;                            // pairs, at most
 
 struct PairDownLds {
     int hl, hs, dm, bytes;
-    MOE_HD PairDownLds(int R, int f, int NL, int ksplit)
+    MOE_HD PairDownLds(int R, int f, int ksplit)
     {
         hl = 0;
-        hs = R * NL * f;
+        hs = R * kLimbs * f;
         dm = hs + R * (f / 32) * 4;
         bytes = dm + R * ksplit * 32 * 4;
     }
@@ -701,13 +685,12 @@ struct PairDownLds {
 template <int kT>
 __global__ __launch_bounds__(64 * kPairDownWaves) void k_decode_pair_down(DownArgs g)
 {
-    constexpr int NL = limbs_of(kT);
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     __shared__ float s_w[kFusedPairs];
     const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, j32 = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int R = g.T * g.k, nb = g.f / 32, npairs = k_pairs(g.f), nt = blockIdx.x;
-    const PairDownLds L(R, g.f, NL, g.ksplit);
+    const PairDownLds L(R, g.f, g.ksplit);
     int8_t* s_hl = reinterpret_cast<int8_t*>(lds);
     float* s_hs = reinterpret_cast<float*>(lds + L.hs);
     float* s_dm = reinterpret_cast<float*>(lds + L.dm);   // [ksplit][pairs][32]
@@ -726,7 +709,7 @@ __global__ __launch_bounds__(64 * kPairDownWaves) void k_decode_pair_down(DownAr
     };
     if (wave < units) open(wave);
     if (tid < R) s_w[tid] = g.wts[tid];
-    for (int i = tid * 16; i < L.hs; i += 64 * kPairDownWaves * 16)   // R NL f: a multiple of 32
+    for (int i = tid * 16; i < L.hs; i += 64 * kPairDownWaves * 16)   // 3 R f: a multiple of 32
         *reinterpret_cast<uint4*>(s_hl + i) = *reinterpret_cast<const uint4*>(g.hl + i);
     for (int i = tid; i < R * nb; i += 64 * kPairDownWaves) s_hs[i] = g.hs[i];
     __syncthreads();
@@ -735,13 +718,13 @@ __global__ __launch_bounds__(64 * kPairDownWaves) void k_decode_pair_down(DownAr
         const int p = u / g.ksplit, ks = u - p * g.ksplit;
         float acc[1][1] = {};
         if (e >= 0) {
-            const int8_t* al = s_hl + (p * NL + j32) * g.f + 16 * h;
+            const int8_t* al = s_hl + (p * kLimbs + j32) * g.f + 16 * h;
             auto act = [&](int b) -> v4i {
                 v4i a = {0, 0, 0, 0};
-                if (j32 < NL) a = *reinterpret_cast<const v4i*>(al + b * 32);
+                if (j32 < kLimbs) a = *reinterpret_cast<const v4i*>(al + b * 32);
                 return a;
             };
-            ring_product<NL, 1>(acc, ring, w, p0, p1, nb, act, [&](int, int b) { return s_hs[p * nb + b]; });
+            ring_product<1>(acc, ring, w, p0, p1, nb, act, [&](int, int b) { return s_hs[p * nb + b]; });
         }
         if (h == 0) s_dm[(ks * R + p) * 32 + j32] = acc[0][0];
     }
@@ -842,7 +825,7 @@ bool down_fused(const DecodeLaunch& D)
 {
     const int R = D.T * D.k;
     return by_pairs(D) && D.d / 32 >= kFusedTiles && R <= kFusedPairs &&
-           PairDownLds(R, D.f, limbs_of(D.dtype), down_ksplit(D)).bytes <= kFusedLds;
+           PairDownLds(R, D.f, down_ksplit(D)).bytes <= kFusedLds;
 }
 
 RouteArgs route_args(const DecodeLaunch& D)
@@ -853,7 +836,6 @@ RouteArgs route_args(const DecodeLaunch& D)
     a.T = D.T;
     a.E = D.E;
     a.k = D.k;
-    a.chunk_rows = limbs_of(D.dtype) == 3 ? Limbs<3>::kTokens : Limbs<2>::kTokens;
     a.eidx = reinterpret_cast<int32_t*>(D.ws + D.L.eidx);
     a.wts = reinterpret_cast<float*>(D.ws + D.L.wts);
     a.counts = reinterpret_cast<int32_t*>(D.ws + D.L.counts);
@@ -927,28 +909,26 @@ hipError_t lds_limit(K kernel, int bytes)
 }
 
 // chunks: the most there can be; tile2: two-tile columns of the matrix
-template <int NL, bool kGateUp>
+template <bool kGateUp>
 hipError_t launch_chunk(const DecodeLaunch& D, int chunks, int K, int tile2, hipStream_t st)
 {
     const int64_t items = (int64_t)chunks * align_up(tile2, 8);
-    const int lds = chunk_lds<NL>(K);
-    const hipError_t e = lds_limit(&k_decode_chunk<NL, kGateUp>, lds);
+    const int lds = chunk_lds(K);
+    const hipError_t e = lds_limit(&k_decode_chunk<kGateUp>, lds);
     if (e != hipSuccess) return e;
     ChunkArgs a;
     a.g = gate_up_args(D);
     a.d = down_args(D);
-    hipLaunchKernelGGL((k_decode_chunk<NL, kGateUp>), dim3((unsigned)(items < 1024 ? items : 1024)), dim3(64 * kChunkWaves), lds,
-                       st, a);
+    hipLaunchKernelGGL(k_decode_chunk<kGateUp>, dim3((unsigned)(items < 1024 ? items : 1024)), dim3(64 * kChunkWaves), lds, st, a);
     return hipGetLastError();
 }
 
 template <int kT>
 hipError_t products_typed(const DecodeLaunch& D, hipStream_t st)
 {
-    constexpr int NL = limbs_of(kT);
     hipError_t e = hipSuccess;
     if (by_pairs(D)) {
-        const int lds = NL * D.d + D.d / 32 * 4;
+        const int lds = kLimbs * D.d + D.d / 32 * 4;
         const dim3 grid(D.f / 32, D.T * D.k);
         // two workgroups of eight waves fill a CU, four of four: more than the first hold would
         // wait for a second round (5 tokens of the resident configuration, 960 workgroups: 20.5 us
@@ -963,19 +943,19 @@ hipError_t products_typed(const DecodeLaunch& D, hipStream_t st)
             hipLaunchKernelGGL((k_decode_pair_gate_up<kT, 8>), grid, dim3(64 * 8), lds, st, gate_up_args(D));
         }
     } else {
-        e = launch_chunk<NL, true>(D, D.L.max_chunks, D.d, D.f / 32, st);
+        e = launch_chunk<true>(D, D.L.max_chunks, D.d, D.f / 32, st);
         if (e != hipSuccess) return e;
     }
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     const DownArgs g = down_args(D);
     if (down_fused(D)) {
-        const int lds = PairDownLds(D.T * D.k, D.f, NL, g.ksplit).bytes;
+        const int lds = PairDownLds(D.T * D.k, D.f, g.ksplit).bytes;
         e = lds_limit(&k_decode_pair_down<kT>, lds);
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL(k_decode_pair_down<kT>, dim3(D.d / 32), dim3(64 * kPairDownWaves), lds, st, g);
     } else {
-        return launch_chunk<NL, false>(D, by_pairs(D) ? D.T * D.k : D.L.max_chunks, D.f, (D.d / 32 + 1) / 2, st);
+        return launch_chunk<false>(D, by_pairs(D) ? D.T * D.k : D.L.max_chunks, D.f, (D.d / 32 + 1) / 2, st);
     }
     return hipGetLastError();
 }
