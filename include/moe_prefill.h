@@ -313,7 +313,7 @@ typedef struct moe_mxfp4_matrix {
     int32_t device;            /* HIP device ordinal */
     int32_t dtype;             /* MOE_F32 / MOE_BF16 / MOE_F16: the type of values */
     int32_t K;                 /* multiple of 32, >= 32 */
-    int64_t M;                 /* rows, >= 0 (0 is a no-op); M * K / 32 < 2^30 */
+    int64_t M;                 /* rows, >= 0 (0 is a no-op); M * K / 32 <= 2^30 - 64 */
     void* values;              /* device [M, K], rows `stride` elements apart; rows 16-byte aligned */
     int64_t stride;            /* >= K */
     uint8_t* codes;            /* device [M, K/2], 16-byte aligned */

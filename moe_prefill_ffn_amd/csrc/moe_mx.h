@@ -10,7 +10,7 @@ namespace moe {
 
 // What one launch takes: a launch has fewer than 2^32 threads (four a block of 32; 512 for 32 rows
 // and a group's last ones), and the tiled kernel counts its tiles in 32 bits.
-constexpr int64_t kMxMostBlocks = (1 << 30) - 1;      // M * K / 32 of quantise and dequantise
+constexpr int64_t kMxMostBlocks = (1 << 30) - 64;     // M * K / 32 of quantise and dequantise: whole workgroups of 64
 constexpr int64_t kMxMostRows = 1 << 27;              // M of a product
 constexpr int64_t kMxMostTiles = 1 << 30;             // its tiles, the smallest being 64 x 64
 

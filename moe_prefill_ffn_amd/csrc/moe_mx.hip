@@ -38,6 +38,7 @@ __device__ __forceinline__ float e8m0(uint32_t s)
 // 5.5 TB/s, next to the 5.2 of a copy kernel over a gigabyte; one row 1.5 us, a launch's time.
 constexpr int kQuantThreads = 256;
 constexpr int kQuantBlocks = kQuantThreads / 4;           // blocks per workgroup
+static_assert((kMxMostBlocks + kQuantBlocks - 1) / kQuantBlocks * kQuantThreads < (int64_t)1 << 32, "threads of a launch");
 
 struct BlockAt {
     int64_t row;

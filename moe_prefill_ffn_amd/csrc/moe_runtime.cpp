@@ -1111,7 +1111,7 @@ static int mx_matrix(const moe_mxfp4_matrix_t* in, bool quantize, void* stream)
         if (!dtype_ok(m.dtype)) return fail(nullptr, MOE_EINVAL, "mxfp4: dtype must be MOE_F32, MOE_BF16 or MOE_F16");
         if (m.K < 32 || m.K % 32) return fail(nullptr, MOE_EINVAL, "mxfp4: K must be a multiple of 32, at least 32");
         if (m.M < 0 || m.M > kMxMostBlocks / (m.K / 32))
-            return fail(nullptr, MOE_EINVAL, "mxfp4: M < 0 or M * K / 32 not below 2^30");
+            return fail(nullptr, MOE_EINVAL, "mxfp4: M < 0 or M * K / 32 above 2^30 - 64");
         if (m.M == 0) {
             g_err.clear();
             return (int)MOE_OK;

@@ -58,3 +58,19 @@ def test_structs_of_a_newer_header(tail, code):
     n.known.K, n.later = 32, tail
     p = ctypes.cast(ctypes.byref(n), ctypes.POINTER(mp.moe_mxfp4_matrix_t))
     assert mp.lib().moe_mxfp4_quantize(p.contents, None) == code
+
+
+@pytest.mark.parametrize("call", ["moe_mxfp4_quantize", "moe_mxfp4_dequantize"])
+@pytest.mark.parametrize("K", [32, 96, 1 << 20])
+def test_the_largest_matrix_of_one_launch(call, K):
+    """The last size whose workgroups of 64 blocks, 256 threads each, stay below 2^32 threads is taken (the call
+    then misses its pointers), the next one is not."""
+    def message(M):
+        m = mp.moe_mxfp4_matrix_t(struct_size=ctypes.sizeof(mp.moe_mxfp4_matrix_t), K=K, M=M, stride=K)
+        assert getattr(mp.lib(), call)(m, None) == mp.MOE_EINVAL
+        return mp.moe_prefill_last_error()
+
+    nb = K // 32
+    most = max(M for M in range((1 << 30) // nb - 100, (1 << 30) // nb + 1) if -(-M * nb // 64) * 256 < 1 << 32)
+    assert "required" in message(most)
+    assert "2^30" in message(most + 1) and "2^30" in message(most + 63 // nb + 1)
