@@ -414,8 +414,6 @@ __device__ __forceinline__ void ring_product(float (&acc)[NT][kTok], Ring<NT, U>
     }
 }
 
-constexpr int kMaxBlocks = 16384 / 32;
-
 struct GateUpArgs {
     RouteArgs r;              // routing and x
     const int32_t* nchunks;
@@ -901,11 +899,15 @@ hipError_t route_typed(const DecodeLaunch& D, hipStream_t st)
     return hipGetLastError();
 }
 
+// The limit is the process's, for every thread that launches the kernel: always the most that any call
+// needs (`most`), so that none can lower it between another's setting and launch.
+constexpr int kMaxDim = 16384;                            // d and f, as the handle checked
+constexpr int pair_lds(int d) { return kLimbs * d + d / 32 * 4; }
 template <class K>
-hipError_t lds_limit(K kernel, int bytes)
+hipError_t lds_limit(K kernel, int bytes, int most)
 {
     if (bytes <= 16 << 10) return hipSuccess;             // within the default limit next to the static arrays
-    return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, most);
 }
 
 // chunks: the most there can be; tile2: two-tile columns of the matrix
@@ -914,7 +916,7 @@ hipError_t launch_chunk(const DecodeLaunch& D, int chunks, int K, int tile2, hip
 {
     const int64_t items = (int64_t)chunks * align_up(tile2, 8);
     const int lds = chunk_lds(K);
-    const hipError_t e = lds_limit(&k_decode_chunk<kGateUp>, lds);
+    const hipError_t e = lds_limit(&k_decode_chunk<kGateUp>, lds, chunk_lds(kMaxDim));
     if (e != hipSuccess) return e;
     ChunkArgs a;
     a.g = gate_up_args(D);
@@ -928,17 +930,17 @@ hipError_t products_typed(const DecodeLaunch& D, hipStream_t st)
 {
     hipError_t e = hipSuccess;
     if (by_pairs(D)) {
-        const int lds = kLimbs * D.d + D.d / 32 * 4;
+        const int lds = pair_lds(D.d);
         const dim3 grid(D.f / 32, D.T * D.k);
         // two workgroups of eight waves fill a CU, four of four: more than the first hold would
         // wait for a second round (5 tokens of the resident configuration, 960 workgroups: 20.5 us
         // of eight waves, 15.4 of four), fewer are done sooner by more waves (1 token: 8.2, 9.0)
         if (grid.x * grid.y > 512) {
-            e = lds_limit(&k_decode_pair_gate_up<kT, 4>, lds);
+            e = lds_limit(&k_decode_pair_gate_up<kT, 4>, lds, pair_lds(kMaxDim));
             if (e != hipSuccess) return e;
             hipLaunchKernelGGL((k_decode_pair_gate_up<kT, 4>), grid, dim3(64 * 4), lds, st, gate_up_args(D));
         } else {
-            e = lds_limit(&k_decode_pair_gate_up<kT, 8>, lds);
+            e = lds_limit(&k_decode_pair_gate_up<kT, 8>, lds, pair_lds(kMaxDim));
             if (e != hipSuccess) return e;
             hipLaunchKernelGGL((k_decode_pair_gate_up<kT, 8>), grid, dim3(64 * 8), lds, st, gate_up_args(D));
         }
@@ -951,7 +953,7 @@ hipError_t products_typed(const DecodeLaunch& D, hipStream_t st)
     const DownArgs g = down_args(D);
     if (down_fused(D)) {
         const int lds = PairDownLds(D.T * D.k, D.f, g.ksplit).bytes;
-        e = lds_limit(&k_decode_pair_down<kT>, lds);
+        e = lds_limit(&k_decode_pair_down<kT>, lds, kFusedLds);
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL(k_decode_pair_down<kT>, dim3(D.d / 32), dim3(64 * kPairDownWaves), lds, st, g);
     } else {
