@@ -169,6 +169,13 @@ __device__ __forceinline__ v16f mfma_fp4(v4i w, v4i x, v16f c, int sw, int sx)
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, x8, c, 4, 4, step, sw, step, sx);   // 4: E2M1
 }
 
+// A bound, clamped into [0, M].
+__device__ __forceinline__ int bound_of(const MxGemm& a, int g)
+{
+    const int64_t b = a.bounds[g];
+    return (int)(b < 0 ? 0 : b > a.M ? a.M : b);
+}
+
 // silu(g) u by the hardware's exp2 and reciprocal (an ulp each).  exp(-g) = 2^t (1 + ln2 r), t the
 // rounded -g log2(e) and r what the rounding left, so that a large |g| costs no bits.
 __device__ __forceinline__ float silu_mul(float g, float u)
@@ -517,10 +524,7 @@ __global__ __launch_bounds__(64 * S::NW) void k_mx_tile(MxGemm a, int n_tiles, i
     uint32_t* s_pre = reinterpret_cast<uint32_t*>(lds);   // nothing else is in the stages' slots then
     uint32_t* s_wave = s_pre + kWin;
     static_assert((kWin + S::NW) * 4 <= 2 * L::kDataBytes, "inside the stages' slots");
-    auto bound = [&](int g) -> int {                      // sound bounds lie within [0, M]
-        const int64_t b = a.bounds[g < a.G ? g : a.G];
-        return (int)(b < 0 ? 0 : b > a.M ? a.M : b);
-    };
+    auto bound = [&](int g) -> int { return bound_of(a, g < a.G ? g : a.G); };
     auto scan = [&](int base) -> uint32_t {
         int b[kPer + 1];
         uint32_t n[kPer], sum = 0;
@@ -734,18 +738,17 @@ __device__ __forceinline__ Rows rows_of_slot(const MxGemm& a, int64_t slot)
     const int lane = threadIdx.x & 63;
     while (span > 1) {
         const int step = (span + 63) >> 6, at = g + lane * step;
-        const bool le = lane * step < span && (int64_t)(a.bounds[at] / kFewRows) + at <= slot;
-        const int n = __popcll(__ballot(le));             // a run of lanes from 0 for sound bounds
+        const bool le = lane * step < span && (int64_t)(bound_of(a, at) / kFewRows) + at <= slot;
+        const int n = __popcll(__ballot(le));             // a run of lanes from 0 for bounds that ascend
         const int skip = (n > 0 ? n - 1 : 0) * step;
         g += skip;
         span = span - skip < step ? span - skip : step;
     }
     g = __builtin_amdgcn_readfirstlane(g);
-    const int64_t b0 = a.bounds[g], b1 = a.bounds[g + 1];
-    int64_t m0 = b0 + (slot - (b0 / kFewRows + g)) * kFewRows, m1 = m0 + kFewRows < b1 ? m0 + kFewRows : b1;
-    // sound bounds ascend within [0, M]; this only keeps others from reaching outside
-    if (m0 < b0 || m0 < 0) m0 = m1;
-    if (m1 > a.M) m1 = a.M;
+    const int64_t b0 = bound_of(a, g), b1 = bound_of(a, g + 1);
+    int64_t m0 = b0 + (slot - (b0 / kFewRows + g)) * kFewRows;
+    const int64_t m1 = m0 + kFewRows < b1 ? m0 + kFewRows : b1;
+    if (m0 < b0) m0 = m1;                                 // bounds that do not ascend: nothing before the group's rows
     return {g, m0, m1};
 }
 
