@@ -786,20 +786,23 @@ namespace {
 
 // Pairs by themselves need no route kernel, but those that share an expert read its weights again,
 // from a cache.  With experts drawn alike the re-reads are (R - D) experts' bytes, D = E (1 - (1 - k / E)^T)
-// the experts reached; about 100 MB of them cost what the route kernel does, whatever the sizes.  Chunks
-// against pairs: 4096 x 1536, 8 of 256 experts, 8 tokens (63 MB) 125 us, 118, 12 tokens (160 MB) 162, 170; 8 of
-// 32, 4 tokens (107 MB) 52, 55; 2048 x 768, 8 of 16, 6 tokens (85 MB) 27, 25, 7 tokens (106 MB) 27.6, 28.3;
-// 1024 x 512, 2 of 8, 16 tokens (21 MB) 19, 13.
+// the experts reached; about 100 MB of them cost what the route kernel does, whatever the sizes.  Pairs
+// against chunks: 4096 x 1536, 8 of 256 experts, 8 tokens (70 MB) 121 us, 122, 12 tokens (158 MB) 171, 166; 8 of
+// 32, 3 tokens (58 MB) 46.5, 49.5, 5 tokens (166 MB) 69, 61; 2048 x 768, 8 of 16, 6 tokens (86 MB) 25.7, 26.8,
+// 8 tokens (128 MB) 30.5, 30.0; 8 of 128, 16 tokens (121 MB) 59, 57; 1024 x 512, 2 of 8, 48 tokens (78 MB) 20, 25.
 constexpr double kPairReread = 100e6;
 constexpr int kPairMost = 128;                            // as far as that was measured
 
 // The fused down and combine (a workgroup a column tile) against a wave for every (pair, K split) of two
-// tiles and a combine: it saves a launch and wins while its workgroups fill some of the chip and have little
-// to do each.  Fused, not: 1024 x 512, 2 pairs 9.3 us, 11.0, 10 pairs 11.9, 11.5; 4096 x 1536, 8 pairs 23.7,
-// 24.6, 24 pairs 45, 39; 512 x 256 (16 tiles), 6 pairs 10.7, 10.6; 4096 x 4096, 6 pairs (56 KB of h) 33, 36, 8
-// pairs (74 KB) 41, 37.
-constexpr int kFusedTiles = 32;
-constexpr int kFusedLds = 64 << 10;
+// tiles and a combine: it saves a launch, and its waves have more of K to go through.  Up to four pairs their K
+// splits are the waves of one round; more win while there is little h.  The width of y does not matter.
+// Fused, not: 2 pairs of 1024 x 768 9.1 us, 11.3, of 128 x 2048 10.2, 12.5; 4 pairs of 1024 x 1536 12.3, 13.8, of
+// 2048 x 4096 21.5, 22.8; 7 pairs of 1024 x 768 (5376 values) 11.3, 11.5; 8 pairs of 2048 x 512 (4096) 13.8, 14.2,
+// of 2048 x 768 (6144) 15.4, 15.2; 5 pairs of 1024 x 1536 (7680) 14.0, 13.8; 8 pairs of 4096 x 1536 28.1, 27.5, of
+// 2048 x 4096 32, 27.
+constexpr int kFusedH = 5632;                             // values of h of more than kFusedFew pairs
+constexpr int kFusedFew = 4;
+constexpr int kFusedLds = 64 << 10;                       // as far as that was measured
 
 bool by_pairs(const DecodeLaunch& D)
 {
@@ -822,7 +825,7 @@ int down_ksplit(const DecodeLaunch& D)
 bool down_fused(const DecodeLaunch& D)
 {
     const int R = D.T * D.k;
-    return by_pairs(D) && D.d / 32 >= kFusedTiles && R <= kFusedPairs &&
+    return by_pairs(D) && R <= kFusedPairs && (R <= kFusedFew || R * D.f <= kFusedH) &&
            PairDownLds(R, D.f, down_ksplit(D)).bytes <= kFusedLds;
 }
 

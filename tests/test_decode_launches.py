@@ -60,7 +60,11 @@ int main()
 }
 """
 
-SIZES = [(d, f, E, k, T) for d, f in [(64, 96), (2048, 768), (4096, 1536), (1184, 352), (16384, 1024), (1024, 16384), (16384, 16384)]
+# (size, launches of a call): the fused down and combine saves one
+RULE = [((512, 256, 8, 2, 1), 2), ((128, 2048, 8, 2, 2), 2), ((2048, 4096, 16, 1, 4), 2), ((2048, 4096, 16, 1, 5), 3),
+        ((2048, 768, 64, 7, 1), 2), ((2048, 768, 64, 8, 1), 3), ((64, 64, 64, 8, 1), 2), ((64, 64, 64, 9, 1), 3),
+        ((64, 16384, 16, 4, 1), 3)]                       # its h is past the LDS of the rule
+SIZES = [s for s, _ in RULE] + [(d, f, E, k, T) for d, f in [(64, 96), (2048, 768), (4096, 1536), (1184, 352), (16384, 1024), (1024, 16384), (16384, 16384)]
          for E, k in [(1, 1), (8, 2), (128, 8)] for T in (1, 2, 24, 128)]
 
 
@@ -104,3 +108,14 @@ def test_every_launch_is_within_its_kernels_limit(events):
             assert grid[0] >= 1 and 1 <= grid[1] <= 65535 and grid[2] <= 1024
             seen += 1
     assert seen > len(SIZES) * 3
+
+
+def test_which_calls_fuse_the_down_product_and_the_combine(events):
+    """One launch for a few pairs' down product and combine; gate/up before it, and nothing else."""
+    it = iter([e for e in events if e[0] == "launch"])
+    for size, n in RULE:
+        for dtype in range(3):
+            got = [next(it) for _ in range(n)]
+            d, f, T, k = size[0], size[1], size[4], size[3]
+            assert got[0][3:5] == [f // 32, T * k], size    # gate/up: a workgroup an f-block and pair
+            assert (got[1][3] == d // 32 and got[1][5] == 1024) == (n == 2), size

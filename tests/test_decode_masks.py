@@ -25,7 +25,7 @@ def check_masked(L, h, blob, x, lg):
 
 @gpu
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("shape,T", [((2048, 768, 9, 8), 1), ((1024, 64, 5, 2), 1), ((1024, 64, 5, 2), 4), ((1024, 96, 5, 1), 8),
+@pytest.mark.parametrize("shape,T", [((2048, 768, 9, 8), 1), ((1024, 512, 9, 8), 1), ((1184, 1376, 5, 2), 2), ((1024, 64, 5, 2), 1), ((1024, 64, 5, 2), 4), ((1024, 96, 5, 1), 8),
                                      ((2048, 768, 9, 8), 3), ((96, 64, 5, 2), 3), ((2048, 768, 9, 8), 20), ((1024, 64, 5, 2), 80)])
 def test_masks_in_every_kernel(layers, shape, T, dtype):
     L, h, blob = layers(*shape)
