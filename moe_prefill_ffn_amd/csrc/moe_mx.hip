@@ -897,22 +897,24 @@ hipError_t launch_shape(const MxGemm& g, hipStream_t st)
     // the tiled kernel reaches A through the row table by 32 bits of offset
     const bool far = (g.rows || g.row_div > 1) && g.a_rows * (g.K / 2) > (int64_t)UINT32_MAX;
     // Fewer tiles than a quarter of the CUs: the few-row kernel's workgroups are narrower and their
-    // waves share K.  64 x 4096 x 4096: 8.3 us against 10.9; 128 rows (64 tiles): 13.6 against 11.1;
-    // 64 groups of 8 rows, N = K = 2048 (more than 1024 tiles): 48 against 30.
+    // waves share K.  64 x 4096 x 4096: 7.5 us against 10.5; 128 rows (64 tiles): 13.2 against 10.6;
+    // 64 groups of 8 rows, N = K = 2048 (more than 1024 tiles): 34.6 against 28.0.
     if (far || (rows <= 64 && tiles(64, 128) < 64)) {
         hipLaunchKernelGGL((k_mx_few<kT, kSwiglu, kMode != kScale1>), dim3((unsigned)slots_of(g, kFewRows), nblk(g.N, 32)),
                            dim3(64 * kFewWaves), 0, st, g);
         return hipGetLastError();
     }
     // 256 x 256 tiles move the fewest bytes a product but start and end slowest: worth it over
-    // several stages and tiles that fill the chip more than once.  8192 x 4096 at K = 4096: 96 us
-    // against 104 of 128 x 128 tiles, K = 1024: 42 against 33; 4096 x 4096 x 4096 (256 tiles): 51, 50;
-    // 64 groups of 256 rows, N = K = 2048 (512 tiles): 91, 83.
-    if (rows >= 320 && g.K >= 2048 && tiles(256, 256) >= 384) return launch_tile<Tile256, kT, kSwiglu, kMode>(g, st);
+    // many stages, tiles that fill the chip more than once and groups that fill their last tile well
+    // enough.  8192 x 4096 at K = 4096: 89 us against 94 of 128 x 128 tiles, K = 8192: 151, 175; K = 2880: 87, 90;
+    // K = 2560: 67, 62; K = 2048: 59, 52; 4096 x 4096 x 4096 (256 tiles): 51, 51; 32 groups of 512 rows, N = 2048,
+    // K = 4096: 95, 96, K = 6144: 140, 170; of 320 rows: 90, 77 and 126, 117.
+    if (rows >= 448 && g.K >= 2816 && tiles(256, 256) >= 384) return launch_tile<Tile256, kT, kSwiglu, kMode>(g, st);
     // 128 x 128 tiles where they fill the chip's two workgroups a CU and the rows fill a good part of
-    // a tile: 2048 x 4096 x 4096 28 us against 33 of 64 x 128, 64 groups of 96 rows (N = K = 2048)
-    // 49 against 53, of 48 37, 38; 512 x 4096 x 4096 (128 tiles) 18 against 15, 64 groups of 24 rows 36, 31.
-    if (rows >= 40 && tiles(128, 128) >= 512) return launch_tile<Tile128, kT, kSwiglu, kMode>(g, st);
+    // a tile: 2048 x 4096 x 4096 27 us against 32 of 64 x 128; 128 groups of 72 rows, N = 768, K = 2048, SwiGLU
+    // 45, 50, of 64 44, 45, of 56 44, 44, of 40 43, 39; 64 groups of 40 rows (N = K = 2048) 30.8, 29.6;
+    // 512 x 4096 x 4096 (128 tiles) 14.6, 12.0.
+    if (rows >= 60 && tiles(128, 128) >= 512) return launch_tile<Tile128, kT, kSwiglu, kMode>(g, st);
     return launch_tile<Tile64, kT, kSwiglu, kMode>(g, st);
 }
 

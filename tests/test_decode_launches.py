@@ -1,45 +1,10 @@
 """The few-token layer's launches, recorded by a host program that stands in for the HIP runtime: the LDS limit
 that a kernel is given holds for every call's size, so that two threads' calls cannot lower each other's."""
-import json
-import os
-import shutil
-import subprocess
-
 import pytest
 
-ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-CSRC = os.path.join(ROOT, "moe_prefill_ffn_amd", "csrc")
-HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+from launch_recorder import record
 
-PROGRAM = r"""
-#include <cstdio>
-#include "moe_decode.h"
-
-extern "C" {
-void** __hipRegisterFatBinary(const void*) { static void* m; return &m; }
-void __hipRegisterFunction(void**, const void*, char*, const char*, unsigned, void*, void*, dim3*, dim3*, int*) {}
-void __hipUnregisterFatBinary(void**) {}
-static struct { dim3 g, b; size_t lds; hipStream_t st; } cfg;
-hipError_t __hipPushCallConfiguration(dim3 g, dim3 b, size_t lds, hipStream_t st) { cfg = {g, b, lds, st}; return hipSuccess; }
-hipError_t __hipPopCallConfiguration(dim3* g, dim3* b, size_t* lds, hipStream_t* st)
-{
-    *g = cfg.g, *b = cfg.b, *lds = cfg.lds, *st = cfg.st;
-    return hipSuccess;
-}
-hipError_t hipGetLastError(void) { return hipSuccess; }
-static const char* sep = "";
-hipError_t hipFuncSetAttribute(const void* f, hipFuncAttribute, int v)
-{
-    std::printf("%s[\"limit\", \"%p\", %d]", sep, f, v), sep = ", ";
-    return hipSuccess;
-}
-hipError_t hipLaunchKernel(const void* f, dim3 g, dim3 b, void**, size_t lds, hipStream_t)
-{
-    std::printf("%s[\"launch\", \"%p\", %zu, %u, %u, %u]", sep, f, lds, g.x, g.y, b.x), sep = ", ";
-    return hipSuccess;
-}
-}
-
+MAIN = r"""
 int main()
 {
     static uint8_t none[256];
@@ -70,22 +35,8 @@ SIZES = [s for s, _ in RULE] + [(d, f, E, k, T) for d, f in [(64, 96), (2048, 76
 
 @pytest.fixture(scope="module")
 def events(tmp_path_factory):
-    if not shutil.which(HIPCC):
-        pytest.skip("no hipcc")
-    at = tmp_path_factory.mktemp("launches")
-    src, exe = at / "main.hip", at / "main"
-    src.write_text(PROGRAM.replace("SIZES", ", ".join("{%d, %d, %d, %d, %d}" % s for s in SIZES)))
-    objs = []
-    for s in (str(src), os.path.join(CSRC, "moe_decode.hip")):
-        objs.append(str(at / (os.path.basename(s) + ".o")))
-        r = subprocess.run([HIPCC, "--offload-host-only", "-std=c++17", "-O1", "-fPIC", "-I", CSRC, "-c", s, "-o", objs[-1]], capture_output=True, text=True)
-        assert r.returncode == 0, r.stderr
-    # what the program never calls (the device code, a kernel of the prompt path) stays unresolved
-    r = subprocess.run(["g++", *objs, "-Wl,--unresolved-symbols=ignore-all", "-o", str(exe)], capture_output=True, text=True)
-    assert r.returncode == 0, r.stderr
-    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
-    assert r.returncode == 0, r.stderr
-    return json.loads(r.stdout)
+    main = MAIN.replace("SIZES", ", ".join("{%d, %d, %d, %d, %d}" % s for s in SIZES))
+    return record(tmp_path_factory.mktemp("launches"), "moe_decode.h", "moe_decode.hip", main)
 
 
 def test_a_kernels_lds_limit_is_the_same_for_every_size(events):
