@@ -448,9 +448,9 @@ __device__ __forceinline__ void store_h(const GateUpArgs& g, int p, int fb, floa
 // it.  Pairs of the same expert each read its weights (from a cache).  The workgroups of
 // f-block 0 and slot 0 leave the token's routing for the next kernel.
 //
-// One token, 8 experts of d = 2048, f = 768 (14 MB): 7.7 us, of which the weights' bytes are 3;
+// One token, 8 experts of d = 2048, f = 768 (14 MB): 7.6 us, of which the weights' bytes are 3;
 // the rest is the launch, the logits' way and eight slots' routing, the sums.  d = 4096,
-// f = 1536 (57 MB): 14.9 us, 3.8 TB/s.
+// f = 1536 (57 MB): 14.8 us, 3.8 TB/s.
 template <int kT, int kPairWaves>
 __global__ __launch_bounds__(64 * kPairWaves) void k_decode_pair_gate_up(GateUpArgs g)
 {
@@ -567,9 +567,9 @@ constexpr int chunk_lds(int K) { return kChunkRows * (kLimbs * (K + kActPad) + K
 // are; the chunks of an expert follow each other at a multiple of 8 workgroups, so that one XCD
 // reads a tile for all of them (the first from memory, the others from its L2).
 //
-// 24 tokens of d = 4096, f = 1536, skewed routing, some 36 of 256 experts reached (380 MB): 149 us the layer, of
-// alike routing, 137 experts (1.4 GB): 278.  The first is bound by the expansion of the codes and the sums' join, paid
-// again for every chunk of an expert, the second by memory (5.2 TB/s).
+// 24 tokens of d = 4096, f = 1536, skewed routing, some 36 of 256 experts reached (380 MB): gate/up 86 us,
+// down 53; of alike routing, 137 experts (1.4 GB): 169 and 96.  The first is bound by the expansion of the codes
+// and the sums' join, paid again for every chunk of an expert, the second by memory (5.5 TB/s).
 constexpr int kChunkWaves = 4;
 
 template <bool kGateUp>
@@ -664,8 +664,9 @@ __global__ __launch_bounds__(64 * kChunkWaves) __attribute__((amdgpu_waves_per_e
 // ------------------------------------------- few pairs: down and combine in one ---
 // A workgroup owns 32 columns of y for all tokens.  Its 16 waves take the (pair, K split) units
 // in turn, the pairs' h in LDS, and leave the units' rows there, where each token's slots are
-// added up in slot order.  One token, 8 experts of d = 2048, f = 768 (7 MB): 7.3 us; d = 4096,
-// f = 1536 (28 MB): 10.5 us.
+// added up in slot order.  One token, 4 experts of d = 2048, f = 768 (3.5 MB): 5.1 us; 8 of d = 2048, f = 512
+// (4.7 MB): 5.6; 4 of d = 4096, f = 1536 (14 MB): 7.8 us; a chain of the first bytes' latency, the ring and
+// two passes through LDS, since its d / 32 workgroups leave CUs idle.
 constexpr int kPairDownWaves = 16;
 constexpr int kFusedPairs = 8;                            // pairs, at most
 
@@ -936,9 +937,11 @@ hipError_t products_typed(const DecodeLaunch& D, hipStream_t st)
         const int lds = pair_lds(D.d);
         const dim3 grid(D.f / 32, D.T * D.k);
         // two workgroups of eight waves fill a CU, four of four: more than the first hold would
-        // wait for a second round (5 tokens of the resident configuration, 960 workgroups: 20.5 us
-        // of eight waves, 15.4 of four), fewer are done sooner by more waves (1 token: 8.2, 9.0)
-        if (grid.x * grid.y > 512) {
+        // wait for a second round.  Fewer are done sooner by more waves, and so are any whose eight
+        // waves have more than a ring of K pairs each.  The layer with eight waves, four: 2048 x 768, 8 of 128
+        // experts, 1 token (192 workgroups) 15.3 us, 15.7, 2 tokens 18.4, 18.3, 3 tokens (576) 23.6, 22.3, 5
+        // tokens 29.0, 27.5; 4096 x 1536, 8 of 256, 4 tokens (1536) 67, 69.5
+        if (grid.x * grid.y > 512 && k_pairs(D.d) <= 8 * 4) {
             e = lds_limit(&k_decode_pair_gate_up<kT, 4>, lds, pair_lds(kMaxDim));
             if (e != hipSuccess) return e;
             hipLaunchKernelGGL((k_decode_pair_gate_up<kT, 4>), grid, dim3(64 * 4), lds, st, gate_up_args(D));

@@ -34,8 +34,8 @@ __device__ __forceinline__ float e8m0(uint32_t s)
 
 // ---------------------------------------------------- quantise, dequantise ---
 // Four lanes per block, eight values each; a wave takes 16 consecutive blocks.  One pass, one read
-// and one write of everything, so memory bounds it: 8192 x 4096 fp32 (152 MB) 28 us either way,
-// 5.5 TB/s, next to the 5.2 of a copy kernel over a gigabyte; one row 1.5 us, a launch's time.
+// and one write of everything, so memory bounds it: 8192 x 4096 fp32 (152 MB) 26.5 us, back
+// 25.0, 5.7 and 6.1 TB/s, next to the 5.2 of a copy kernel over a gigabyte; one row 1.5 us, a launch's time.
 constexpr int kQuantThreads = 256;
 constexpr int kQuantBlocks = kQuantThreads / 4;           // blocks per workgroup
 static_assert((kMxMostBlocks + kQuantBlocks - 1) / kQuantBlocks * kQuantThreads < (int64_t)1 << 32, "threads of a launch");
@@ -261,10 +261,13 @@ struct MxLds {
 // and the epilogue's stores drain under them.  (A workgroup a tile spent 14 us of 43 a tile of
 // 8192 x 4096 x 4096 on its start, its first loads and its stores.)
 //
-// What bounds it: large dense products the matrix cores -- 8192 x 4096 x 4096, bf16 out, 85 to 92 us or
-// 3.1 PFLOP/s, 4.4 as K grows; the instruction alone on random codes reaches 5.6 to 6.7 on all CUs,
+// What bounds it: large dense products the matrix cores -- 8192 x 4096 x 4096, bf16 out, 89 to 92 us or
+// 3.0 PFLOP/s, 4.4 as K grows; the instruction alone on random codes reaches 5.6 to 6.7 on all CUs,
 // where power holds the clock (10 on zeros).  Grouped ones memory -- 24576 rows in 256 groups
-// (N = 4096, K = 1536, fp32 out) move 1.28 GB in 334 us, 3.8 TB/s.
+// (N = 4096, K = 1536, fp32 out) move 1.28 GB in 341 us, 3.8 TB/s.  Scale rows that are not 16-byte aligned cost
+// more the more scales there are to an output: 8192 x 4096 x 2816 (words) takes 77 us and 2880
+// (bytes at any address) 88, between 67 at K = 2560 and 83 at 3584 (16 bytes); gate and up of 128 groups of 64 rows (N = 768)
+// 59 at K = 2560, 72 at 2816, 114 at 2880.
 template <class S, int kT, bool kSwiglu, int kMode>
 __global__ __launch_bounds__(64 * S::NW) void k_mx_tile(MxGemm a, int n_tiles, int64_t n_slots)
 {

@@ -29,7 +29,10 @@ int main()
 RULE = [((512, 256, 8, 2, 1), 2), ((128, 2048, 8, 2, 2), 2), ((2048, 4096, 16, 1, 4), 2), ((2048, 4096, 16, 1, 5), 3),
         ((2048, 768, 64, 7, 1), 2), ((2048, 768, 64, 8, 1), 3), ((64, 64, 64, 8, 1), 2), ((64, 64, 64, 9, 1), 3),
         ((64, 16384, 16, 4, 1), 3)]                       # its h is past the LDS of the rule
-SIZES = [s for s, _ in RULE] + [(d, f, E, k, T) for d, f in [(64, 96), (2048, 768), (4096, 1536), (1184, 352), (16384, 1024), (1024, 16384), (16384, 16384)]
+# (size, threads of a gate/up workgroup)
+WAVES = [((2048, 768, 128, 8, 2), 512), ((2048, 768, 128, 8, 3), 256), ((2048, 512, 128, 8, 4), 512), ((2080, 768, 128, 8, 5), 512),
+         ((4096, 1536, 256, 8, 4), 512), ((1184, 352, 60, 4, 16), 256)]
+SIZES = [s for s, _ in RULE + WAVES] + [(d, f, E, k, T) for d, f in [(64, 96), (2048, 768), (4096, 1536), (1184, 352), (16384, 1024), (1024, 16384), (16384, 16384)]
          for E, k in [(1, 1), (8, 2), (128, 8)] for T in (1, 2, 24, 128)]
 
 
@@ -70,3 +73,11 @@ def test_which_calls_fuse_the_down_product_and_the_combine(events):
             d, f, T, k = size[0], size[1], size[4], size[3]
             assert got[0][3:5] == [f // 32, T * k], size    # gate/up: a workgroup an f-block and pair
             assert (got[1][3] == d // 32 and got[1][5] == 1024) == (n == 2), size
+
+
+def test_the_waves_of_a_pair(events):
+    """Four waves a workgroup where there are more than two a CU and a wave of eight would have a ring of K at most."""
+    it = iter([e for e in events if e[0] == "launch"][3 * sum(n for _, n in RULE):])
+    for size, threads in WAVES:
+        for dtype in range(3):
+            assert [next(it) for _ in range(3)][0][5] == threads, size
