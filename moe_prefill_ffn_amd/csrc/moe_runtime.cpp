@@ -65,6 +65,7 @@ struct moe_prefill {
     std::vector<int> slot_layer, layer_slot;
     std::vector<hipEvent_t> ev_ready, ev_free;
     std::vector<char> ready_set, free_set, from_prefetch;
+    std::vector<char> free_captured;  // ev_free was last recorded into a graph under capture
     int active = -1;
     uint64_t prefetch_counter = 0;
     uint64_t fail_at = 0;   // test hook: this prefetch enqueue (1-based) is treated as failed
@@ -392,6 +393,23 @@ hipError_t enqueue_copy(moe_prefill_t* h, int s, int layer)
     return hipSuccess;
 }
 
+// The work on st so far holds a call's last reads of slot s.  Calls on other streams may still read
+// the slot, and the event stands for them all: it follows the one recorded before.  (A stream under
+// capture cannot wait for work outside it, nor other streams for a captured event.)
+hipError_t slot_read(moe_prefill_t* h, int s, hipStream_t st)
+{
+    hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
+    hipError_t e = hipStreamIsCapturing(st, &cs);
+    const bool capturing = cs != hipStreamCaptureStatusNone;
+    if (e == hipSuccess && h->free_set[s] && !h->free_captured[s] && !capturing) e = hipStreamWaitEvent(st, h->ev_free[s], 0);
+    if (e == hipSuccess) e = hipEventRecord(h->ev_free[s], st);
+    if (e != hipSuccess) return e;
+    h->free_set[s] = 1;
+    h->free_captured[s] = capturing;
+    h->active = s;
+    return hipSuccess;
+}
+
 // Pool memory for n slots of slot_bytes: a reserved address range with one physical
 // allocation mapped per slot (vmm), else one hipMalloc.  On failure nothing is left allocated.
 hipError_t pool_alloc(moe_prefill_t* h, int n, uint64_t slot_bytes)
@@ -570,6 +588,7 @@ void pool_release(moe_prefill_t* h)
     h->ev_free.clear();
     h->ready_set.clear();
     h->free_set.clear();
+    h->free_captured.clear();
     h->from_prefetch.clear();
     h->slot_kind.clear();
     h->res_live = h->depth_live = 0;
@@ -910,13 +929,11 @@ int moe_prefill_run_layer(moe_prefill_t* h, const moe_layer_io_t* io_in, void* s
         return hip_fail(h, e, "layer launch");
     }
     if (slot >= 0) {
-        e = hipEventRecord(h->ev_free[slot], st);   // the down GEMM was the last reader
+        e = slot_read(h, slot, st);                 // the down GEMM was the last reader
         if (e != hipSuccess) {
             h->mask_dirty = true;
             return hip_fail(h, e, "hipEventRecord");
         }
-        h->free_set[slot] = 1;
-        h->active = slot;
     }
     e = launch_combine(LL, st);
     if (e != hipSuccess) {
@@ -1086,10 +1103,8 @@ int moe_decode_run_layer(moe_prefill_t* h, const moe_decode_io_t* io_in, void* s
         if (e == hipSuccess) e = launch_decode_products(D, st);
         if (e != hipSuccess) return hip_fail(h, e, "decode: launch");
         if (W.slot >= 0) {
-            e = hipEventRecord(h->ev_free[W.slot], st);   // the down product was the last reader
+            e = slot_read(h, W.slot, st);                 // the down product was the last reader
             if (e != hipSuccess) return hip_fail(h, e, "hipEventRecord");
-            h->free_set[W.slot] = 1;
-            h->active = W.slot;
         }
         e = launch_decode_combine(D, st);
         if (e != hipSuccess) return hip_fail(h, e, "decode: launch");
@@ -1355,6 +1370,7 @@ int stream_pool_configure(moe_prefill_t* h, stream_pool_params_t* inout)
     h->ev_free.assign(s.slots, nullptr);
     h->ready_set.assign(s.slots, 0);
     h->free_set.assign(s.slots, 0);
+    h->free_captured.assign(s.slots, 0);
     h->from_prefetch.assign(s.slots, 0);
     h->slot_kind.assign(s.slots, kSlotStreaming);
     for (int i = 0; i < s.residents; ++i) h->slot_kind[i] = kSlotResident;
