@@ -224,7 +224,7 @@ def _plain_combine(s):
 
 def _plain_lora(s):
     c = s["case"]
-    x, y = s["x"].float(), s["base"].float()
+    x, y = s["x"].float(), s["base"].float().clone()      # the sum is not the base's: it is read again by the next pass
     for i in range(c["n"]):
         at = torch.nonzero(s["adapters"] == i).flatten()
         y[at] += (x[at] @ s["a"][i].float().t()) @ s["b"][i].float().t() * s["scales"][i]
