@@ -228,8 +228,8 @@ int moe_prefill_run_layer_noalloc(const moe_prefill_params_t* p, const moe_layer
 
 /* ---------------------------------------------------- element types --- */
 
-/* Types of the activations that the few-token layer and the MXFP4 operators
- * take and return. */
+/* Types of the matrices that the few-token layer, the MXFP4 operators and those of
+ * 16-bit experts and adapters take and return. */
 enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 };
 
 /* -------------------------------------------------- a few tokens' layer --- */
@@ -366,6 +366,154 @@ typedef struct moe_mxfp4_gemm_args {
 } moe_mxfp4_gemm_args_t;
 
 int moe_mxfp4_gemm(const moe_mxfp4_gemm_args_t* a, void* stream);
+
+/* ------------------------------------------- experts in 16 bits --- */
+/*
+ * What a layer of 16-bit experts takes, whatever its router: the row table of the
+ * chosen experts, the products over its groups, and the weighted sum of the experts'
+ * rows per token.  The table, bounds and pair order are those that
+ * moe_prefill_run_layer exports (page #663, "What": row table, group bounds, grouped
+ * products, combine), so the MXFP4 products run over a table of moe_group_rows as
+ * well, and these products over an exported one.
+ *
+ * As the MXFP4 calls, these need no handle: `device` names the HIP device whose memory
+ * the pointers are, and failures are read with moe_prefill_last_error(NULL).  They
+ * allocate nothing and keep no state; calls on different streams are independent (with
+ * a workspace each where they take one), all can be captured in a HIP graph, and the
+ * same call gives the same bits.
+ */
+
+/* The row table of n_pairs pairs p, pair p belonging to group eidx[p] (p = t * top_k + j:
+ * slot j of token t).  A pair whose eidx is outside [0, n_groups) (an empty slot: -1) is
+ * in no group.
+ *   bounds[e] .. bounds[e+1]  rows of group e, bounds[0] = 0
+ *   rows[r]                   the pair of row r, ascending inside a group; behind
+ *                             bounds[n_groups] left as it was
+ *   pos[p]                    its row, -1 for a pair in no group */
+typedef struct moe_group_args {
+    uint32_t struct_size;
+    int32_t device;            /* HIP device ordinal */
+    const int32_t* eidx;       /* device [n_pairs] */
+    int64_t n_pairs;           /* 0 .. 2^27 (0: all bounds are 0) */
+    int32_t n_groups;          /* 1..1024 */
+    int32_t reserved0;
+    int32_t* bounds;           /* device [n_groups + 1] */
+    int32_t* rows;             /* device [n_pairs], NULL: not wanted */
+    int32_t* pos;              /* device [n_pairs], NULL: not wanted; may be eidx */
+    int32_t* counts;           /* device [n_groups] pairs of each group, NULL: not wanted */
+    void* workspace;           /* device scratch, 256-byte aligned, for this call alone until it
+                                  has finished; NULL where moe_group_workspace_size() is 0 */
+    uint64_t workspace_bytes;
+} moe_group_args_t;
+
+/* Device bytes of moe_group_args_t::workspace (0 up to 4096 pairs).  Host only. */
+int moe_group_workspace_size(int64_t n_pairs, int32_t n_groups, uint64_t* bytes);
+int moe_group_rows(const moe_group_args_t* a, void* stream);
+
+/*
+ * out[r, n] = sum over K of A[src(r), :] B[g(r), n, :] in fp32, rounded once to
+ * out_dtype; with swiglu B has 2N rows a group (N gate rows, then N up rows) and
+ * out[r, n] = silu(gate) * up.  bounds, rows, top_k: as moe_mxfp4_gemm_args_t, unsound
+ * values of them included; rows in no group are left as they were.  Infinities and
+ * NaN go the way of the sum that they enter and reach no other element.  Another row
+ * count may take another order of the sum over K.
+ */
+typedef struct moe_grouped_gemm_args {
+    uint32_t struct_size;
+    int32_t device;
+    const void* a;             /* device [a_rows, K], rows a_stride elements apart; rows 16-byte aligned */
+    int64_t a_stride;          /* >= K */
+    int64_t a_rows;            /* >= 1 if M > 0, < 2^31 */
+    const void* b;             /* device [n_groups, N or 2N, K], rows 16-byte aligned */
+    int64_t b_stride;          /* elements from a row of B to the next, >= K */
+    int64_t b_group_stride;    /* elements from a group's first row to the next group's (any if n_groups is 1) */
+    const int32_t* bounds;     /* device [n_groups + 1], ascending within [0, M]; NULL: dense */
+    const int32_t* rows;       /* device [M]; NULL: in order */
+    int32_t n_groups;          /* 1..65535 (1 if dense) */
+    int32_t top_k;             /* >= 1 */
+    int64_t M;                 /* rows of out, 0 (a no-op) .. 2^27, and
+                                  (M / 32 + n_groups) * ceil(N / 32) <= 2^30 */
+    int32_t N, K;              /* N in 1..2^20, K a multiple of 8 in 8..2^20 */
+    int32_t swiglu;            /* 0 or 1 */
+    int32_t dtype;             /* of A and B: MOE_BF16 or MOE_F16 */
+    int32_t out_dtype;         /* MOE_F32 or dtype */
+    int32_t reserved0;
+    void* out;                 /* device [M, N], rows out_stride elements apart; overlaps neither A nor B */
+    int64_t out_stride;        /* >= N */
+} moe_grouped_gemm_args_t;
+
+int moe_grouped_gemm(const moe_grouped_gemm_args_t* a, void* stream);
+
+/*
+ * y[t, :] = base[t, :] + sum over j of weights[t, j] * d[pos[t, j], :], summed in slot
+ * order in fp32 and rounded once.  A slot whose pos is outside [0, d_rows) (-1: an empty
+ * slot) is left out, whatever its weight.  base NULL: 0.
+ */
+typedef struct moe_combine_args {
+    uint32_t struct_size;
+    int32_t device;
+    const void* d;             /* device [d_rows, N], rows d_stride elements apart */
+    int64_t d_stride;          /* >= N */
+    int64_t d_rows;            /* 0 .. 2^31 - 1 */
+    const float* weights;      /* device [n_tokens, top_k] */
+    const int32_t* pos;        /* device [n_tokens, top_k] */
+    const void* base;          /* device [n_tokens, N], rows base_stride elements apart, or NULL; may be y */
+    int64_t base_stride;       /* >= N */
+    void* y;                   /* device [n_tokens, N], rows y_stride elements apart */
+    int64_t y_stride;          /* >= N */
+    int64_t n_tokens;          /* 0 (a no-op) .. 2^23 */
+    int32_t N;                 /* 1..2^20 */
+    int32_t top_k;             /* 1..1024 */
+    int32_t d_dtype;           /* MOE_F32 / MOE_BF16 / MOE_F16 */
+    int32_t base_dtype;
+    int32_t y_dtype;
+    int32_t reserved0;
+} moe_combine_args_t;
+
+int moe_combine_rows(const moe_combine_args_t* a, void* stream);
+
+/* ------------------------------------------------ low-rank adapters --- */
+/*
+ * The adapters of many requests beside one shared projection (moe_mxfp4_gemm or
+ * moe_grouped_gemm, whose output is `base`):
+ *
+ *   out[t, :] = base[t, :] + scales[i] * ((x[t, :] A_i^T) B_i^T),  i = adapters[t]
+ *
+ * A row whose adapter is outside [0, n_adapters) (-1: none) gets out = base.  Rows of an
+ * adapter may stand anywhere.  x A_i^T is summed in fp32 and enters the second product with
+ * 16 bits or more of it (22 or more for an fp32 out); the rest is fp32, rounded once.  An
+ * infinity or a NaN in an adapter, or in a row of x, reaches the rows that use it only.
+ * No handle, as the calls above; same bits for the same call.
+ */
+typedef struct moe_lora_args {
+    uint32_t struct_size;
+    int32_t device;
+    const void* x;             /* device [M, K], rows x_stride elements apart; rows 16-byte aligned */
+    int64_t x_stride;          /* >= K */
+    const void* a;             /* device [n_adapters, rank, K], 16-byte aligned */
+    const void* b;             /* device [n_adapters, N, rank], 16-byte aligned */
+    const int32_t* adapters;   /* device [M] */
+    const float* scales;       /* device [n_adapters], NULL: 1 */
+    const void* base;          /* device [M, N], rows base_stride elements apart, or NULL (0); may be out */
+    int64_t base_stride;       /* >= N */
+    void* out;                 /* device [M, N], rows out_stride elements apart */
+    int64_t out_stride;        /* >= N */
+    int64_t M;                 /* 0 (a no-op) .. 2^23 */
+    int32_t N, K;              /* N in 1..2^20, K a multiple of 8 in 8..2^20 */
+    int32_t rank;              /* a multiple of 8 in 8..256; a smaller rank is padded with zeros */
+    int32_t n_adapters;        /* 1..2^20 */
+    int32_t dtype;             /* of x, a and b: MOE_BF16 or MOE_F16 */
+    int32_t base_dtype;        /* MOE_F32 / MOE_BF16 / MOE_F16 */
+    int32_t out_dtype;
+    int32_t reserved0;
+    void* workspace;           /* device scratch, 256-byte aligned, for this call alone until it
+                                  has finished */
+    uint64_t workspace_bytes;  /* >= moe_lora_workspace_size() for these sizes */
+} moe_lora_args_t;
+
+/* Device bytes of moe_lora_args_t::workspace, for M rows or fewer.  Host only. */
+int moe_lora_workspace_size(int64_t M, int32_t K, int32_t rank, uint64_t* bytes);
+int moe_lora_add(const moe_lora_args_t* a, void* stream);
 
 /* ---------------------------------------------------------- stream pool --- */
 

@@ -1,5 +1,5 @@
-"""MI355X-native MoE prompt (prefill) FFN layer, the same layer for a few tokens, and the
-MXFP4 operators -- Python binding.
+"""MI355X-native MoE prompt (prefill) FFN layer, the same layer for a few tokens, the MXFP4
+operators, and those of 16-bit experts and low-rank adapters -- Python binding.
 
 A thin ctypes binding of ``libmoe_prefill.so`` (C ABI in
 ``include/moe_prefill.h``).  It only marshals arguments: routing, grouping,
@@ -72,9 +72,41 @@ class moe_mxfp4_gemm_args_t(ctypes.Structure):
                 ("out", _vp), ("out_stride", _i64)]
 
 
+class moe_group_args_t(ctypes.Structure):
+    _fields_ = [("struct_size", _u32), ("device", _i32), ("eidx", _vp), ("n_pairs", _i64), ("n_groups", _i32),
+                ("reserved0", _i32), ("bounds", _vp), ("rows", _vp), ("pos", _vp), ("counts", _vp),
+                ("workspace", _vp), ("workspace_bytes", _u64)]
+
+
+class moe_grouped_gemm_args_t(ctypes.Structure):
+    _fields_ = [("struct_size", _u32), ("device", _i32), ("a", _vp), ("a_stride", _i64), ("a_rows", _i64),
+                ("b", _vp), ("b_stride", _i64), ("b_group_stride", _i64), ("bounds", _vp), ("rows", _vp),
+                ("n_groups", _i32), ("top_k", _i32), ("M", _i64), ("N", _i32), ("K", _i32), ("swiglu", _i32),
+                ("dtype", _i32), ("out_dtype", _i32), ("reserved0", _i32), ("out", _vp), ("out_stride", _i64)]
+
+
+class moe_combine_args_t(ctypes.Structure):
+    _fields_ = [("struct_size", _u32), ("device", _i32), ("d", _vp), ("d_stride", _i64), ("d_rows", _i64),
+                ("weights", _vp), ("pos", _vp), ("base", _vp), ("base_stride", _i64), ("y", _vp), ("y_stride", _i64),
+                ("n_tokens", _i64), ("N", _i32), ("top_k", _i32), ("d_dtype", _i32), ("base_dtype", _i32),
+                ("y_dtype", _i32), ("reserved0", _i32)]
+
+
+class moe_lora_args_t(ctypes.Structure):
+    _fields_ = [("struct_size", _u32), ("device", _i32), ("x", _vp), ("x_stride", _i64), ("a", _vp), ("b", _vp),
+                ("adapters", _vp), ("scales", _vp), ("base", _vp), ("base_stride", _i64), ("out", _vp),
+                ("out_stride", _i64), ("M", _i64), ("N", _i32), ("K", _i32), ("rank", _i32), ("n_adapters", _i32),
+                ("dtype", _i32), ("base_dtype", _i32), ("out_dtype", _i32), ("reserved0", _i32),
+                ("workspace", _vp), ("workspace_bytes", _u64)]
+
+
 _DECODE_IO_SIZE = ctypes.sizeof(moe_decode_io_t)
 _MX_MATRIX_SIZE = ctypes.sizeof(moe_mxfp4_matrix_t)
 _MX_GEMM_SIZE = ctypes.sizeof(moe_mxfp4_gemm_args_t)
+_GROUP_SIZE = ctypes.sizeof(moe_group_args_t)
+_GROUPED_GEMM_SIZE = ctypes.sizeof(moe_grouped_gemm_args_t)
+_COMBINE_SIZE = ctypes.sizeof(moe_combine_args_t)
+_LORA_SIZE = ctypes.sizeof(moe_lora_args_t)
 
 MOE_F32, MOE_BF16, MOE_F16 = 0, 1, 2
 _DTYPE_ID = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
@@ -139,6 +171,8 @@ EXPORTED_SYMBOLS = [
     "moe_prefill_exp_host", "moe_prefill_exp_device", "moe_prefill_run_layer_noalloc",
     "moe_decode_workspace_size", "moe_decode_run_layer",
     "moe_mxfp4_quantize", "moe_mxfp4_dequantize", "moe_mxfp4_gemm",
+    "moe_group_workspace_size", "moe_group_rows", "moe_grouped_gemm", "moe_combine_rows",
+    "moe_lora_workspace_size", "moe_lora_add",
 ]
 
 _lib = None
@@ -184,6 +218,12 @@ def lib():
     L.moe_mxfp4_quantize.argtypes = [ctypes.POINTER(moe_mxfp4_matrix_t), _vp]
     L.moe_mxfp4_dequantize.argtypes = [ctypes.POINTER(moe_mxfp4_matrix_t), _vp]
     L.moe_mxfp4_gemm.argtypes = [ctypes.POINTER(moe_mxfp4_gemm_args_t), _vp]
+    L.moe_group_workspace_size.argtypes = [_i64, _i32, ctypes.POINTER(_u64)]
+    L.moe_group_rows.argtypes = [ctypes.POINTER(moe_group_args_t), _vp]
+    L.moe_grouped_gemm.argtypes = [ctypes.POINTER(moe_grouped_gemm_args_t), _vp]
+    L.moe_combine_rows.argtypes = [ctypes.POINTER(moe_combine_args_t), _vp]
+    L.moe_lora_workspace_size.argtypes = [_i64, _i32, _i32, ctypes.POINTER(_u64)]
+    L.moe_lora_add.argtypes = [ctypes.POINTER(moe_lora_args_t), _vp]
     _lib = L
     return L
 
@@ -605,6 +645,205 @@ def moe_mxfp4_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch
         bounds.data_ptr() if bounds is not None else None, rows.data_ptr() if rows is not None else None, G, top_k, M, N, K,
         1 if swiglu else 0, out_dtype, out.data_ptr(), _rows_of(out, "out", M, N, index))
     rc = lib().moe_mxfp4_gemm(a, raw)
+    if rc:
+        _check(rc)
+    return out
+
+
+# ---------------------------------------------------- experts in 16 bits ---
+
+def _vector(t: torch.Tensor, name: str, shape, dtype, index: int) -> int:
+    """Address of a contiguous tensor of that shape and type on device `index`."""
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype or t.get_device() != index or not t.is_contiguous():
+        raise TypeError(f"{name}: expected a contiguous {dtype} tensor on device {index}")
+    return t.data_ptr()
+
+
+def _workspace(workspace: Optional[torch.Tensor], nbytes: Callable[[], int], index: int,
+               stream: Optional[torch.cuda.Stream]):
+    """(tensor to keep until the call is enqueued, address, bytes) of a caller's workspace, or of one of
+    nbytes() from torch's allocator."""
+    if workspace is None:
+        n = nbytes()
+        if n == 0:
+            return None, None, 0
+        workspace = _scratch(n, torch.uint8, index, stream)
+    elif workspace.get_device() != index:
+        raise TypeError(f"workspace: expected a tensor on device {index}")
+    return workspace, _dev_ptr(workspace, torch.uint8, "workspace") if workspace.numel() else None, workspace.numel()
+
+
+def moe_group_workspace_size(n_pairs: int, n_groups: int) -> int:
+    """Bytes of moe_group_rows' workspace (0: it needs none)."""
+    out = _u64()
+    _check(lib().moe_group_workspace_size(n_pairs, n_groups, ctypes.byref(out)))
+    return int(out.value)
+
+
+def moe_group_rows(eidx: torch.Tensor, n_groups: int, bounds: Optional[torch.Tensor] = None,
+                   rows: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None,
+                   counts: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None):
+    """The row table of the experts that a router chose: (bounds, rows, pos).
+
+    eidx: int32, contiguous, [T, k] or any shape; pair p is its p-th element, in no group where it is
+    outside [0, n_groups).  bounds int32 [n_groups + 1]; rows int32 [P], the pairs in group order, ascending
+    inside a group, untouched behind bounds[n_groups]; pos int32 like eidx, each pair's row, -1: none.
+    counts: int32 [n_groups], filled if given.  workspace: device uint8 scratch of
+    moe_group_workspace_size() bytes that no other call in flight uses."""
+    index = _mx_device(eidx, "eidx")
+    P = eidx.numel()
+    at = _vector(eidx, "eidx", eidx.shape, torch.int32, index)
+    raw = _stream_of(stream, index)
+    keep, ws, ws_bytes = _workspace(workspace, lambda: moe_group_workspace_size(P, n_groups), index, stream)
+    if bounds is None:
+        bounds = _result((n_groups + 1,), torch.int32, index, stream)
+    if rows is None:
+        rows = _result((P,), torch.int32, index, stream)
+    if pos is None:
+        pos = _result(tuple(eidx.shape), torch.int32, index, stream)
+    a = moe_group_args_t(_GROUP_SIZE, index, at, P, n_groups, 0, _vector(bounds, "bounds", (n_groups + 1,), torch.int32, index),
+                         _vector(rows, "rows", (P,), torch.int32, index), _vector(pos, "pos", eidx.shape, torch.int32, index),
+                         _vector(counts, "counts", (n_groups,), torch.int32, index) if counts is not None else None, ws, ws_bytes)
+    rc = lib().moe_group_rows(a, raw)
+    if rc:
+        _check(rc)
+    return bounds, rows, pos
+
+
+def moe_grouped_gemm(a: torch.Tensor, b: torch.Tensor, out: Optional[torch.Tensor] = None,
+                     dtype: Optional[torch.dtype] = None, bounds: Optional[torch.Tensor] = None,
+                     rows: Optional[torch.Tensor] = None, top_k: int = 1, swiglu: bool = False,
+                     stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """out[r] = A[src(r)] B[g(r)]^T of bf16 or fp16 matrices (fp32 sums, one rounding to out's type).
+
+    a [A, K] (rows may be strided), b [N, K] or [G, N, K] (its rows and groups too; K a multiple of 8, rows
+    16-byte aligned); with swiglu B has 2N rows a group, gate then up.  bounds: int32 [G + 1], group g's rows
+    of out; rows: int32 [M], src(r) = rows[r] // top_k; without rows src(r) = r // top_k and M = A * top_k.
+    out (or a new tensor of ``dtype``): a's type (the default) or float32.  Rows of out in no group are left as
+    they were."""
+    index = _mx_device(a, "a")
+    b_shape = b.shape
+    if a.dim() != 2 or len(b_shape) not in (2, 3):
+        raise ValueError("a: expected a matrix; b: a matrix, or one per group")
+    if top_k < 1:
+        raise ValueError("top_k must be at least 1")
+    A, K = a.shape
+    G = b_shape[0] if len(b_shape) == 3 else 1
+    NB = b_shape[-2]
+    if swiglu and NB % 2:
+        raise ValueError("b: swiglu needs gate and up rows, an even number")
+    in_dtype = _DTYPE_ID.get(a.dtype)
+    if in_dtype not in (MOE_BF16, MOE_F16) or b.dtype != a.dtype or b.get_device() != index:
+        raise TypeError(f"a and b: expected the same of bfloat16, float16, on device {index}")
+    if b_shape[-1] != K:
+        raise ValueError(f"b: expected rows of {K}")
+    N = NB // 2 if swiglu else NB
+    M = rows.shape[0] if rows is not None else A * top_k
+    if b.stride(-1) != 1 and K > 1:
+        raise ValueError("b: rows must be contiguous")
+    b_stride = b.stride(-2) if NB > 1 else K
+    if b_stride < K:
+        raise ValueError("b: rows overlap")
+    raw = _stream_of(stream, index)
+    if bounds is None and G != 1:
+        raise ValueError("b of several groups needs bounds")
+    bounds_at = _vector(bounds, "bounds", (G + 1,), torch.int32, index) if bounds is not None else None
+    rows_at = _vector(rows, "rows", (M,), torch.int32, index) if rows is not None else None
+    if out is None:
+        out = _result((M, N), a.dtype if dtype is None else dtype, index, stream)
+    out_dtype = _DTYPE_ID.get(out.dtype)
+    if out_dtype not in (MOE_F32, in_dtype):
+        raise TypeError("out: expected float32 or the type of a")
+    args = moe_grouped_gemm_args_t(
+        _GROUPED_GEMM_SIZE, index, a.data_ptr(), _rows_of(a, "a", A, K, index), A, b.data_ptr(), b_stride,
+        b.stride(0) if G > 1 else 0, bounds_at, rows_at, G, top_k, M, N, K, 1 if swiglu else 0, in_dtype, out_dtype, 0,
+        out.data_ptr(), _rows_of(out, "out", M, N, index))
+    rc = lib().moe_grouped_gemm(args, raw)
+    if rc:
+        _check(rc)
+    return out
+
+
+def moe_combine_rows(d: torch.Tensor, weights: torch.Tensor, pos: torch.Tensor, y: Optional[torch.Tensor] = None,
+                     base: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None,
+                     stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """y[t] = base[t] + sum_j weights[t, j] * d[pos[t, j]], summed in slot order in fp32, rounded once.
+
+    d [R, N], base [T, N] (None: 0; may be y) and y (or a new tensor of ``dtype``, by default d's type): fp32, bf16
+    or fp16 each, rows may be strided.  weights fp32, pos int32, [T, k]; a slot whose pos is outside [0, R)
+    is left out."""
+    index = _mx_device(d, "d")
+    if d.dim() != 2 or pos.dim() != 2:
+        raise ValueError("d and pos: expected matrices")
+    R, N = d.shape
+    T, k = pos.shape
+    raw = _stream_of(stream, index)
+    weights_at = _vector(weights, "weights", (T, k), torch.float32, index)
+    pos_at = _vector(pos, "pos", (T, k), torch.int32, index)
+    if y is None:
+        y = _result((T, N), d.dtype if dtype is None else dtype, index, stream)
+    types = [_DTYPE_ID.get(t.dtype) if t is not None else MOE_F32 for t in (d, base, y)]
+    if None in types:
+        raise TypeError("d, base and y: expected float32, bfloat16 or float16")
+    args = moe_combine_args_t(
+        _COMBINE_SIZE, index, d.data_ptr(), _rows_of(d, "d", R, N, index), R, weights_at, pos_at,
+        base.data_ptr() if base is not None else None, _rows_of(base, "base", T, N, index) if base is not None else 0,
+        y.data_ptr(), _rows_of(y, "y", T, N, index), T, N, k, *types, 0)
+    rc = lib().moe_combine_rows(args, raw)
+    if rc:
+        _check(rc)
+    return y
+
+
+# ----------------------------------------------------- low-rank adapters ---
+
+def moe_lora_workspace_size(M: int, K: int, rank: int) -> int:
+    """Bytes of moe_lora_add's workspace for M rows or fewer."""
+    out = _u64()
+    _check(lib().moe_lora_workspace_size(M, K, rank, ctypes.byref(out)))
+    return int(out.value)
+
+
+def moe_lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapters: torch.Tensor,
+                 base: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                 scales: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None,
+                 workspace: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """out[t] = base[t] + scales[i] * (x[t] A_i^T) B_i^T with i = adapters[t]; a row whose adapter is outside
+    [0, n) (-1) gets base[t].  Returns out.
+
+    x [M, K], a [n, rank, K] and b [n, N, rank]: the same of bf16, fp16 (K and rank multiples of 8, rank up to
+    256); adapters int32 [M]; scales fp32 [n] (None: 1); base [M, N] (None: 0; may be out) and out (or a new
+    tensor of ``dtype``, by default x's type): fp32, bf16 or fp16 each.  Rows of x, base and out may be
+    strided.  workspace: device uint8 scratch of moe_lora_workspace_size() bytes that no other call in flight
+    uses; without one the call takes it from torch's allocator, on ``stream``."""
+    index = _mx_device(x, "x")
+    if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("x: expected a matrix; a and b: one per adapter")
+    M, K = x.shape
+    n, r = a.shape[:2]
+    N = b.shape[1]
+    in_dtype = _DTYPE_ID.get(x.dtype)
+    if in_dtype not in (MOE_BF16, MOE_F16):
+        raise TypeError("x: expected bfloat16 or float16")
+    a_at, b_at = _vector(a, "a", (n, r, K), x.dtype, index), _vector(b, "b", (n, N, r), x.dtype, index)
+    adapters_at = _vector(adapters, "adapters", (M,), torch.int32, index)
+    scales_at = _vector(scales, "scales", (n,), torch.float32, index) if scales is not None else None
+    raw = _stream_of(stream, index)
+    keep, ws, ws_bytes = _workspace(workspace, lambda: moe_lora_workspace_size(M, K, r), index, stream)
+    if out is None:
+        out = _result((M, N), x.dtype if dtype is None else dtype, index, stream)
+    types = [_DTYPE_ID.get(t.dtype) if t is not None else MOE_F32 for t in (base, out)]
+    if None in types:
+        raise TypeError("base and out: expected float32, bfloat16 or float16")
+    args = moe_lora_args_t(
+        _LORA_SIZE, index, x.data_ptr(), _rows_of(x, "x", M, K, index), a_at, b_at, adapters_at, scales_at,
+        base.data_ptr() if base is not None else None, _rows_of(base, "base", M, N, index) if base is not None else 0,
+        out.data_ptr(), _rows_of(out, "out", M, N, index), M, N, K, r, n, in_dtype, *types, 0, ws, ws_bytes)
+    rc = lib().moe_lora_add(args, raw)
     if rc:
         _check(rc)
     return out

@@ -15,16 +15,14 @@
 #include "moe_dtype.h"
 #include "moe_math.h"
 #include "moe_mx.h"
+#include "moe_tile.h"
 
 namespace moe {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v2f __attribute__((ext_vector_type(2)));
-typedef float v16f __attribute__((ext_vector_type(16)));
 
 namespace {
-
-unsigned nblk(int64_t n, int per) { return (unsigned)((n + per - 1) / per); }
 
 // 2^(s - 127); s = 0 is the fp32 subnormal 2^-127, s = 255 NaN
 __device__ __forceinline__ float e8m0(uint32_t s)
@@ -150,8 +148,6 @@ __global__ __launch_bounds__(kQuantThreads) void k_mx_dequantize(MxQuant q, int6
 //
 // A block past the end of K is read from the last block (in bounds, any finite codes) with
 // scale byte 0 on both sides: 2^-254 of a product below 2^11 is 0 in fp32.
-typedef int v4i __attribute__((ext_vector_type(4)));
-
 // A row of the product reads this row of A.
 __device__ __forceinline__ int64_t a_row(const MxGemm& a, int64_t r)
 {
@@ -169,53 +165,7 @@ __device__ __forceinline__ v16f mfma_fp4(v4i w, v4i x, v16f c, int sw, int sx)
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, x8, c, 4, 4, step, sw, step, sx);   // 4: E2M1
 }
 
-// A bound, clamped into [0, M].
-__device__ __forceinline__ int bound_of(const MxGemm& a, int g)
-{
-    const int64_t b = a.bounds[g];
-    return (int)(b < 0 ? 0 : b > a.M ? a.M : b);
-}
-
-// silu(g) u by the hardware's exp2 and reciprocal (an ulp each).  exp(-g) = 2^t (1 + ln2 r), t the
-// rounded -g log2(e) and r what the rounding left, so that a large |g| costs no bits.
-__device__ __forceinline__ float silu_mul(float g, float u)
-{
-    const float log2e = 0x1.715476p+0f, log2e_lo = 0x1.4ae0c0p-26f;   // the fp32 nearest log2(e), and the rest
-    const float t = -g * log2e;
-    const float r = __builtin_fmaf(-g, log2e, -t) - g * log2e_lo;
-    const float p = __builtin_amdgcn_exp2f(t);
-    // past the range of exp (p = 0 or infinity) there is nothing to correct
-    const float e = t > -126.0f && t < 128.0f ? __builtin_fmaf(p, 0x1.62e430p-1f * r, p) : p;
-    return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
-}
-
 // ------------------------------------------------------------- tiled kernel ---
-// Direct global->LDS loads, lane i's bytes at wave_base + size * i; inline asm so that the
-// compiler does not drain them (the ring waits for them itself).
-__device__ __forceinline__ uint32_t lds_addr(const void* p)
-{
-    return __builtin_amdgcn_readfirstlane(
-        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p);
-}
-__device__ __forceinline__ void g2lds16(const void* g, uint32_t lds)
-{
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(lds) : "memory", "m0");
-}
-// the same from a wave-uniform base and 32 bits of offset a lane
-__device__ __forceinline__ void g2lds16_at(const uint8_t* base, uint32_t off, uint32_t lds)
-{
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory", "m0");
-}
-__device__ __forceinline__ void g2lds4(const void* g, uint32_t lds)
-{
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(lds) : "memory", "m0");
-}
-
-// Chunk c (16 bytes, one block) of a 128-byte row r sits in slot c ^ swz(r): any 8
-// consecutive rows touch 8 distinct 16-byte bank groups of 128 bytes, any 16 rows 16
-// distinct ones of 256.
-__device__ __forceinline__ int swz(int r) { return (r ^ ((r >> 3) & 1)) & 7; }
-
 // WM x WN waves, each TM x TN tiles of 32 x 32: BM rows of A by BN rows of B, K in stages of
 // 256 codes (128 bytes a row) through two LDS slots.
 //
@@ -235,12 +185,6 @@ struct MxShape {
 // a row every second stage; two words a row and stage; three words a row and stage around
 // bytes at any address.
 enum ScaleMode { kScale16, kScale4, kScale1 };
-
-constexpr int kListMost = 256;                            // tiles a workgroup lists at a time
-
-struct ListedTile {
-    int g, m0, m1, nt;
-};
 
 template <class S, int kMode>
 struct MxLds {
@@ -720,47 +664,12 @@ __global__ __launch_bounds__(64 * S::NW) void k_mx_tile(MxGemm a, int n_tiles, i
 // operands' first bytes, the waves' sums.
 constexpr int kFewWaves = 8, kFewRows = 32;
 
-// Groups of a row table: row slot s belongs to the last group g whose first slot
-// bounds[g] / 32 + g is <= s (a group of c rows never needs more than the
-// bounds[g + 1] / 32 + 1 - bounds[g] / 32 slots up to the next group's first), so a
-// workgroup finds its rows from the bounds alone, and where there is nothing to do it ends.
-struct Rows {
-    int g;
-    int64_t m0, m1;           // rows [m0, m1); m0 >= m1: nothing to do
-};
-
-// The rows of a slot, the same on all lanes, by the wave together.
-__device__ __forceinline__ Rows rows_of_slot(const MxGemm& a, int64_t slot)
-{
-    if (!a.bounds) {
-        const int64_t m0 = slot * kFewRows;
-        return {0, m0, m0 + kFewRows < a.M ? m0 + kFewRows : a.M};
-    }
-    // 64 groups are compared at a time, one per lane: two rounds of loads up to 4096 groups
-    int g = 0, span = a.G;
-    const int lane = threadIdx.x & 63;
-    while (span > 1) {
-        const int step = (span + 63) >> 6, at = g + lane * step;
-        const bool le = lane * step < span && (int64_t)(bound_of(a, at) / kFewRows) + at <= slot;
-        const int n = __popcll(__ballot(le));             // a run of lanes from 0 for bounds that ascend
-        const int skip = (n > 0 ? n - 1 : 0) * step;
-        g += skip;
-        span = span - skip < step ? span - skip : step;
-    }
-    g = __builtin_amdgcn_readfirstlane(g);
-    const int64_t b0 = bound_of(a, g), b1 = bound_of(a, g + 1);
-    int64_t m0 = b0 + (slot - (b0 / kFewRows + g)) * kFewRows;
-    const int64_t m1 = m0 + kFewRows < b1 ? m0 + kFewRows : b1;
-    if (m0 < b0) m0 = m1;                                 // bounds that do not ascend: nothing before the group's rows
-    return {g, m0, m1};
-}
-
 template <int kT, bool kSwiglu, bool kAligned>
 __global__ __launch_bounds__(64 * kFewWaves) void k_mx_few(MxGemm a)
 {
     constexpr int NT = kSwiglu ? 2 : 1;
     __shared__ float red[kFewWaves][NT][32][33];
-    const Rows t = rows_of_slot(a, blockIdx.x);
+    const Rows t = rows_of_slot<kFewRows>(a, blockIdx.x);
     if (t.m0 >= t.m1) return;                             // uniform
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, j = lane & 31;
     const int nb = a.K / 32, NB = kSwiglu ? 2 * a.N : a.N;

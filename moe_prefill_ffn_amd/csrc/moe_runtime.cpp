@@ -19,10 +19,13 @@
 #include "../../include/moe_prefill.h"
 #include "moe_decode.h"
 #include "moe_dtype.h"
+#include "moe_gemm16.h"
 #include "moe_kernels.h"
 #include "moe_layout.h"
+#include "moe_lora.h"
 #include "moe_mx.h"
 #include "moe_pool_plan.h"
+#include "moe_rows.h"
 
 namespace moe {
 bool pack_expert(int d, int f, const int8_t* wgu_q, const uint16_t* wgu_s, const int8_t* wd_q,
@@ -1209,6 +1212,252 @@ int moe_mxfp4_gemm(const moe_mxfp4_gemm_args_t* in, void* stream)
         g.dtype = a.dtype;
         const hipError_t e = launch_mx_gemm(g, static_cast<hipStream_t>(stream));
         if (e != hipSuccess) return hip_fail(nullptr, e, "mxfp4: launch");
+        g_err.clear();
+        return (int)MOE_OK;
+    });
+}
+
+// ------------------------------------------------------ experts in 16 bits ---
+
+int moe_group_workspace_size(int64_t n_pairs, int32_t n_groups, uint64_t* bytes)
+{
+    return guarded(nullptr, [&] {
+        if (!bytes) return fail(nullptr, MOE_EINVAL, "null bytes pointer");
+        if (n_pairs < 0 || n_pairs > kGroupMostPairs) return fail(nullptr, MOE_EINVAL, "group: n_pairs must be in [0, 2^27]");
+        if (n_groups < 1 || n_groups > kGroupMostGroups) return fail(nullptr, MOE_EINVAL, "group: n_groups must be in [1, 1024]");
+        *bytes = group_ws(n_pairs, n_groups);
+        g_err.clear();
+        return (int)MOE_OK;
+    });
+}
+
+int moe_group_rows(const moe_group_args_t* in, void* stream)
+{
+    return guarded(nullptr, [&] {
+        moe_group_args_t a;
+        std::string why;
+        if (!read_struct(in, &a, &why)) return fail(nullptr, MOE_EINVAL, why);
+        if (a.n_pairs < 0 || a.n_pairs > kGroupMostPairs) return fail(nullptr, MOE_EINVAL, "group: n_pairs must be in [0, 2^27]");
+        if (a.n_groups < 1 || a.n_groups > kGroupMostGroups)
+            return fail(nullptr, MOE_EINVAL, "group: n_groups must be in [1, 1024]");
+        if ((!a.eidx && a.n_pairs) || !a.bounds) return fail(nullptr, MOE_EINVAL, "group: eidx and bounds are required");
+        if ((addr(a.eidx) | addr(a.bounds) | addr(a.rows) | addr(a.pos) | addr(a.counts)) % 4)
+            return fail(nullptr, MOE_EINVAL, "group: eidx, bounds, rows, pos and counts must be 4-byte aligned");
+        const uint64_t need = group_ws(a.n_pairs, a.n_groups);
+        if (need && (!a.workspace || a.workspace_bytes < need))
+            return fail(nullptr, MOE_EINVAL, "group: workspace smaller than moe_group_workspace_size()");
+        if (need && addr(a.workspace) % 256) return fail(nullptr, MOE_EINVAL, "group: workspace must be 256-byte aligned");
+        const int rc = noalloc_device_ok(a.device);
+        if (rc != MOE_OK) return rc;
+        DevGuard guard(a.device);
+        GroupRows g{};
+        g.eidx = a.eidx;
+        g.pairs = a.n_pairs;
+        g.E = a.n_groups;
+        g.counts = a.counts;
+        g.bounds = a.bounds;
+        g.rows = a.rows;
+        g.pos = a.pos;
+        g.ws = static_cast<int32_t*>(a.workspace);
+        const hipError_t e = launch_group_rows(g, static_cast<hipStream_t>(stream));
+        if (e != hipSuccess) return hip_fail(nullptr, e, "group: launch");
+        g_err.clear();
+        return (int)MOE_OK;
+    });
+}
+
+int moe_grouped_gemm(const moe_grouped_gemm_args_t* in, void* stream)
+{
+    return guarded(nullptr, [&] {
+        moe_grouped_gemm_args_t a;
+        std::string why;
+        if (!read_struct(in, &a, &why)) return fail(nullptr, MOE_EINVAL, why);
+        if (a.dtype != MOE_BF16 && a.dtype != MOE_F16) return fail(nullptr, MOE_EINVAL, "grouped_gemm: dtype must be MOE_BF16 or MOE_F16");
+        if (a.out_dtype != MOE_F32 && a.out_dtype != a.dtype)
+            return fail(nullptr, MOE_EINVAL, "grouped_gemm: out_dtype must be MOE_F32 or dtype");
+        if (a.swiglu != 0 && a.swiglu != 1) return fail(nullptr, MOE_EINVAL, "grouped_gemm: swiglu must be 0 or 1");
+        if (a.K < 8 || a.K % 8 || a.K > (1 << 20)) return fail(nullptr, MOE_EINVAL, "grouped_gemm: K must be a multiple of 8 in [8, 2^20]");
+        if (a.N < 1 || a.N > (1 << 20)) return fail(nullptr, MOE_EINVAL, "grouped_gemm: N must be in [1, 2^20]");
+        if (a.M < 0 || a.M > kGemm16MostRows) return fail(nullptr, MOE_EINVAL, "grouped_gemm: M must be in [0, 2^27]");
+        if (a.n_groups < 1 || a.n_groups > 65535 || (!a.bounds && a.n_groups != 1))
+            return fail(nullptr, MOE_EINVAL, "grouped_gemm: n_groups must be in [1, 65535], and 1 without bounds");
+        if ((a.M / 32 + a.n_groups) * ((a.N + 31) / 32) > kGemm16MostTiles)
+            return fail(nullptr, MOE_EINVAL, "grouped_gemm: (M / 32 + n_groups) * N / 32 above 2^30; take the rows in parts");
+        if (a.top_k < 1) return fail(nullptr, MOE_EINVAL, "grouped_gemm: top_k must be at least 1");
+        if (a.M == 0) {
+            g_err.clear();
+            return (int)MOE_OK;
+        }
+        if (!a.a || !a.b || !a.out) return fail(nullptr, MOE_EINVAL, "grouped_gemm: a, b and out are required");
+        if (a.a_rows < 1 || a.a_rows > INT32_MAX || (!a.rows && a.a_rows < (a.M + a.top_k - 1) / a.top_k))
+            return fail(nullptr, MOE_EINVAL, "grouped_gemm: A has 2^31 rows or more, or fewer than the product reads");
+        if (!stride_ok(a.a_stride, a.K) || !stride_ok(a.b_stride, a.K) || !stride_ok(a.out_stride, a.N) ||
+            (a.n_groups > 1 && !stride_ok(a.b_group_stride, 0)))
+            return fail(nullptr, MOE_EINVAL, "grouped_gemm: a row stride below the row's length, a negative one, or one above 2^40");
+        if (a.n_groups == 1) a.b_group_stride = 0;
+        if ((addr(a.a) | addr(a.b) | (uint64_t)(a.a_stride * 2) | (uint64_t)(a.b_stride * 2) | (uint64_t)(a.b_group_stride * 2)) % 16)
+            return fail(nullptr, MOE_EINVAL, "grouped_gemm: the rows of a and b must be 16-byte aligned");
+        if (addr(a.out) % dtype_bytes(a.out_dtype) || (addr(a.bounds) | addr(a.rows)) % 4)
+            return fail(nullptr, MOE_EINVAL, "grouped_gemm: out, bounds and rows must be aligned to their elements");
+        const int rc = noalloc_device_ok(a.device);
+        if (rc != MOE_OK) return rc;
+        DevGuard guard(a.device);
+        Gemm16 g{};
+        g.a = static_cast<const uint8_t*>(a.a);
+        g.a_stride = a.a_stride * 2;
+        g.a_rows = a.a_rows;
+        g.rows = a.rows;
+        g.row_div = a.top_k;
+        g.b = static_cast<const uint8_t*>(a.b);
+        g.b_stride = a.b_stride * 2;
+        g.b_group = a.b_group_stride * 2;
+        g.bounds = a.bounds;
+        g.G = a.n_groups;
+        g.M = a.M;
+        g.N = a.N;
+        g.K = a.K;
+        g.swiglu = a.swiglu;
+        g.in_type = a.dtype;
+        g.out = a.out;
+        g.out_stride = a.out_stride;
+        g.out_type = a.out_dtype;
+        const hipError_t e = launch_gemm16(g, static_cast<hipStream_t>(stream));
+        if (e != hipSuccess) return hip_fail(nullptr, e, "grouped_gemm: launch");
+        g_err.clear();
+        return (int)MOE_OK;
+    });
+}
+
+int moe_combine_rows(const moe_combine_args_t* in, void* stream)
+{
+    return guarded(nullptr, [&] {
+        moe_combine_args_t a;
+        std::string why;
+        if (!read_struct(in, &a, &why)) return fail(nullptr, MOE_EINVAL, why);
+        if (!dtype_ok(a.d_dtype) || !dtype_ok(a.y_dtype) || (a.base && !dtype_ok(a.base_dtype)))
+            return fail(nullptr, MOE_EINVAL, "combine: dtypes must be MOE_F32, MOE_BF16 or MOE_F16");
+        if (a.N < 1 || a.N > (1 << 20)) return fail(nullptr, MOE_EINVAL, "combine: N must be in [1, 2^20]");
+        if (a.top_k < 1 || a.top_k > 1024) return fail(nullptr, MOE_EINVAL, "combine: top_k must be in [1, 1024]");
+        if (a.n_tokens < 0 || a.n_tokens > kCombineMostTokens) return fail(nullptr, MOE_EINVAL, "combine: n_tokens must be in [0, 2^23]");
+        if (a.d_rows < 0 || a.d_rows > INT32_MAX) return fail(nullptr, MOE_EINVAL, "combine: d_rows must be in [0, 2^31 - 1]");
+        if (a.n_tokens == 0) {
+            g_err.clear();
+            return (int)MOE_OK;
+        }
+        if ((!a.d && a.d_rows) || !a.weights || !a.pos || !a.y)
+            return fail(nullptr, MOE_EINVAL, "combine: d, weights, pos and y are required");
+        if (!stride_ok(a.d_stride, a.N) || !stride_ok(a.y_stride, a.N) || (a.base && !stride_ok(a.base_stride, a.N)))
+            return fail(nullptr, MOE_EINVAL, "combine: a row stride below N, or above 2^40");
+        if (addr(a.d) % dtype_bytes(a.d_dtype) || addr(a.y) % dtype_bytes(a.y_dtype) ||
+            (a.base && addr(a.base) % dtype_bytes(a.base_dtype)) || (addr(a.weights) | addr(a.pos)) % 4)
+            return fail(nullptr, MOE_EINVAL, "combine: d, base, y, weights and pos must be aligned to their elements");
+        const int rc = noalloc_device_ok(a.device);
+        if (rc != MOE_OK) return rc;
+        DevGuard guard(a.device);
+        CombineRows c{};
+        c.d = a.d;
+        c.d_stride = a.d_stride;
+        c.d_rows = a.d_rows;
+        c.d_type = a.d_dtype;
+        c.weights = a.weights;
+        c.pos = a.pos;
+        c.base = a.base;
+        c.base_stride = a.base_stride;
+        c.base_type = a.base_dtype;
+        c.y = a.y;
+        c.y_stride = a.y_stride;
+        c.y_type = a.y_dtype;
+        c.T = a.n_tokens;
+        c.n = a.N;
+        c.k = a.top_k;
+        const hipError_t e = launch_combine_rows(c, static_cast<hipStream_t>(stream));
+        if (e != hipSuccess) return hip_fail(nullptr, e, "combine: launch");
+        g_err.clear();
+        return (int)MOE_OK;
+    });
+}
+
+// ------------------------------------------------------ low-rank adapters ---
+
+static bool lora_dims_ok(int64_t M, int K, int r, std::string* why)
+{
+    if (M < 0 || M > kLoraMostRows)
+        *why = "lora: M must be in [0, 2^23]";
+    else if (K < 8 || K % 8 || K > (1 << 20))
+        *why = "lora: K must be a multiple of 8 in [8, 2^20]";
+    else if (r < 8 || r % 8 || r > kLoraMostRank)
+        *why = "lora: rank must be a multiple of 8 in [8, 256]";
+    else
+        return true;
+    return false;
+}
+
+int moe_lora_workspace_size(int64_t M, int32_t K, int32_t rank, uint64_t* bytes)
+{
+    return guarded(nullptr, [&] {
+        std::string why;
+        if (!bytes) return fail(nullptr, MOE_EINVAL, "null bytes pointer");
+        if (!lora_dims_ok(M, K, rank, &why)) return fail(nullptr, MOE_EINVAL, why);
+        *bytes = M ? lora_ws(M, K, rank) : 0;
+        g_err.clear();
+        return (int)MOE_OK;
+    });
+}
+
+int moe_lora_add(const moe_lora_args_t* in, void* stream)
+{
+    return guarded(nullptr, [&] {
+        moe_lora_args_t a;
+        std::string why;
+        if (!read_struct(in, &a, &why)) return fail(nullptr, MOE_EINVAL, why);
+        if (a.dtype != MOE_BF16 && a.dtype != MOE_F16) return fail(nullptr, MOE_EINVAL, "lora: dtype must be MOE_BF16 or MOE_F16");
+        if (!dtype_ok(a.out_dtype) || (a.base && !dtype_ok(a.base_dtype)))
+            return fail(nullptr, MOE_EINVAL, "lora: out_dtype and base_dtype must be MOE_F32, MOE_BF16 or MOE_F16");
+        if (!lora_dims_ok(a.M, a.K, a.rank, &why)) return fail(nullptr, MOE_EINVAL, why);
+        if (a.N < 1 || a.N > (1 << 20)) return fail(nullptr, MOE_EINVAL, "lora: N must be in [1, 2^20]");
+        if (a.n_adapters < 1 || a.n_adapters > kLoraMostAdapters)
+            return fail(nullptr, MOE_EINVAL, "lora: n_adapters must be in [1, 2^20]");
+        if (a.M == 0) {
+            g_err.clear();
+            return (int)MOE_OK;
+        }
+        if (!a.x || !a.a || !a.b || !a.adapters || !a.out || !a.workspace)
+            return fail(nullptr, MOE_EINVAL, "lora: x, a, b, adapters, out and workspace are required");
+        if (!stride_ok(a.x_stride, a.K) || !stride_ok(a.out_stride, a.N) || (a.base && !stride_ok(a.base_stride, a.N)))
+            return fail(nullptr, MOE_EINVAL, "lora: a row stride below the row's length, or above 2^40");
+        if ((addr(a.x) | addr(a.a) | addr(a.b) | (uint64_t)(a.x_stride * 2)) % 16)
+            return fail(nullptr, MOE_EINVAL, "lora: the rows of x, and a and b, must be 16-byte aligned");
+        if (addr(a.out) % dtype_bytes(a.out_dtype) || (a.base && addr(a.base) % dtype_bytes(a.base_dtype)) ||
+            (addr(a.adapters) | addr(a.scales)) % 4)
+            return fail(nullptr, MOE_EINVAL, "lora: out, base, adapters and scales must be aligned to their elements");
+        if (addr(a.workspace) % 256) return fail(nullptr, MOE_EINVAL, "lora: workspace must be 256-byte aligned");
+        if (a.workspace_bytes < lora_ws(a.M, a.K, a.rank))
+            return fail(nullptr, MOE_EINVAL, "lora: workspace smaller than moe_lora_workspace_size()");
+        const int rc = noalloc_device_ok(a.device);
+        if (rc != MOE_OK) return rc;
+        DevGuard guard(a.device);
+        LoraAdd l{};
+        l.x = static_cast<const uint8_t*>(a.x);
+        l.x_stride = a.x_stride * 2;
+        l.a = static_cast<const uint8_t*>(a.a);
+        l.b = static_cast<const uint8_t*>(a.b);
+        l.in_type = a.dtype;
+        l.adapters = a.adapters;
+        l.n = a.n_adapters;
+        l.scales = a.scales;
+        l.base = a.base;
+        l.base_stride = a.base_stride;
+        l.base_type = a.base_dtype;
+        l.out = a.out;
+        l.out_stride = a.out_stride;
+        l.out_type = a.out_dtype;
+        l.M = a.M;
+        l.N = a.N;
+        l.K = a.K;
+        l.r = a.rank;
+        l.ws = static_cast<float*>(a.workspace);
+        const hipError_t e = launch_lora_add(l, static_cast<hipStream_t>(stream));
+        if (e != hipSuccess) return hip_fail(nullptr, e, "lora: launch");
         g_err.clear();
         return (int)MOE_OK;
     });
