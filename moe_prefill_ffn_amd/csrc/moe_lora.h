@@ -11,20 +11,21 @@ namespace moe {
 constexpr int kLoraMostRank = 256, kLoraMostAdapters = 1 << 20;
 constexpr int64_t kLoraMostRows = 1 << 23;                // tiles of 16 rows, 256 threads each, in one launch
 
-// Parts of K whose sums are kept apart (each workgroup sums one): enough workgroups to fill the
-// chip from the few tiles of 16 rows that a small batch has, each with at least kLoraUnit of K.
-constexpr int kLoraTile = 16, kLoraUnit = 256;
+// Rows of a tile, and parts of K whose sums are kept apart (each workgroup sums one): enough
+// workgroups to fill the chip from the few tiles that a small batch has, each with at least kLoraUnit of K.
+constexpr int kLoraUnit = 256, kLoraMostParts = 16, kLoraFill = 512;
+static inline int lora_tile(int64_t M) { return M > 1024 ? 32 : 16; }
 static inline int lora_parts(int64_t M, int K)
 {
-    const int64_t tiles = (M + kLoraTile - 1) / kLoraTile, want = (512 + tiles - 1) / tiles, most = (K + kLoraUnit - 1) / kLoraUnit;
-    const int64_t p = want < most ? want : most;
-    return (int)(p < 16 ? p : 16);
+    const int64_t tiles = (M + lora_tile(M) - 1) / lora_tile(M), want = (kLoraFill + tiles - 1) / tiles;
+    const int64_t most = (K + kLoraUnit - 1) / kLoraUnit, p = want < most ? want : most;
+    return (int)(p < kLoraMostParts ? p : kLoraMostParts);
 }
-// sums of the parts, [parts][M][r] fp32: enough for M rows or fewer (tiles * ceil(512 / tiles) < tiles + 512)
+// sums of the parts, [parts][M][r] fp32: enough for M rows or fewer (tiles * ceil(kLoraFill / tiles) < tiles + kLoraFill)
 static inline uint64_t lora_ws(int64_t M, int K, int r)
 {
-    const int64_t rows = (M + kLoraTile - 1) / kLoraTile * kLoraTile, most = (K + kLoraUnit - 1) / kLoraUnit;
-    const int64_t all = rows * (most < 16 ? most : 16), few = rows + 512 * kLoraTile;
+    const int64_t rows = (M + 31) / 32 * 32, most = (K + kLoraUnit - 1) / kLoraUnit;
+    const int64_t all = rows * (most < kLoraMostParts ? most : kLoraMostParts), few = rows + kLoraFill * 32;
     return ((uint64_t)(all < few ? all : few) * r * 4 + 255) / 256 * 256;
 }
 
