@@ -13,7 +13,7 @@ LIB = os.path.join(HERE, "libmoe_prefill.so")
 MICRO_LIB = os.path.join(HERE, "libmoe_micro.so")   # measurement kernels (roofline denominators)
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-SOURCES = ["moe_mx.hip", "moe_gemm16.hip", "moe_kernels.hip", "moe_decode.hip", "moe_lora.hip", "moe_rows.hip",
+SOURCES = ["moe_mx.hip", "moe_gemm16_bf16.hip", "moe_gemm16_f16.hip", "moe_kernels.hip", "moe_decode.hip", "moe_lora.hip", "moe_rows.hip",
            "moe_runtime.cpp", "moe_pack.cpp", "moe_pool_plan.cpp"]
 
 # -ffp-contract=off: no fused multiply-adds beyond the ones written out.

@@ -1,10 +1,10 @@
-// Launch interface of the 16-bit products (host side of moe_gemm16.hip).
+// Launch interface of the 16-bit products (host side of moe_gemm16_kernels.h).
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "moe_layout.h"
+#include "moe_dtype.h"
 
 namespace moe {
 
@@ -24,12 +24,18 @@ struct Gemm16 {
     int64_t M;
     int N, K;
     int swiglu;
-    int in_type;              // of A and B
+    int in_type;              // of A and B: kBF16 or kF16
     void* out;                // [M, N]
     int64_t out_stride;
     int out_type;             // kF32 or in_type
 };
 
-hipError_t launch_gemm16(const Gemm16& g, hipStream_t st);
+hipError_t launch_gemm16_bf16(const Gemm16& g, hipStream_t st);
+hipError_t launch_gemm16_f16(const Gemm16& g, hipStream_t st);
+inline hipError_t launch_gemm16(const Gemm16& g, hipStream_t st)
+{
+    if (g.M == 0) return hipSuccess;
+    return g.in_type == kBF16 ? launch_gemm16_bf16(g, st) : launch_gemm16_f16(g, st);
+}
 
 }  // namespace moe

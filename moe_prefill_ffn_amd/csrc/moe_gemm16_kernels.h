@@ -1,7 +1,10 @@
 // HIP kernels (CDNA4 / gfx950) of products of 16-bit matrices (bf16 or fp16), dense or over the
 // groups of a row table:
 //   out[r, n] = sum_k A[src(r), k] B[g(r), n, k]
-// in fp32, with SwiGLU of gate and up rows of B where asked for, rounded once.
+// in fp32, with SwiGLU of gate and up rows of B where asked for, rounded once.  Included by one source a
+// type, so that they compile at once.
+#pragma once
+
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -33,6 +36,62 @@ __device__ __forceinline__ v16f mfma16(v4i w, v4i x, v16f c)
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, w), __builtin_bit_cast(v8h, x), c, 0, 0, 0);
 }
 
+// Rows [m0, m1) of group g; m0 >= m1: nothing to do.
+struct Rows {
+    int g;
+    int64_t m0, m1;
+};
+
+// The rows of tile number x of the groups' tiles of BM rows that hold any, the same on all lanes, by each
+// wave for itself.
+template <int BM>
+__device__ __forceinline__ Rows rows_of_tile(const Gemm16& a, int64_t x)
+{
+    if (!a.bounds) return {0, x * BM, x * BM + BM < a.M ? x * BM + BM : a.M};
+    constexpr int kPer = 8;                               // groups a lane
+    const int lane = threadIdx.x & 63;
+    for (int base = 0; base < a.G; base += 64 * kPer) {
+        int b[kPer + 1];
+        uint32_t n = 0;
+#pragma unroll
+        for (int i = 0; i <= kPer; ++i) {
+            const int g = base + lane * kPer + i;
+            b[i] = bound_of(a, g < a.G ? g : a.G);
+        }
+        auto tiles = [&](int i) { return b[i + 1] > b[i] ? (uint32_t)(b[i + 1] - b[i] + BM - 1) / BM : 0u; };
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) n += tiles(i);     // 2^23 a group at most, which leaves the next one none where bounds do not ascend
+        uint32_t upto = n;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const uint32_t y = (uint32_t)__shfl_up((int)upto, o);
+            if (lane >= o) upto += y;
+        }
+        const uint32_t all = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
+        if (x >= all) {
+            x -= all;
+            continue;
+        }
+        const int at = __builtin_ctzll(__ballot((int64_t)upto > x));   // the lane that has it
+        int64_t left = x - (upto - n);
+        int g = 0, m0 = 0, m1 = 0;
+        bool found = false;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const uint32_t t = tiles(i);
+            if (!found && left < (int64_t)t) {
+                g = base + lane * kPer + i;
+                m0 = b[i] + (int)left * BM;
+                m1 = m0 + BM < b[i + 1] ? m0 + BM : b[i + 1];
+                found = true;
+            }
+            if (!found) left -= t;
+        }
+        return {__builtin_amdgcn_readlane(g, at), __builtin_amdgcn_readlane(m0, at), __builtin_amdgcn_readlane(m1, at)};
+    }
+    return {0, 0, 0};
+}
+
 // A row of the product reads this row of A.
 __device__ __forceinline__ int64_t a_row(const Gemm16& a, int64_t r)
 {
@@ -43,16 +102,16 @@ __device__ __forceinline__ int64_t a_row(const Gemm16& a, int64_t r)
 
 // ------------------------------------------------------------- tiled kernel ---
 // WM x WN waves, each TM x TN tiles of 32 x 32: BM rows of A by BN rows of B, K in stages of
-// 64 values (128 bytes a row, a cache line) through two LDS slots.
-template <int WM_, int WN_, int TM_, int TN_>
+// 64 values (128 bytes a row, a cache line) through NS LDS slots.
+template <int WM_, int WN_, int TM_, int TN_, int NS_>
 struct Shape {
-    static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_;
+    static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_, NS = NS_;
     static constexpr int NW = WM * WN, BM = 32 * WM * TM, BN = 32 * WN * TN, kRows = BM + BN;
     // 1 KiB data loads per wave and stage: of A's rows, of B's
     static constexpr int NLA = BM / 8 / NW, NLB = BN / 8 / NW, NL = NLA + NLB;
     static_assert(NLA * NW * 8 == BM && NLB * NW * 8 == BN, "whole loads");
     static constexpr int kDataBytes = kRows * 128;
-    static constexpr int kRowsOff = 2 * kDataBytes;       // row indices of two tiles
+    static constexpr int kRowsOff = NS * kDataBytes;      // row indices of two tiles
     static constexpr int kListOff = kRowsOff + 2 * BM * 4;
     static constexpr int kLds = kListOff + kListMost * (int)sizeof(ListedTile);
 };
@@ -72,9 +131,10 @@ __global__ __launch_bounds__(64 * S::NW) void k_gemm16_tile(Gemm16 a, int n_tile
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / S::WN, wn = wave % S::WN;
     const int chunks = a.K / 8;                           // of 16 bytes
-    // at least two stages (a stage past the end of K adds 0): a stage issues the one two further,
-    // which is then in this tile or the next
-    const int nst = chunks > 8 ? (chunks + 7) >> 3 : 2;
+    // at least NS stages (a stage past the end of K adds 0): a stage issues the one NS further, which is
+    // then in this tile or the next
+    constexpr int NS = S::NS;
+    const int nst = chunks > 8 * (NS - 1) ? (chunks + 7) >> 3 : NS;
     constexpr int kOutCols = kSwiglu ? S::BN / 2 : S::BN;
     int32_t* s_rows = reinterpret_cast<int32_t*>(lds + S::kRowsOff);
     ListedTile* s_list = reinterpret_cast<ListedTile*>(lds + S::kListOff);
@@ -117,11 +177,11 @@ __global__ __launch_bounds__(64 * S::NW) void k_gemm16_tile(Gemm16 a, int n_tile
             dofs[l] += ((lane & 7) ^ swz(q)) * 16;
         }
     };
-    // Stages are counted through a list's tiles; a stage sits in slot gs % 2.
-    auto issue_data = [&](int l, int gs, int s) {
+    // Stages go through the slots in turn, through a list's tiles.
+    auto issue_data = [&](int l, int slot, int s) {
         const bool is_a = l < S::NLA;
         const int ql = is_a ? wave * S::NLA + l : wave * S::NLB + l - S::NLA;       // load of the operand: 8 rows
-        const uint32_t to = lds0 + (gs & 1) * S::kDataBytes + ((is_a ? 0 : S::BM / 8) + ql) * 1024;
+        const uint32_t to = lds0 + slot * S::kDataBytes + ((is_a ? 0 : S::BM / 8) + ql) * 1024;
         const uint8_t* base = (is_a ? a_at : b_at + (kSwiglu && (ql & 4) ? up : 0)) + s * 128;
         if constexpr (!kTail) {
             g2lds16_at(base, dofs[l], to);
@@ -142,8 +202,8 @@ __global__ __launch_bounds__(64 * S::NW) void k_gemm16_tile(Gemm16 a, int n_tile
     struct Ops {
         v4i v[kOps];
     };
-    auto read_op = [&](int i, int gs, int step, Ops& o) {
-        o.v[i] = *reinterpret_cast<const v4i*>(lds + (gs & 1) * S::kDataBytes + op_row(i) * 128 + (((4 * h + step) ^ swz(j)) << 4));
+    auto read_op = [&](int i, int slot, int step, Ops& o) {
+        o.v[i] = *reinterpret_cast<const v4i*>(lds + slot * S::kDataBytes + op_row(i) * 128 + (((4 * h + step) ^ swz(j)) << 4));
     };
 
     v16f acc[S::TM][S::TN];
@@ -264,7 +324,7 @@ __global__ __launch_bounds__(64 * S::NW) void k_gemm16_tile(Gemm16 a, int n_tile
         asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
         point_data(cur, 0);
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < NS; ++u)
 #pragma unroll
             for (int l = 0; l < S::NL; ++l) issue_data(l, u, u);
         asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
@@ -272,52 +332,55 @@ __global__ __launch_bounds__(64 * S::NW) void k_gemm16_tile(Gemm16 a, int n_tile
 #pragma unroll
         for (int i = 0; i < kOps; ++i) read_op(i, 0, 0, o0);
         clear();
-        int gs = 0;
-        bool stored = false;                              // the last tile's kStores stores are out, nothing else behind the loads
+        int slot = 0;
+        bool stored = false;                              // the last tile's kStores stores are out, behind the loads
         for (int ti = 0; ti < count; ++ti) {
             ListedTile next = cur;
-            for (int s = 0; s < nst; ++s, ++gs) {
-                // Stage gs, four steps of kProd products.  Steps 0 and 1 read the operands of steps 1
-                // to 3; then every wave has read its share of slot gs % 2, and the barrier frees it for
-                // stage gs + 2 and admits stage gs + 1 (its loads, the only ones out but for stores,
-                // have had a stage's time).  Step 2 issues the loads of stage gs + 2, step 3 reads step
-                // 0 of stage gs + 1.  Each memory instruction is placed behind a product of its own, in
-                // whose 32 cycles it issues.
+            for (int s = 0; s < nst; ++s) {
+                // A stage, four steps of kProd products.  Steps 0 and 1 read the operands of steps 1 to 3;
+                // then every wave has read its share of the slot, and the barrier frees it for the stage NS
+                // further and admits the next stage, whose loads have had NS - 1 stages' time (the loads of the
+                // NS - 2 stages behind it, and stores, may still be out).  Step 2 issues the loads of the stage
+                // NS further, step 3 reads step 0 of the next.  Each memory instruction is placed behind a
+                // product of its own, in whose 32 cycles it issues.
+                const int after = slot + 1 < NS ? slot + 1 : 0;
                 products(o0, [&](int at) {
 #pragma unroll
                     for (int i = at * 2 * kOps / kProd; i < (at + 1) * 2 * kOps / kProd; ++i) {
                         if (i < kOps)
-                            read_op(i, gs, 1, o1);
+                            read_op(i, slot, 1, o1);
                         else
-                            read_op(i - kOps, gs, 2, o2);
+                            read_op(i - kOps, slot, 2, o2);
                     }
                 });
                 products(o1, [&](int at) {
 #pragma unroll
-                    for (int i = at * kOps / kProd; i < (at + 1) * kOps / kProd; ++i) read_op(i, gs, 3, o3);
+                    for (int i = at * kOps / kProd; i < (at + 1) * kOps / kProd; ++i) read_op(i, slot, 3, o3);
                 });
+                constexpr int kBehind = (NS - 2) * S::NL, kMost = kBehind + kStores < 63 ? kBehind + kStores : 63;
                 if (stored) {
-                    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kStores < 63 ? kStores : 63) : "memory");
+                    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kMost) : "memory");
                     stored = false;
                 } else {
-                    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kBehind) : "memory");
                 }
                 // past the list's last tile: its first stages again, not used
-                const int s2 = s + 2 < nst ? s + 2 : s + 2 - nst;
-                if (s + 2 == nst && ti + 1 < count) {     // this tile's loads are all issued: on to the next
+                const int s2 = s + NS < nst ? s + NS : s + NS - nst;
+                if (s + NS == nst && ti + 1 < count) {    // this tile's loads are all issued: on to the next
                     next = listed(ti + 1);
                     point_data(next, (ti + 1) & 1);
                     if (ti + 2 < count) issue_rows(listed(ti + 2), ti & 1);   // its buffer: this tile's, pointed long ago
                 }
                 products(o2, [&](int at) {
 #pragma unroll
-                    for (int l = at * S::NL / kProd; l < (at + 1) * S::NL / kProd; ++l) issue_data(l, gs + 2, s2);
+                    for (int l = at * S::NL / kProd; l < (at + 1) * S::NL / kProd; ++l) issue_data(l, slot, s2);
                 });
                 products(o3, [&](int at) {
                     // past the list's last stage: an old one, not used
 #pragma unroll
-                    for (int i = at * kOps / kProd; i < (at + 1) * kOps / kProd; ++i) read_op(i, gs + 1, 0, o0);
+                    for (int i = at * kOps / kProd; i < (at + 1) * kOps / kProd; ++i) read_op(i, after, 0, o0);
                 });
+                slot = after;
             }
             const bool whole = vec && cur.m0 + S::BM <= cur.m1 && (cur.nt + 1) * kOutCols <= a.N;   // uniform
             if (whole)
@@ -333,63 +396,101 @@ __global__ __launch_bounds__(64 * S::NW) void k_gemm16_tile(Gemm16 a, int n_tile
 }
 
 // ----------------------------------------------------------- few-row kernel ---
-// Up to 32 rows of a group by 32 columns (SwiGLU: 32 gate and 32 up rows of B) per workgroup; its
-// waves take every eighth 64 values of K, fed straight from memory, and add up through LDS in wave
-// order.  A chunk past the end of K is 0 in both operands.
-constexpr int kFewWaves = 8, kFewRows = 32;
+// Up to 16 kR rows of a group by 16 kN / NG columns (SwiGLU, NG = 2: 16 gate and 16 up rows of B) per
+// workgroup; its waves take every eighth 64 values of K, fed straight from memory, four such units' loads
+// out at a time, and add up through LDS in wave order.  What bounds it is B's bytes, read once.
+constexpr int kFewWaves = 8;
 
-template <int kIn, int kT, bool kSwiglu>
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+// The operands as in mfma16, 16 rows of each: lane group g = lane / 16 takes 8 values of K and gets four
+// consecutive columns of row lane % 16.
+template <int kIn>
+__device__ __forceinline__ v4f mfma16x16(v4i w, v4i x, v4f c)
+{
+    if constexpr (kIn == kBF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, w), __builtin_bit_cast(v8bf, x), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, w), __builtin_bit_cast(v8h, x), c, 0, 0, 0);
+}
+
+// kR row tiles; kN tiles of 16 rows of B (SwiGLU: half of them gate, half up)
+template <int kIn, int kT, bool kSwiglu, int kR, int kN>
 __global__ __launch_bounds__(64 * kFewWaves) void k_gemm16_few(Gemm16 a)
 {
-    constexpr int NT = kSwiglu ? 2 : 1;
-    __shared__ float red[kFewWaves][NT][32][33];
-    const Rows t = rows_of_slot<kFewRows>(a, blockIdx.x);
+    constexpr int BM = 16 * kR, kCols = kSwiglu ? 8 * kN : 16 * kN;
+    __shared__ float red[kFewWaves][BM][16 * kN + 4];
+    const Rows t = rows_of_tile<BM>(a, blockIdx.x);
     if (t.m0 >= t.m1) return;                             // uniform
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, j = lane & 31;
-    const int chunks = a.K / 8;
-    const int n0 = (int)blockIdx.y * 32;
-    const uint8_t* x = a.a + a_row(a, t.m0 + j < t.m1 ? t.m0 + j : t.m1 - 1) * a.a_stride;
-    const uint8_t* w[NT];
+    const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int chunks = a.K / 8, n0 = (int)blockIdx.y * kCols;
+    const uint8_t* x[kR];
+    const uint8_t* w[kN];
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
-        w[i] = a.b + t.g * a.b_group + (int64_t)((n0 + j < a.N ? n0 + j : a.N - 1) + i * a.N) * a.b_stride;
-    v16f acc[NT];
+    for (int q = 0; q < kR; ++q) x[q] = a.a + a_row(a, t.m0 + 16 * q + i < t.m1 ? t.m0 + 16 * q + i : t.m1 - 1) * a.a_stride + 32 * g;
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int q = 0; q < kN; ++q) {
+        const int at = n0 + 16 * (kSwiglu ? q / 2 : q) + i, n = at < a.N ? at : a.N - 1;
+        w[q] = a.b + t.g * a.b_group + (int64_t)(kSwiglu && (q & 1) ? n + a.N : n) * a.b_stride + 32 * g;
+    }
+    v4f acc[kR][kN];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][e] = 0.0f;
-    for (int u = wave * 8; u < chunks; u += 8 * kFewWaves) {
-        v4i vx[4], vw[NT][4];
+    for (int q = 0; q < kR; ++q)
+#pragma unroll
+        for (int n = 0; n < kN; ++n) acc[q][n] = v4f{0, 0, 0, 0};
+    // two units; lane group g has chunks u + 2 g, + 1 of one that starts at chunk u; past the end of K 0
+    constexpr int kStep = 8 * kFewWaves;
+    struct Frag {
+        v4i x[4][kR], w[4][kN];
+    };
+    auto load = [&](Frag& f, int u0) {
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-            const int c = u + 4 * h + s;
-            const bool in = c < chunks;
+            const int u = u0 + (s >> 1) * kStep;
+            const bool in = u + 8 <= chunks || u + 2 * g + (s & 1) < chunks;
+            const int64_t at = (int64_t)(u + (s & 1)) * 16;
 #pragma unroll
-            for (int i = 0; i < NT; ++i) vw[i][s] = in ? *reinterpret_cast<const v4i*>(w[i] + c * 16) : v4i{0, 0, 0, 0};
-            vx[s] = in ? *reinterpret_cast<const v4i*>(x + c * 16) : v4i{0, 0, 0, 0};
+            for (int n = 0; n < kN; ++n) f.w[s][n] = in ? *reinterpret_cast<const v4i*>(w[n] + at) : v4i{0, 0, 0, 0};
+#pragma unroll
+            for (int q = 0; q < kR; ++q) f.x[s][q] = in ? *reinterpret_cast<const v4i*>(x[q] + at) : v4i{0, 0, 0, 0};
         }
+    };
+    auto multiply = [&](const Frag& f) {
 #pragma unroll
         for (int s = 0; s < 4; ++s)
 #pragma unroll
-            for (int i = 0; i < NT; ++i) acc[i] = mfma16<kIn>(vw[i][s], vx[s], acc[i]);
+            for (int n = 0; n < kN; ++n)
+#pragma unroll
+                for (int q = 0; q < kR; ++q) acc[q][n] = mfma16x16<kIn>(f.w[s][n], f.x[s][q], acc[q][n]);
+    };
+    Frag f0, f1;
+    const int u0 = wave * 8;
+    if (u0 < chunks) load(f0, u0);
+    if (u0 + 2 * kStep < chunks) load(f1, u0 + 2 * kStep);
+    for (int u = u0; u < chunks; u += 4 * kStep) {
+        multiply(f0);
+        if (u + 4 * kStep < chunks) load(f0, u + 4 * kStep);
+        if (u + 2 * kStep >= chunks) break;
+        multiply(f1);
+        if (u + 6 * kStep < chunks) load(f1, u + 6 * kStep);
     }
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int q = 0; q < kR; ++q)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) red[wave][i][j][8 * (e >> 2) + 4 * h + (e & 3)] = acc[i][e];
+        for (int n = 0; n < kN; ++n) *reinterpret_cast<v4f*>(&red[wave][16 * q + i][16 * n + 4 * g]) = acc[q][n];
     __syncthreads();
     typedef typename Elem<kT>::type T;
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-        const int row = p * 16 + (tid >> 5), col = tid & 31;
+    for (int e = tid; e < BM * kCols; e += 64 * kFewWaves) {
+        const int row = e / kCols, col = e % kCols, at = kSwiglu ? col / 16 * 32 + col % 16 : col;
         if (t.m0 + row >= t.m1 || n0 + col >= a.N) continue;
-        float z[NT] = {};
+        float z = 0.0f, z2 = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int v = 0; v < kFewWaves; ++v) z[i] += red[v][i][row][col];
-        static_cast<T*>(a.out)[(t.m0 + row) * a.out_stride + n0 + col] =
-            from_f32<kT>(kSwiglu ? silu_mul(z[0], z[NT - 1]) : z[0]);
+        for (int v = 0; v < kFewWaves; ++v) {
+            z += red[v][row][at];
+            if (kSwiglu) z2 += red[v][row][at + 16];
+        }
+        static_cast<T*>(a.out)[(t.m0 + row) * a.out_stride + n0 + col] = from_f32<kT>(kSwiglu ? silu_mul(z, z2) : z);
     }
 }
 
@@ -399,14 +500,28 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_gemm16_few(Gemm16 a)
 namespace {
 
 // The most tiles of BM rows that the groups can have.
-int64_t slots_of(const Gemm16& g, int BM) { return g.bounds ? g.M / BM + g.G : (g.M + BM - 1) / BM; }
+int64_t slots_of(const Gemm16& g, int BM)
+{
+    const int64_t n = g.bounds ? g.M / BM + g.G : (g.M + BM - 1) / BM;
+    return n < g.M ? n : g.M;
+}
 
-using Tile256 = Shape<2, 2, 4, 4>;        // 256 x 256
-using Tile128 = Shape<2, 2, 2, 2>;        // 128 x 128
-using Tile64 = Shape<2, 2, 1, 2>;         // 64 x 128
+// Few tiles leave a workgroup a CU to itself: deep rings, whose loads have up to seven stages' time.
+// (64 x 128 through two slots took 37 us for 64 x 4096 x 4096, a load's latency a stage; 64 x 64 through
+// eight 18.)
+using Deep64 = Shape<2, 2, 1, 1, 8>;      // 64 x 64
+using DeepWide = Shape<2, 2, 1, 2, 6>;    // 64 x 128
+using Deep128 = Shape<2, 2, 2, 2, 4>;     // 128 x 128
+using Tile128 = Shape<2, 2, 2, 2, 2>;     // 128 x 128, two workgroups a CU
+using TileWide = Shape<2, 2, 2, 4, 3>;    // 128 x 256
+using Tile256 = Shape<2, 2, 4, 4, 2>;     // 256 x 256
+
+// as many workgroups as the chip holds at once: 256 CUs, 160 KiB of LDS each
+template <class S>
+constexpr int kGrid = 256 * (163840 / S::kLds);
 
 template <class S, int kIn, int kT, bool kSwiglu, bool kTail>
-hipError_t launch_tile(const Gemm16& g, hipStream_t st)
+hipError_t launch_kernel(const Gemm16& g, hipStream_t st)
 {
     const int n_tiles = (int)nblk(g.N, kSwiglu ? S::BN / 2 : S::BN);
     const int64_t slots = slots_of(g, S::BM), total = slots * n_tiles;   // at most 2^30 (kGemm16MostTiles)
@@ -414,51 +529,87 @@ hipError_t launch_tile(const Gemm16& g, hipStream_t st)
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_gemm16_tile<S, kIn, kT, kSwiglu, kTail>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds);
     if (e != hipSuccess) return e;
-    // as many workgroups as the chip holds at once: 256 CUs, 160 KiB of LDS each
-    constexpr int kGrid = 256 * (163840 / S::kLds);
     const unsigned grid = 8 * nblk(total, 8);
-    hipLaunchKernelGGL((k_gemm16_tile<S, kIn, kT, kSwiglu, kTail>), dim3(grid < (unsigned)kGrid ? grid : (unsigned)kGrid), dim3(64 * S::NW),
-                       S::kLds, st, g, n_tiles, slots);
+    hipLaunchKernelGGL((k_gemm16_tile<S, kIn, kT, kSwiglu, kTail>), dim3(grid < (unsigned)kGrid<S> ? grid : (unsigned)kGrid<S>),
+                       dim3(64 * S::NW), S::kLds, st, g, n_tiles, slots);
     return hipGetLastError();
 }
 
-template <int kIn, int kT, bool kSwiglu, bool kTail>
-hipError_t launch_shape(const Gemm16& g, hipStream_t st)
+template <class S, int kIn, int kT, bool kSwiglu>
+hipError_t launch_tile(const Gemm16& g, hipStream_t st)
 {
-    const int64_t rows = g.M / g.G;       // rows a group has on average
-    // tiles of a shape: what a grouped product has at most
-    auto tiles = [&](int BM, int BN) { return slots_of(g, BM) * (int64_t)nblk(g.N, kSwiglu ? BN / 2 : BN); };
-    // the tiled kernel reaches a tile's rows, or all of A through the row table, by 32 bits of offset
-    const int64_t a_span = (g.rows || g.row_div > 1 ? g.a_rows : 256) * g.a_stride, b_span = 256 * g.b_stride;
-    const bool far = a_span > (int64_t)UINT32_MAX || b_span > (int64_t)UINT32_MAX;
-    if (far || (rows <= 64 && tiles(64, 128) < 64)) {
-        hipLaunchKernelGGL((k_gemm16_few<kIn, kT, kSwiglu>), dim3((unsigned)slots_of(g, kFewRows), nblk(g.N, 32)), dim3(64 * kFewWaves), 0, st, g);
-        return hipGetLastError();
-    }
-    if (rows >= 256 && tiles(256, 256) >= 384) return launch_tile<Tile256, kIn, kT, kSwiglu, kTail>(g, st);
-    if (rows >= 60 && tiles(128, 128) >= 512) return launch_tile<Tile128, kIn, kT, kSwiglu, kTail>(g, st);
-    return launch_tile<Tile64, kIn, kT, kSwiglu, kTail>(g, st);
+    return g.K % 64 || g.K < 64 * S::NS ? launch_kernel<S, kIn, kT, kSwiglu, true>(g, st) : launch_kernel<S, kIn, kT, kSwiglu, false>(g, st);
+}
+
+template <int kIn, int kT, bool kSwiglu, int kR, int kN>
+hipError_t launch_few(const Gemm16& g, hipStream_t st)
+{
+    hipLaunchKernelGGL((k_gemm16_few<kIn, kT, kSwiglu, kR, kN>), dim3((unsigned)slots_of(g, 16 * kR), nblk(g.N, (kSwiglu ? 8 : 16) * kN)),
+                       dim3(64 * kFewWaves), 0, st, g);
+    return hipGetLastError();
+}
+
+// What a shape's tiles would take, in us at K = 4096 but for the operands' way from memory, which is the same
+// for all: the rounds of tiles that the chip goes through, each as long as measured on dense products
+// (bf16, K = 4096; 128 x 128 in twos: half a round takes 43).
+template <class S>
+int rounds_time(const Gemm16& g, int a_round)
+{
+    // tiles as the groups have them on average: half a tile each is empty
+    const int64_t some = g.M < g.G ? g.M : g.G, half = g.M / S::BM + g.G / 2;
+    const int64_t slots = g.bounds ? (half > some ? half : some) : (g.M + S::BM - 1) / S::BM;
+    const int64_t tiles = slots * (int64_t)nblk(g.N, g.swiglu ? S::BN / 2 : S::BN), rest = tiles % kGrid<S>;
+    const int64_t t = tiles / kGrid<S> * a_round + (rest == 0 ? 0 : rest <= kGrid<S> - 256 ? 43 : a_round);
+    return (int)(t < INT32_MAX ? t : INT32_MAX);
 }
 
 template <int kIn, int kT, bool kSwiglu>
-hipError_t launch_tail(const Gemm16& g, hipStream_t st)
+hipError_t launch_shape(const Gemm16& g, hipStream_t st)
 {
-    return g.K % 64 || g.K < 128 ? launch_shape<kIn, kT, kSwiglu, true>(g, st) : launch_shape<kIn, kT, kSwiglu, false>(g, st);
+    // the tiled kernel reaches a tile's rows, or all of A through the row table, by 32 bits of offset
+    const int64_t a_span = (g.rows || g.row_div > 1 ? g.a_rows : Tile256::BM) * g.a_stride, b_span = Tile256::BN * g.b_stride;
+    const bool far = a_span > (int64_t)UINT32_MAX || b_span > (int64_t)UINT32_MAX;
+    // Too few tiles to fill the chip, whose waves the few-row kernel has share K.  Groups of a row or two: gate/up of
+    // 8 rows (N = 768, K = 2048) 13 us against 17 of 64 x 128 tiles, of 16 rows 20, 22, of 32 rows 43, 43; down of 16 rows
+    // (N = 2048, K = 768) 13.5, 13.4.  One matrix 4096 x 4096: 1 row 7.7 us against 18 of 64 x 64, 16 rows 10, 18, 32
+    // rows 16.6, 17.9, 48 rows 20, 18; with SwiGLU (N = 1536) 32 rows 15.4, 23, 64 rows 19, 23; 1024 x 2048: 64 rows 6.1, 10.8.
+    const int64_t tiles16 = slots_of(g, 16) * (int64_t)nblk(g.N, 16);
+    const bool few = far || (g.bounds ? g.M <= 24 : g.M <= (kSwiglu ? 64 : 32) || tiles16 <= 256);
+    if constexpr (kSwiglu) {
+        if (few && !g.bounds && g.M > 32) return launch_few<kIn, kT, true, 2, 2>(g, st);
+        if (few) return launch_few<kIn, kT, true, 1, 2>(g, st);
+    } else {
+        // 32 columns a workgroup: half the reads of A where there are workgroups enough (20 rows: 16.0 us, 17.8)
+        if (few && tiles16 <= 256) return launch_few<kIn, kT, false, 1, 1>(g, st);
+        if (few) return launch_few<kIn, kT, false, 1, 2>(g, st);
+    }
+    // The shape whose tiles are through first.  Measured at 4096 x 4096, us of 64 x 64, 64 x 128, 128 x 128, the same in
+    // twos, 128 x 256, 256 x 256: 64 rows 18, 23, 30, 41, 49, 81; 512: 35, 26, 32, 42, 50, 84; 1024: 64, 48, 37, 50, 53, 87;
+    // 2048: 122, 92, 68, 66, 68, 95; 5000: 314, 228, 174, 158, 174, 190; 8192: -, 318, -, 271, 249, 221.  Over groups, where B's
+    // bytes are most of it: 512 rows in 64 groups (N = K = 2048) 108, 115, 119, 126, 126, 146; gate/up of 64 rows in
+    // each of 128 (N = 768, K = 2048) -, 180, 160, 161, 159, 196; down of 256 in each of 256 (N = 4096, K = 1536) 1902, 1576,
+    // 1359, 1298, 1205, 1380.
+    const int t[] = {kSwiglu ? INT32_MAX : rounds_time<Deep64>(g, 18), rounds_time<DeepWide>(g, 24), rounds_time<Deep128>(g, 36),
+                     rounds_time<Tile128>(g, 68), rounds_time<TileWide>(g, 62), rounds_time<Tile256>(g, 108)};
+    int best = 0;
+    for (int i = 1; i < 6; ++i) best = t[i] < t[best] ? i : best;
+    if constexpr (!kSwiglu) {                             // gate and up rows are 32 each in a wave
+        if (best == 0) return launch_tile<Deep64, kIn, kT, kSwiglu>(g, st);
+    }
+    if (best == 1) return launch_tile<DeepWide, kIn, kT, kSwiglu>(g, st);
+    if (best == 2) return launch_tile<Deep128, kIn, kT, kSwiglu>(g, st);
+    if (best == 3) return launch_tile<Tile128, kIn, kT, kSwiglu>(g, st);
+    if (best == 4) return launch_tile<TileWide, kIn, kT, kSwiglu>(g, st);
+    return launch_tile<Tile256, kIn, kT, kSwiglu>(g, st);
 }
 
 template <int kIn>
-hipError_t launch_typed(const Gemm16& g, hipStream_t st)
+hipError_t launch_gemm16_typed(const Gemm16& g, hipStream_t st)
 {
-    if (g.out_type == kF32) return g.swiglu ? launch_tail<kIn, kF32, true>(g, st) : launch_tail<kIn, kF32, false>(g, st);
-    return g.swiglu ? launch_tail<kIn, kIn, true>(g, st) : launch_tail<kIn, kIn, false>(g, st);
+    if (g.out_type == kF32) return g.swiglu ? launch_shape<kIn, kF32, true>(g, st) : launch_shape<kIn, kF32, false>(g, st);
+    return g.swiglu ? launch_shape<kIn, kIn, true>(g, st) : launch_shape<kIn, kIn, false>(g, st);
 }
 
 }  // namespace
-
-hipError_t launch_gemm16(const Gemm16& g, hipStream_t st)
-{
-    if (g.M == 0) return hipSuccess;
-    return g.in_type == kBF16 ? launch_typed<kBF16>(g, st) : launch_typed<kF16>(g, st);
-}
 
 }  // namespace moe

@@ -664,12 +664,47 @@ __global__ __launch_bounds__(64 * S::NW) void k_mx_tile(MxGemm a, int n_tiles, i
 // operands' first bytes, the waves' sums.
 constexpr int kFewWaves = 8, kFewRows = 32;
 
+// Groups of a row table: row slot s belongs to the last group g whose first slot
+// bounds[g] / 32 + g is <= s (a group of c rows never needs more than the
+// bounds[g + 1] / 32 + 1 - bounds[g] / 32 slots up to the next group's first), so a
+// workgroup finds its rows from the bounds alone, and where there is nothing to do it ends.
+struct Rows {
+    int g;
+    int64_t m0, m1;           // rows [m0, m1); m0 >= m1: nothing to do
+};
+
+// The rows of a slot, the same on all lanes, by the wave together.
+__device__ __forceinline__ Rows rows_of_slot(const MxGemm& a, int64_t slot)
+{
+    if (!a.bounds) {
+        const int64_t m0 = slot * kFewRows;
+        return {0, m0, m0 + kFewRows < a.M ? m0 + kFewRows : a.M};
+    }
+    // 64 groups are compared at a time, one per lane: two rounds of loads up to 4096 groups
+    int g = 0, span = a.G;
+    const int lane = threadIdx.x & 63;
+    while (span > 1) {
+        const int step = (span + 63) >> 6, at = g + lane * step;
+        const bool le = lane * step < span && (int64_t)(bound_of(a, at) / kFewRows) + at <= slot;
+        const int n = __popcll(__ballot(le));             // a run of lanes from 0 for bounds that ascend
+        const int skip = (n > 0 ? n - 1 : 0) * step;
+        g += skip;
+        span = span - skip < step ? span - skip : step;
+    }
+    g = __builtin_amdgcn_readfirstlane(g);
+    const int64_t b0 = bound_of(a, g), b1 = bound_of(a, g + 1);
+    int64_t m0 = b0 + (slot - (b0 / kFewRows + g)) * kFewRows;
+    const int64_t m1 = m0 + kFewRows < b1 ? m0 + kFewRows : b1;
+    if (m0 < b0) m0 = m1;                                 // bounds that do not ascend: nothing before the group's rows
+    return {g, m0, m1};
+}
+
 template <int kT, bool kSwiglu, bool kAligned>
 __global__ __launch_bounds__(64 * kFewWaves) void k_mx_few(MxGemm a)
 {
     constexpr int NT = kSwiglu ? 2 : 1;
     __shared__ float red[kFewWaves][NT][32][33];
-    const Rows t = rows_of_slot<kFewRows>(a, blockIdx.x);
+    const Rows t = rows_of_slot(a, blockIdx.x);
     if (t.m0 >= t.m1) return;                             // uniform
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, j = lane & 31;
     const int nb = a.K / 32, NB = kSwiglu ? 2 * a.N : a.N;

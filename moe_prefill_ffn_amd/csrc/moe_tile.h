@@ -1,5 +1,5 @@
 // What the kernels of products over a row table share: loads straight into LDS, the order of
-// rows in LDS, where a group's rows are, SwiGLU.
+// rows in LDS, the groups' bounds, SwiGLU.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -66,42 +66,6 @@ constexpr int kListMost = 256;                            // tiles a workgroup l
 struct ListedTile {
     int g, m0, m1, nt;
 };
-
-// Groups of a row table: row slot s belongs to the last group g whose first slot
-// bounds[g] / kSlotRows + g is <= s (a group of c rows never needs more than the
-// bounds[g + 1] / kSlotRows + 1 - bounds[g] / kSlotRows slots up to the next group's first), so a
-// workgroup finds its rows from the bounds alone, and where there is nothing to do it ends.
-struct Rows {
-    int g;
-    int64_t m0, m1;           // rows [m0, m1); m0 >= m1: nothing to do
-};
-
-// The rows of a slot, the same on all lanes, by the wave together.
-template <int kSlotRows, class Args>
-__device__ __forceinline__ Rows rows_of_slot(const Args& a, int64_t slot)
-{
-    if (!a.bounds) {
-        const int64_t m0 = slot * kSlotRows;
-        return {0, m0, m0 + kSlotRows < a.M ? m0 + kSlotRows : a.M};
-    }
-    // 64 groups are compared at a time, one per lane: two rounds of loads up to 4096 groups
-    int g = 0, span = a.G;
-    const int lane = threadIdx.x & 63;
-    while (span > 1) {
-        const int step = (span + 63) >> 6, at = g + lane * step;
-        const bool le = lane * step < span && (int64_t)(bound_of(a, at) / kSlotRows) + at <= slot;
-        const int n = __popcll(__ballot(le));             // a run of lanes from 0 for bounds that ascend
-        const int skip = (n > 0 ? n - 1 : 0) * step;
-        g += skip;
-        span = span - skip < step ? span - skip : step;
-    }
-    g = __builtin_amdgcn_readfirstlane(g);
-    const int64_t b0 = bound_of(a, g), b1 = bound_of(a, g + 1);
-    int64_t m0 = b0 + (slot - (b0 / kSlotRows + g)) * kSlotRows;
-    const int64_t m1 = m0 + kSlotRows < b1 ? m0 + kSlotRows : b1;
-    if (m0 < b0) m0 = m1;                                 // bounds that do not ascend: nothing before the group's rows
-    return {g, m0, m1};
-}
 
 }  // namespace
 

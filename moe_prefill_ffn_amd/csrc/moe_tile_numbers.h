@@ -83,9 +83,19 @@ struct TileNumbers {
         return (uint32_t)__builtin_amdgcn_readfirstlane((int)all);
     }
 
+    // Tile `in` of a group of `high` row tiles by n_tiles column tiles: bands of 8 row tiles, in a band one
+    // column tile after the other.
+    __device__ __forceinline__ static void place(uint32_t in, uint32_t high, int n_tiles, int* row, int* nt)
+    {
+        const uint32_t band = in / (uint32_t)(8 * n_tiles), first = band * 8, of = high - first < 8 ? high - first : 8;
+        in -= first * n_tiles;
+        *row = (int)(first + in % of);
+        *nt = (int)(in / of);
+    }
+
     // The run's tiles from number list0 on, into LDS: as many as there are, kListMost at most.  Tiles are
-    // numbered in bands of 8 row tiles by all column tiles, so that what an XCD runs at once shares rows
-    // of A and of B in its L2.  n_tiles * slots <= 2^30.
+    // numbered group by group, so that what an XCD runs at once shares rows of A and of B in its L2 and a
+    // group's B is read at one time.  n_tiles * slots <= 2^30.
     template <class Args>
     __device__ __forceinline__ int list(const Args& a, ListedTile* s_list, int64_t list0, const TileRun& run, int n_tiles)
     {
@@ -93,22 +103,21 @@ struct TileNumbers {
         const int tid = threadIdx.x;
         const int64_t id = list0 + (int64_t)tid * run.step;
         const bool want = tid < kListMost && id < run.end;
-        const uint32_t band = (uint32_t)id / (uint32_t)(8 * n_tiles), first = band * 8;
-        const uint32_t high = slots - first < 8 ? (uint32_t)(slots - first) : 8;
-        const uint32_t in = (uint32_t)id - first * n_tiles;
-        const int64_t at = first + (want ? in % high : 0);
-        const int nt = want ? (int)(in / high) : 0;
+        int row, nt;
         __syncthreads();                                  // the previous list is done
         if (!a.bounds) {
-            const int64_t end = (at + 1) * BM;
-            if (want) s_list[tid] = {0, (int)(at * BM), (int)(end < a.M ? end : a.M), nt};
+            if (want) {
+                place((uint32_t)id, (uint32_t)slots, n_tiles, &row, &nt);
+                const int64_t m0 = (int64_t)row * BM;
+                s_list[tid] = {0, (int)m0, (int)(m0 + BM < a.M ? m0 + BM : a.M), nt};
+            }
         }
-        int64_t before = 0;                               // tiles before the window's
+        const int64_t at = want ? (uint32_t)id / (uint32_t)n_tiles : 0;    // row tiles before it, whole groups' among them
+        int64_t before = 0;                               // row tiles before the window's
         for (int base = 0; a.bounds && base < a.G; base += kWin) {
             const bool have = a.G <= kWin && list0 == run.first;           // scanned already, uniform
             const uint32_t n = have ? first_window : scan(a, base);
             const int64_t x = at - before;
-            before += n;
             if (want && x >= 0 && x < n) {
                 int lo = 0, hi = kWin - 1;                // the last group with s_pre <= x
                 while (lo < hi) {
@@ -118,9 +127,12 @@ struct TileNumbers {
                     else
                         hi = mid - 1;
                 }
-                const int g = base + lo, m0 = bound(a, g) + (int)((uint32_t)x - s_pre[lo]) * BM, end = bound(a, g + 1);
-                s_list[tid] = {g, m0, m0 + BM < end ? m0 + BM : end, nt};
+                const int g = base + lo, m0 = bound(a, g), end = bound(a, g + 1);
+                place((uint32_t)(id - (before + s_pre[lo]) * n_tiles), (uint32_t)(end - m0 + BM - 1) / BM, n_tiles, &row, &nt);
+                const int r0 = m0 + row * BM;
+                s_list[tid] = {g, r0, r0 + BM < end ? r0 + BM : end, nt};
             }
+            before += n;
         }
         __syncthreads();
         const int64_t left = (run.end - list0 + run.step - 1) / run.step;
