@@ -11,21 +11,26 @@ namespace moe {
 constexpr int kLoraMostRank = 256, kLoraMostAdapters = 1 << 20;
 constexpr int64_t kLoraMostRows = 1 << 23;                // tiles of 16 rows, 256 threads each, in one launch
 
-// Rows of a tile, and parts of K whose sums are kept apart (each workgroup sums one): enough
-// workgroups to fill the chip from the few tiles that a small batch has, each with at least kLoraUnit of K.
+// Above this many rows the tiles are larger, see moe_lora.hip.
+constexpr int kLoraFewRows = 1024;
+static inline bool lora_few(int64_t M) { return M <= kLoraFewRows; }
+// Rows of a tile of x A^T, ranks of one, and parts of K whose sums are kept apart (each workgroup sums
+// one): enough workgroups to fill the chip from the few tiles of a small batch, each with at least
+// kLoraUnit of K.
 constexpr int kLoraUnit = 256, kLoraMostParts = 16, kLoraFill = 512;
-static inline int lora_tile(int64_t M) { return M > 1024 ? 32 : 16; }
-static inline int lora_parts(int64_t M, int K)
+static inline int lora_tile(int64_t M, int r) { return lora_few(M) ? 16 : r <= 16 ? 128 : r <= 32 ? 64 : 32; }
+static inline int lora_ranks(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : 64; }
+static inline int lora_parts(int64_t M, int K, int r)
 {
-    const int64_t tiles = (M + lora_tile(M) - 1) / lora_tile(M), want = (kLoraFill + tiles - 1) / tiles;
+    const int64_t tiles = (M + lora_tile(M, r) - 1) / lora_tile(M, r), want = (kLoraFill + tiles - 1) / tiles;
     const int64_t most = (K + kLoraUnit - 1) / kLoraUnit, p = want < most ? want : most;
     return (int)(p < kLoraMostParts ? p : kLoraMostParts);
 }
 // sums of the parts, [parts][M][r] fp32: enough for M rows or fewer (tiles * ceil(kLoraFill / tiles) < tiles + kLoraFill)
 static inline uint64_t lora_ws(int64_t M, int K, int r)
 {
-    const int64_t rows = (M + 31) / 32 * 32, most = (K + kLoraUnit - 1) / kLoraUnit;
-    const int64_t all = rows * (most < kLoraMostParts ? most : kLoraMostParts), few = rows + kLoraFill * 32;
+    const int64_t rows = (M + 127) / 128 * 128, most = (K + kLoraUnit - 1) / kLoraUnit;
+    const int64_t all = rows * (most < kLoraMostParts ? most : kLoraMostParts), few = rows + (int64_t)kLoraFill * lora_tile(kLoraFewRows + 1, r);
     return ((uint64_t)(all < few ? all : few) * r * 4 + 255) / 256 * 256;
 }
 

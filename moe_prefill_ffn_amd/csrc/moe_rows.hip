@@ -42,10 +42,31 @@ __global__ __launch_bounds__(kGroupThreads) void k_group_count(GroupRows g, int6
 __global__ __launch_bounds__(kGroupThreads) void k_group_place(GroupRows g, int64_t chunk)
 {
     extern __shared__ int lds[];
+    __shared__ int s_sum[2][kGroupThreads];
     const int E = g.E, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int* s_count = lds;                                   // [waves][E]: pairs of the wave, then its next row
     int* s_first = lds + kGroupWaves * E;                 // [E]: pairs of earlier workgroups
     int* s_wave = s_first + E;
+    // the other workgroups' counts: `parts` threads a group, each every so-many-th workgroup, eight loads out
+    int ep = 64;
+    while (ep < E) ep *= 2;
+    const int parts = kGroupThreads / ep;
+    if (gridDim.x > 1) {
+        const int e = tid & (ep - 1), blocks = (int)gridDim.x;
+        int all = 0, before = 0;
+        for (int b0 = tid / ep; b0 < blocks; b0 += 8 * parts) {
+            int n[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) n[i] = e < E && b0 + i * parts < blocks ? g.ws[(int64_t)(b0 + i * parts) * E + e] : 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                all += n[i];
+                before += b0 + i * parts < (int)blockIdx.x ? n[i] : 0;
+            }
+        }
+        s_sum[0][tid] = all;
+        s_sum[1][tid] = before;
+    }
     const int64_t p0 = blockIdx.x * chunk, p1 = p0 + chunk < g.pairs ? p0 + chunk : g.pairs;
     const int64_t share = ((p1 - p0 + kGroupWaves - 1) / kGroupWaves + 63) / 64 * 64;
     const int64_t w0 = p0 + wave * share < p1 ? p0 + wave * share : p1, w1 = w0 + share < p1 ? w0 + share : p1;
@@ -58,16 +79,14 @@ __global__ __launch_bounds__(kGroupThreads) void k_group_place(GroupRows g, int6
     __syncthreads();
     // thread e: the group's pairs in all, and before this workgroup's (E <= 1024 threads)
     int all = 0, before = 0;
-    if (tid < E) {
-        if (gridDim.x > 1) {
-            for (int b = 0; b < (int)gridDim.x; ++b) {
-                const int n = g.ws[(int64_t)b * E + tid];
-                all += n;
-                before += b < (int)blockIdx.x ? n : 0;
-            }
-        } else {
-            for (int w = 0; w < kGroupWaves; ++w) all += s_count[w * E + tid];
+    if (gridDim.x > 1) {
+        for (int q = 0; tid < E && q < parts; ++q) {      // tid + q ep < 1024
+            all += s_sum[0][tid + q * ep];
+            before += s_sum[1][tid + q * ep];
         }
+    } else if (tid < E) {
+#pragma unroll
+        for (int w = 0; w < kGroupWaves; ++w) all += s_count[w * E + tid];
     }
     int upto = all;
 #pragma unroll
@@ -85,11 +104,13 @@ __global__ __launch_bounds__(kGroupThreads) void k_group_place(GroupRows g, int6
             g.bounds[tid] = first;
             if (tid == E - 1) g.bounds[E] = first + all;
         }
-        int at = first + before;
+        int at = first + before, n[kGroupWaves];
+#pragma unroll
+        for (int w = 0; w < kGroupWaves; ++w) n[w] = s_count[w * E + tid];
+#pragma unroll
         for (int w = 0; w < kGroupWaves; ++w) {
-            const int n = s_count[w * E + tid];
             s_count[w * E + tid] = at;
-            at += n;
+            at += n[w];
         }
     }
     __syncthreads();
