@@ -292,125 +292,149 @@ __device__ __forceinline__ Parts<kIn, kP, kKS> split(const float (&s)[kKS][8])
     return p;
 }
 
-// Eight consecutive values of a row: from two 16-byte vectors (16-bit types: the first); the n there
-// are one by one; and to memory, `wide` in aligned 16-byte vectors.
-__device__ __forceinline__ void unpack8(const uint4 (&raw)[2], int type, float (&v)[8])
+// n consecutive values, n * size <= 16 bytes, of a vector of that type; and to aligned memory.
+template <int n>
+__device__ __forceinline__ void unpack(const uint4& raw, int type, float (&v)[n])
 {
-    const uint32_t w[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     if (type == kF32) {
+        if constexpr (n == 4) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[e]);
+            for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(w[e]);
+        }
     } else if (type == kBF16) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+        for (int e = 0; e < n; ++e) v[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = (float)__builtin_bit_cast(_Float16, (uint16_t)(w[e / 2] >> (16 * (e & 1))));
+        for (int e = 0; e < n; ++e) v[e] = (float)__builtin_bit_cast(_Float16, (uint16_t)(w[e / 2] >> (16 * (e & 1))));
     }
 }
-__device__ __forceinline__ void load_row8(const void* p, int64_t at, int type, int n, float (&v)[8])
+template <int n>
+__device__ __forceinline__ void store_row(void* p, int64_t at, int type, const float (&v)[n])
 {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        v[e] = 0.0f;
-        if (e >= n) continue;
-        v[e] = type == kF32 ? static_cast<const float*>(p)[at + e] : type == kBF16 ? (float)static_cast<const __bf16*>(p)[at + e]
-                                                                                   : (float)static_cast<const _Float16*>(p)[at + e];
+    if (type == kF32) {
+        if constexpr (n == 4) store_n<kF32, 4>(static_cast<float*>(p) + at, v);
+    } else if (type == kBF16) {
+        store_n<kBF16, n>(static_cast<__bf16*>(p) + at, v);
+    } else {
+        store_n<kF16, n>(static_cast<_Float16*>(p) + at, v);
     }
 }
-__device__ __forceinline__ void store_row8(void* p, int64_t at, int type, bool wide, int n, const float (&v)[8])
+__device__ __forceinline__ float load1(const void* p, int64_t at, int type)
 {
-    if (wide) {
-        if (type == kF32) {
-            const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
-            store_n<kF32, 4>(static_cast<float*>(p) + at, lo);
-            store_n<kF32, 4>(static_cast<float*>(p) + at + 4, hi);
-        } else if (type == kBF16) {
-            store_n<kBF16, 8>(static_cast<__bf16*>(p) + at, v);
-        } else {
-            store_n<kF16, 8>(static_cast<_Float16*>(p) + at, v);
-        }
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        if (e >= n) continue;
-        if (type == kF32)
-            static_cast<float*>(p)[at + e] = v[e];
-        else if (type == kBF16)
-            static_cast<__bf16*>(p)[at + e] = (__bf16)v[e];
-        else
-            static_cast<_Float16*>(p)[at + e] = (_Float16)v[e];
-    }
+    return type == kF32 ? static_cast<const float*>(p)[at] : type == kBF16 ? (float)static_cast<const __bf16*>(p)[at]
+                                                                           : (float)static_cast<const _Float16*>(p)[at];
+}
+__device__ __forceinline__ void store1(void* p, int64_t at, int type, float v)
+{
+    if (type == kF32)
+        static_cast<float*>(p)[at] = v;
+    else if (type == kBF16)
+        static_cast<__bf16*>(p)[at] = (__bf16)v;
+    else
+        static_cast<_Float16*>(p)[at] = (_Float16)v;
 }
 
-// A workgroup: 16 kR rows by cols columns (a multiple of 128), its waves 32 columns at a time as two
-// products of 16 columns.  Product t has columns 8 (i / 4) + 4 t + i % 4 of the 32, so that lane group g gets 8
-// consecutive ones, 8 g on, of its row from the two.  The loads of B and base for the next 32 columns are out
-// under the products (kKS > 4: registers are too few), those for the first under the sum of the parts, which
-// the workgroup makes once, in LDS.
-template <int kIn, int kP, int kKS, int kR>
-__global__ __launch_bounds__(kLoraThreads) void k_lora_up(LoraAdd l, int parts, int cols, int wide)
+// Few rows, or rows that are not aligned vectors.  A workgroup: 16 rows by cols columns (a multiple of 256), its
+// waves 64 columns at a time, as products of 16.  The parts are summed once, in LDS.  A wave's results go through
+// LDS, so that base and out are read and written a whole line at a time: kV values a lane (4 where one of the two
+// is fp32, else 8; 1: rows that are not aligned vectors).
+template <int kIn, int kP, int kKS, int kV>
+__global__ __launch_bounds__(kLoraThreads) void k_lora_up_few(LoraAdd l, int parts, int cols)
 {
-    constexpr int kRanks = 32 * kKS;
-    __shared__ float sum[16 * kR][kRanks + 4];
+    constexpr int kRanks = 32 * kKS, kRows = 16;
+    constexpr int kB = kKS <= 2 ? 4 : kKS == 4 ? 2 : 1;   // products of 16 columns whose B is in registers at once
+    __shared__ float sum[kRows][kRanks + 4];
+    __shared__ float tile[kLoraWaves][kRows][68];
     const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4, wave = tid >> 6;
-    const int64_t m0 = (int64_t)blockIdx.x * (16 * kR);
-    const int first = (int)blockIdx.y * cols + wave * 32, end = ((int)blockIdx.y + 1) * cols < l.N ? ((int)blockIdx.y + 1) * cols : l.N;
-    constexpr int kStep = 32 * kLoraWaves;
-    const int id[1] = {lane < 16 * kR ? adapter_of(l, m0 + lane) : -1};
-    int ids[kR];
-#pragma unroll
-    for (int q = 0; q < kR; ++q) ids[q] = __shfl(id[0], 16 * q + i);
+    const int64_t m0 = (int64_t)blockIdx.x * kRows;
+    const int first = (int)blockIdx.y * cols + wave * 64, end = ((int)blockIdx.y + 1) * cols < l.N ? ((int)blockIdx.y + 1) * cols : l.N;
+    constexpr int kStep = 64 * kLoraWaves;
+    const int id[1] = {lane < kRows ? adapter_of(l, m0 + lane) : -1};
+    const bool there = lane < kRows && m0 + lane < l.M;
     const int base_size = dtype_bytes(l.base_type);
-    struct Cols {                                         // 32 columns' operands
-        v4i b[2][kKS];
-        uint4 base[kR][2];                                // this lane's 8 of a row, 16 or 32 bytes
+    // out = base + z (null: 0) of the rows in `rows` in columns n0 .. n0 + 63: lane's columns from `col` on, of every
+    // kPer-th row
+    constexpr int kLanes = 64 / kV, kPer = kV, kIt = kV > 1 ? kRows / kPer : 1;
+    const int col = kV * (lane % kLanes), row0 = lane / kLanes;
+    struct Base {
+        uint4 v[kIt];
     };
-    // eight columns from n on of this lane's row of row tile q
-    auto finish = [&](int q, int n, float factor, float scale, const float (&z)[8], const uint4 (&raw)[2]) {
-        const int64_t m = m0 + 16 * q + i;
-        if (n >= l.N) return;
-        float v[8] = {};
-        if (l.base) {
-            if (wide)
-                unpack8(raw, l.base_type, v);
-            else
-                load_row8(l.base, m * l.base_stride + n, l.base_type, l.N - n, v);
+    auto load_base = [&](uint64_t rows, int n0, Base& raw) {
+        if constexpr (kV > 1) {
+            if (!l.base || n0 + col >= l.N) return;
+#pragma unroll
+            for (int t = 0; t < kIt; ++t) {
+                const int row = kPer * t + row0;
+                if (!(rows >> row & 1)) continue;
+                const uint8_t* p = static_cast<const uint8_t*>(l.base) + ((m0 + row) * l.base_stride + n0 + col) * base_size;
+                if (kV * base_size == 16) {
+                    raw.v[t] = *reinterpret_cast<const uint4*>(p);
+                } else {
+                    const uint2 half = *reinterpret_cast<const uint2*>(p);
+                    raw.v[t].x = half.x;
+                    raw.v[t].y = half.y;
+                }
+            }
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += z[e] * factor * scale;
-        store_row8(l.out, m * l.out_stride + n, l.out_type, wide, l.N - n, v);
     };
-    auto load_base = [&](int cur, int n0, uint4 (&raw)[kR][2]) {
-        if (!l.base || !wide || n0 + 8 * g >= l.N) return;
+    auto finish = [&](uint64_t rows, int n0, const Base& raw, const float (*z)[68]) {
+        if constexpr (kV > 1) {
+            if (n0 + col >= l.N) return;
 #pragma unroll
-        for (int q = 0; q < kR; ++q) {
-            const int64_t m = m0 + 16 * q + i;
-            if (ids[q] != cur || m >= l.M) continue;
-            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(l.base) + (m * l.base_stride + n0 + 8 * g) * base_size);
-            raw[q][0] = p[0];
-            if (base_size == 4) raw[q][1] = p[1];
+            for (int t = 0; t < kIt; ++t) {
+                const int row = kPer * t + row0;
+                if (!(rows >> row & 1)) continue;
+                float v[kV] = {};
+                if (l.base) unpack<kV>(raw.v[t], l.base_type, v);
+                if (z) {
+#pragma unroll
+                    for (int e = 0; e < kV; e += 4) {
+                        const v4f add = *reinterpret_cast<const v4f*>(&z[row][col + e]);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) v[e + x] += add[x];
+                    }
+                }
+                store_row<kV>(l.out, (m0 + row) * l.out_stride + n0 + col, l.out_type, v);
+            }
+        } else {
+            const int n = n0 + lane;
+            if (n >= l.N) return;
+            for (int t = 0; t < kRows; t += 8) {
+                if (!(rows >> t & 255)) continue;         // uniform
+                float v[8] = {};
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (l.base && (rows >> (t + e) & 1)) v[e] = load1(l.base, (m0 + t + e) * l.base_stride + n, l.base_type);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (rows >> (t + e) & 1) store1(l.out, (m0 + t + e) * l.out_stride + n, l.out_type, v[e] + (z ? z[t + e][lane] : 0.0f));
+            }
         }
     };
     each_adapter(id, blockIdx.z, gridDim.z, [&](int cur) {
-        auto load = [&](Cols& c, int n0) {
+        const uint64_t rows = __ballot(id[0] == cur);
+        v4i b[kB][kKS];
+        auto load_b = [&](int n0) {                       // of kB products' columns from n0 on
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int col = n0 + 8 * (i >> 2) + 4 * t + (i & 3), n = col < l.N ? col : l.N - 1;
-                const uint8_t* b = l.b + ((int64_t)cur * l.N + n) * l.r * 2 + 16 * g;
+            for (int t = 0; t < kB; ++t) {
+                const int n = n0 + 16 * t + i < l.N ? n0 + 16 * t + i : l.N - 1;
+                const uint8_t* p = l.b + ((int64_t)cur * l.N + n) * l.r * 2 + 16 * g;
 #pragma unroll
-                for (int k = 0; k < kKS; ++k) c.b[t][k] = 32 * k + 8 * g < l.r ? *reinterpret_cast<const v4i*>(b + 64 * k) : v4i{0, 0, 0, 0};
+                for (int k = 0; k < kKS; ++k) b[t][k] = 32 * k + 8 * g < l.r ? *reinterpret_cast<const v4i*>(p + 64 * k) : v4i{0, 0, 0, 0};
             }
-            load_base(cur, n0, c.base);
         };
-        Cols c0, c1;
-        if (first < end) load(c0, first);
+        Base raw;
+        if (first < end) {
+            load_b(first);
+            load_base(rows, first, raw);
+        }
         __syncthreads();                                  // the last adapter's sums are read
-        for (int e = tid * 4; e < 16 * kR * kRanks; e += 4 * kLoraThreads) {
-            const int row = e / kRanks, q = e % kRanks, who = __shfl(id[0], row);
+        for (int e = tid * 4; e < kRows * kRanks; e += 4 * kLoraThreads) {
+            const int row = e / kRanks, q = e % kRanks;
             v4f s = {0, 0, 0, 0};
-            if (q < l.r && who == cur) {
+            if (q < l.r && (rows >> row & 1)) {
                 const float* w = l.ws + (m0 + row) * l.r + q;
                 const int64_t step = l.M * l.r;
                 int part = 0;
@@ -427,99 +451,284 @@ __global__ __launch_bounds__(kLoraThreads) void k_lora_up(LoraAdd l, int parts, 
             *reinterpret_cast<v4f*>(&sum[row][q]) = s;
         }
         __syncthreads();
-        Parts<kIn, kP, kKS> p[kR];
+        float s[kKS][8];
 #pragma unroll
-        for (int q = 0; q < kR; ++q) {
-            float s[kKS][8];
+        for (int k = 0; k < kKS; ++k)
 #pragma unroll
-            for (int k = 0; k < kKS; ++k)
+            for (int e = 0; e < 8; e += 4) {
+                const v4f v = *reinterpret_cast<const v4f*>(&sum[i][32 * k + 8 * g + e]);
 #pragma unroll
-                for (int e = 0; e < 8; e += 4) {
-                    const v4f v = *reinterpret_cast<const v4f*>(&sum[16 * q + i][32 * k + 8 * g + e]);
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) s[k][e + z] = v[z];
-                }
-            p[q] = split<kIn, kP, kKS>(s);
-        }
+                for (int z = 0; z < 4; ++z) s[k][e + z] = v[z];
+            }
+        const Parts<kIn, kP, kKS> p = split<kIn, kP, kKS>(s);
         const float scale = l.scales ? l.scales[cur] : 1.0f;
-        auto compute = [&](const Cols& c, int n0) {
-            v4f acc[kR][2];
+        for (int n0 = first; n0 < end; n0 += kStep) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+            for (int t0 = 0; t0 < 4; t0 += kB) {
+                v4f acc[kB];
 #pragma unroll
-                for (int q = 0; q < kR; ++q) acc[q][t] = v4f{0, 0, 0, 0};
+                for (int t = 0; t < kB; ++t) {
+                    acc[t] = v4f{0, 0, 0, 0};
 #pragma unroll
-                for (int k = 0; k < kKS; ++k)
+                    for (int k = 0; k < kKS; ++k)
 #pragma unroll
-                    for (int z = kP - 1; z >= 0; --z)
+                        for (int z = kP - 1; z >= 0; --z) acc[t] = mfma16x16<kIn>(b[t][k], p.v[k][z], acc[t]);
+                }
+                if (t0 + kB < 4)
+                    load_b(n0 + 16 * (t0 + kB));
+                else if (n0 + kStep < end)
+                    load_b(n0 + kStep);
 #pragma unroll
-                        for (int q = 0; q < kR; ++q) acc[q][t] = mfma16x16<kIn>(c.b[t][k], p[q].v[k][z], acc[q][t]);
+                for (int t = 0; t < kB; ++t) {
+                    v4f v;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = acc[t][e] * p.back * scale;
+                    *reinterpret_cast<v4f*>(&tile[wave][i][16 * (t0 + t) + 4 * g]) = v;
+                }
             }
-#pragma unroll
-            for (int q = 0; q < kR; ++q) {
-                if (ids[q] != cur) continue;
-                const float z[8] = {acc[q][0][0], acc[q][0][1], acc[q][0][2], acc[q][0][3], acc[q][1][0], acc[q][1][1], acc[q][1][2], acc[q][1][3]};
-                finish(q, n0 + 8 * g, p[q].back, scale, z, c.base[q]);
-            }
-        };
-        for (int n0 = first; n0 < end; n0 += 2 * kStep) {
-            if constexpr (kKS <= 4) {
-                if (n0 + kStep < end) load(c1, n0 + kStep);
-                compute(c0, n0);
-                if (n0 + kStep >= end) break;
-                if (n0 + 2 * kStep < end) load(c0, n0 + 2 * kStep);
-                compute(c1, n0 + kStep);
-            } else {
-                compute(c0, n0);
-                if (n0 + kStep >= end) break;
-                load(c0, n0 + kStep);
-                compute(c0, n0 + kStep);
-                if (n0 + 2 * kStep < end) load(c0, n0 + 2 * kStep);
-            }
+            // within a wave LDS works in order; the compiler must not move across
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            finish(rows, n0, raw, tile[wave]);
+            if (n0 + kStep < end) load_base(rows, n0 + kStep, raw);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         }
     });
     if (blockIdx.z != 0 || l.out == l.base) return;       // in place: rows of no adapter stay as they are
-    const float none[8] = {};
+    const uint64_t none = __ballot(there && id[0] < 0);
+    if (!none) return;
     for (int n0 = first; n0 < end; n0 += kStep) {
-        uint4 raw[kR][2];
-        load_base(-1, n0, raw);
-#pragma unroll
-        for (int q = 0; q < kR; ++q)
-            if (ids[q] < 0 && m0 + 16 * q + i < l.M) finish(q, n0 + 8 * g, 0.0f, 0.0f, none, raw[q]);
+        Base raw;
+        load_base(none, n0, raw);
+        finish(none, n0, raw, nullptr);
     }
 }
 
+// Many rows.  A workgroup: 64 rows, 16 of each of four waves, by cols columns (a multiple of 64), 64 at a time as a
+// stage in LDS: B's rows and base.  A fifth wave issues the stages' loads, NS - 1 ahead, straight into LDS, and alone
+// waits for them; the others' stores, which come back in order with a wave's loads, hold nothing up.  A wave adds its
+// products to base, and writes 16 rows a line at a time through LDS.  What bounds it is base and out, read and
+// written once.  (Four waves that loaded for themselves held too little in flight: 69 us with stores from the result
+// registers, 59 a line at a time, for 8192 rows of rank 64 and 4096 columns, 128 MB.)
+constexpr int kUpRows = 64, kUpCols = 64, kUpThreads = kLoraThreads + 64;
+
+template <int kKS>
+struct UpShape {
+    static constexpr int kRow = 64 * kKS, kB = kUpCols * kRow;               // bytes of a row of B (r padded), of a stage's
+    static constexpr int kChunks = 4 * kKS;
+    // which chunk of 16 bytes is in slot c of row n: 16 rows' same chunk lies in 16 distinct bank groups of 256 bytes
+    static __device__ __forceinline__ int swap(int n) { return (kKS == 1 ? n >> 2 : kKS == 2 ? n >> 1 : n) & (kChunks < 16 ? kChunks - 1 : 15); }
+};
+constexpr int up_slots(int KS, int base_size) { return KS == 8 || (KS == 4 && base_size == 4) ? 3 : 4; }
+// rows of the waves' results, padded against bank conflicts
+constexpr int up_out_row(int out_size) { return kUpCols * out_size + 16; }
+constexpr int up_lds(int KS, int base_size, int out_size)
+{
+    return up_slots(KS, base_size) * kUpCols * (64 * KS + kUpRows * base_size) + kUpRows * up_out_row(out_size);
+}
+
+// kBase, kOut: bytes of an element of base (0: there is none) and of out; those of 2 bytes are of x's type, known
+// here so that nothing branches between a stage's loads from LDS (2.1 us a stage where it did, of one wave a SIMD)
+template <int kIn, int kP, int kKS, int kBase, int kOut>
+__global__ __launch_bounds__(kUpThreads) void k_lora_up(LoraAdd l, int parts, int cols)
+{
+    using S = UpShape<kKS>;
+    constexpr int NS = up_slots(kKS, kBase), kBaseRow = kUpCols * kBase, kStage = S::kB + kUpRows * kBaseRow;
+    constexpr int kLoadsB = S::kB / 1024, kLoadsBase = kUpRows * kBaseRow / 1024, NL = kLoadsB + kLoadsBase;
+    static_assert((NS - 2) * NL <= 63, "vmcnt");
+    constexpr int kBaseChunks = kBaseRow / 16, kOutRow = up_out_row(kOut);
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t m0 = (int64_t)blockIdx.x * kUpRows;
+    const int first = (int)blockIdx.y * cols, end = first + cols < l.N ? first + cols : l.N, n = (end - first + kUpCols - 1) / kUpCols;
+    const int id[1] = {adapter_of(l, m0 + lane)};
+    auto base_swap = [](int row) { return kBase == 2 ? (row >> 1) & 7 : row & 15; };
+    each_adapter(id, 0, 1, [&](int cur) {
+        const uint64_t rows = __ballot(id[0] == cur);
+        if (wave == kLoraWaves) {
+            const uint32_t lds0 = lds_addr(lds);
+            const uint8_t* b_at = l.b + ((int64_t)cur * l.N + first) * l.r * 2;
+            const uint8_t* base_at = static_cast<const uint8_t*>(l.base) + (m0 * l.base_stride + first) * kBase;
+            // What is not there (a column past the end, a rank past r, a row of another adapter) is read from what
+            // is, and not used.  32 bits of offset: the host checked that 64 rows of base span less.
+            const int one = __builtin_ctzll(rows);
+            uint32_t base_row[kLoadsBase > 0 ? kLoadsBase : 1];
+#pragma unroll
+            for (int k = 0; k < kLoadsBase; ++k) {
+                const int row = (k * 64 + lane) / (kBase ? kBaseChunks : 1);
+                base_row[k] = (uint32_t)((rows >> row & 1) ? row : one) * (uint32_t)(l.base_stride * kBase);
+            }
+            auto issue = [&](int s) {
+                const uint32_t to = lds0 + s % NS * kStage;
+                const int last = end - 1 - first - s * kUpCols;          // the last column's place in the stage
+                const uint8_t* bs = b_at + (int64_t)s * kUpCols * l.r * 2;
+#pragma unroll 4                                          // all at once keeps too many addresses
+                for (int k = 0; k < kLoadsB; ++k) {
+                    const int at = k * 64 + lane, col = at / S::kChunks, c = at % S::kChunks ^ S::swap(col);
+                    g2lds16_at(bs, (uint32_t)((col < last ? col : last) * l.r * 2 + (8 * c < l.r ? c : 0) * 16), to + k * 1024);
+                }
+                if constexpr (kBase) {
+                    const uint8_t* from = base_at + s * kUpCols * kBase;
+#pragma unroll
+                    for (int k = 0; k < kLoadsBase; ++k) {
+                        const int at = k * 64 + lane, c = at % kBaseChunks ^ base_swap(at / kBaseChunks);
+                        g2lds16_at(from, base_row[k] + (c * (16 / kBase) <= last ? c : 0) * 16, to + S::kB + k * 1024);
+                    }
+                }
+            };
+#pragma unroll
+            for (int s = 0; s < NS - 1; ++s)
+                if (s < n) issue(s);
+            for (int s = 0; s < n; ++s) {
+                if (s + NS - 1 <= n)                      // the loads of the NS - 2 stages behind it may be out
+                    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((NS - 2) * NL) : "memory");
+                else
+                    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+                if (s + NS - 1 < n) issue(s + NS - 1);    // into the slot that every wave has read
+            }
+        } else {
+            const int row = 16 * wave + i;                // of the tile
+            const bool mine = rows >> row & 1;
+            float sums[kKS][8];
+#pragma unroll
+            for (int k = 0; k < kKS; ++k) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sums[k][e] = 0.0f;
+                const int q = 32 * k + 8 * g;
+                if (mine && q < l.r) {
+                    const float* w = l.ws + (m0 + row) * l.r + q;
+                    for (int part = 0; part < parts; ++part, w += l.M * l.r) {
+                        const v4f lo = *reinterpret_cast<const v4f*>(w), hi = *reinterpret_cast<const v4f*>(w + 4);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            sums[k][e] += lo[e];
+                            sums[k][4 + e] += hi[e];
+                        }
+                    }
+                }
+            }
+            const Parts<kIn, kP, kKS> p = split<kIn, kP, kKS>(sums);
+            const float scale = l.scales ? l.scales[cur] : 1.0f;
+            uint8_t* out_rows = lds + NS * kStage + 16 * wave * kOutRow;
+            for (int s = 0; s < n; ++s) {
+                // this wave's reads of the stage before are done; the fifth wave admits this one
+                asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                const uint8_t* at = lds + s % NS * kStage;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const int col = 16 * t + i;
+                    v4f acc = {0, 0, 0, 0};
+#pragma unroll
+                    for (int k = 0; k < kKS; ++k) {
+                        v4i b = *reinterpret_cast<const v4i*>(at + col * S::kRow + (((4 * k + g) ^ S::swap(col)) << 4));
+                        if (32 * k + 8 * g >= l.r) b = v4i{0, 0, 0, 0};
+#pragma unroll
+                        for (int z = kP - 1; z >= 0; --z) acc = mfma16x16<kIn>(b, p.v[k][z], acc);
+                    }
+                    float v[4] = {};                      // columns 16 t + 4 g .. + 3 of the row
+                    if constexpr (kBase) {
+                        const int byte = (16 * t + 4 * g) * kBase;
+                        const uint8_t* from = at + S::kB + row * kBaseRow + (((byte >> 4) ^ base_swap(row)) << 4) + (byte & 15);
+                        uint4 raw;
+                        if constexpr (kBase == 4) {
+                            raw = *reinterpret_cast<const uint4*>(from);
+                        } else {
+                            const uint2 half = *reinterpret_cast<const uint2*>(from);
+                            raw = {half.x, half.y, 0, 0};
+                        }
+                        unpack<4>(raw, kBase == 4 ? (int)kF32 : kIn, v);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] += acc[e] * p.back * scale;
+                    store_row<4>(out_rows + i * kOutRow, 16 * t + 4 * g, kOut == 4 ? (int)kF32 : kIn, v);
+                }
+                // within a wave LDS works in order; the compiler must not move across
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                constexpr int kLanes = kUpCols * kOut / 16, kPer = 64 / kLanes;        // lanes a row, rows at a time
+                const int out_col = first + s * kUpCols + lane % kLanes * (16 / kOut);
+#pragma unroll
+                for (int q = 0; q < 16; q += kPer) {
+                    const int r = q + lane / kLanes;
+                    const uint4 v = *reinterpret_cast<const uint4*>(out_rows + r * kOutRow + lane % kLanes * 16);
+                    if (out_col < end && (rows >> (16 * wave + r) & 1))
+                        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(l.out) + ((m0 + 16 * wave + r) * l.out_stride + out_col) * kOut) = v;
+                }
+            }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // every wave has read the last stage
+    });
+    if (l.out == l.base || wave == kLoraWaves) return;    // in place: rows of no adapter stay as they are
+    const uint64_t none = __ballot(m0 + lane < l.M && id[0] < 0);
+    constexpr int kV = 16 / (kOut > kBase ? kOut : kBase), kLanes = kUpCols / kV;
+    for (int n0 = first; n0 < end; n0 += kUpCols) {
+        const int col = n0 + kV * (lane % kLanes);
+#pragma unroll
+        for (int r = lane / kLanes; r < 16; r += 64 / kLanes) {
+            const int64_t m = m0 + 16 * wave + r;
+            if (col >= end || !(none >> (16 * wave + r) & 1)) continue;
+            float v[kV] = {};
+            if constexpr (kBase == 4)
+                load_n<kF32, kV>(static_cast<const float*>(l.base) + m * l.base_stride + col, v);
+            else if constexpr (kBase == 2)
+                load_n<kIn, kV>(static_cast<const typename Elem<kIn>::type*>(l.base) + m * l.base_stride + col, v);
+            store_row<kV>(l.out, m * l.out_stride + col, kOut == 4 ? (int)kF32 : kIn, v);
+        }
+    }
+}
+
+template <int kIn, int kP, int kKS, int kBase, int kOut>
+hipError_t launch_up_ring(const LoraAdd& l, int parts, hipStream_t st)
+{
+    constexpr int lds = up_lds(kKS, kBase, kOut);
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_lora_up<kIn, kP, kKS, kBase, kOut>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+    // as many columns a workgroup as leave the chip full
+    const unsigned tiles = nblk(l.M, kUpRows);
+    const int64_t blocks = nblk(l.N, kUpCols), want = (256 * (163840 / lds) + tiles - 1) / tiles;
+    const int cols = (int)((blocks + want - 1) / want) * kUpCols;
+    hipLaunchKernelGGL((k_lora_up<kIn, kP, kKS, kBase, kOut>), dim3(tiles, nblk(l.N, cols)), dim3(kUpThreads), lds, st, l, parts, cols);
+    return hipSuccess;
+}
+
 template <int kIn, int kP, int kKS>
-void launch_up_tile(const LoraAdd& l, int parts, int ways, hipStream_t st)
+hipError_t launch_up_ranks(const LoraAdd& l, int parts, int ways, hipStream_t st)
 {
     // whole vectors of 8 columns at aligned addresses
     auto even = [&](const void* p, int64_t stride, int type) {
         return (reinterpret_cast<uintptr_t>(p) | (uint64_t)(stride * dtype_bytes(type))) % 16 == 0;
     };
-    const int wide = l.N % 8 == 0 && even(l.out, l.out_stride, l.out_type) && (!l.base || even(l.base, l.base_stride, l.base_type));
-    // a wave splits s into its parts once for its columns: as many columns as leave the chip full
-    const int rows = lora_few(l.M) ? 16 : 32;
-    const unsigned tiles = nblk(l.M, rows);
-    const int64_t blocks = nblk(l.N, 32 * kLoraWaves), want = (1024 + tiles - 1) / tiles;
-    const int cols = (int)((blocks + want - 1) / want) * 32 * kLoraWaves;
+    const bool wide = l.N % 8 == 0 && even(l.out, l.out_stride, l.out_type) && (!l.base || even(l.base, l.base_stride, l.base_type));
+    const int base = l.base ? dtype_bytes(l.base_type) : 0, out = dtype_bytes(l.out_type);
+    const bool types = (out == 4 || l.out_type == kIn) && (base != 2 || l.base_type == kIn);
+    if (!lora_few(l.M) && wide && types && (!l.base || l.base_stride * base <= 1 << 25)) {
+        if constexpr (kIn == kF16 || kP == 3) {
+            if (out == 4) return base == 0 ? launch_up_ring<kIn, kP, kKS, 0, 4>(l, parts, st) : base == 2 ? launch_up_ring<kIn, kP, kKS, 2, 4>(l, parts, st)
+                                                                                                         : launch_up_ring<kIn, kP, kKS, 4, 4>(l, parts, st);
+        }
+        if constexpr (kP == 2)
+            return base == 0 ? launch_up_ring<kIn, kP, kKS, 0, 2>(l, parts, st) : base == 2 ? launch_up_ring<kIn, kP, kKS, 2, 2>(l, parts, st)
+                                                                                           : launch_up_ring<kIn, kP, kKS, 4, 2>(l, parts, st);
+    }
+    const unsigned tiles = nblk(l.M, 16);
+    const int64_t blocks = nblk(l.N, 64 * kLoraWaves), want = (1024 + tiles - 1) / tiles;
+    const int cols = (int)((blocks + want - 1) / want) * 64 * kLoraWaves;
     const dim3 grid(tiles, nblk(l.N, cols), ways);
-    if (rows == 16)
-        hipLaunchKernelGGL((k_lora_up<kIn, kP, kKS, 1>), grid, dim3(kLoraThreads), 0, st, l, parts, cols, wide);
+    auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kLoraThreads), 0, st, l, parts, cols); };
+    if (!wide)
+        launch(k_lora_up_few<kIn, kP, kKS, 1>);
+    else if (base == 4 || out == 4)
+        launch(k_lora_up_few<kIn, kP, kKS, 4>);
     else
-        hipLaunchKernelGGL((k_lora_up<kIn, kP, kKS, 2>), grid, dim3(kLoraThreads), 0, st, l, parts, cols, wide);
+        launch(k_lora_up_few<kIn, kP, kKS, 8>);
+    return hipSuccess;
 }
 
 template <int kIn, int kP>
-void launch_up(const LoraAdd& l, int parts, int ways, hipStream_t st)
+hipError_t launch_up(const LoraAdd& l, int parts, int ways, hipStream_t st)
 {
-    if (l.r <= 32)
-        launch_up_tile<kIn, kP, 1>(l, parts, ways, st);
-    else if (l.r <= 64)
-        launch_up_tile<kIn, kP, 2>(l, parts, ways, st);
-    else if (l.r <= 128)
-        launch_up_tile<kIn, kP, 4>(l, parts, ways, st);
-    else
-        launch_up_tile<kIn, kP, 8>(l, parts, ways, st);
+    return l.r <= 32 ? launch_up_ranks<kIn, kP, 1>(l, parts, ways, st) : l.r <= 64 ? launch_up_ranks<kIn, kP, 2>(l, parts, ways, st)
+           : l.r <= 128 ? launch_up_ranks<kIn, kP, 4>(l, parts, ways, st) : launch_up_ranks<kIn, kP, 8>(l, parts, ways, st);
 }
 
 template <int kIn, int WR, int WC>
@@ -546,13 +755,12 @@ hipError_t launch_typed(const LoraAdd& l, hipStream_t st)
     const hipError_t e = lora_ranks(l.r) == 16 ? launch_down<kIn, 4, 1>(l, parts, ways, st) : lora_ranks(l.r) == 32 ? launch_down<kIn, 2, 2>(l, parts, ways, st)
                                                                                                                     : launch_down<kIn, 1, 4>(l, parts, ways, st);
     if (e != hipSuccess) return e;
-    bool three = false;
-    if constexpr (kIn == kBF16) {
-        three = l.out_type == kF32;
-        if (three) launch_up<kIn, 3>(l, parts, ways, st);
-    }
-    if (!three) launch_up<kIn, 2>(l, parts, ways, st);
-    return hipGetLastError();
+    hipError_t e2;
+    if constexpr (kIn == kBF16)
+        e2 = l.out_type == kF32 ? launch_up<kIn, 3>(l, parts, ways, st) : launch_up<kIn, 2>(l, parts, ways, st);
+    else
+        e2 = launch_up<kIn, 2>(l, parts, ways, st);
+    return e2 != hipSuccess ? e2 : hipGetLastError();
 }
 
 }  // namespace
