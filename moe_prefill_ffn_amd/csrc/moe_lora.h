@@ -14,12 +14,11 @@ constexpr int64_t kLoraMostRows = 1 << 23;                // tiles of 16 rows, 2
 // Above this many rows the tiles are larger, see moe_lora.hip.
 constexpr int kLoraFewRows = 1024;
 static inline bool lora_few(int64_t M) { return M <= kLoraFewRows; }
-// Rows of a tile of x A^T, ranks of one, and parts of K whose sums are kept apart (each workgroup sums
+// Rows of a tile of x A^T, and parts of K whose sums are kept apart (each workgroup sums
 // one): enough workgroups to fill the chip from the few tiles of a small batch, each with at least
 // kLoraUnit of K.
 constexpr int kLoraUnit = 256, kLoraMostParts = 16, kLoraFill = 512;
-static inline int lora_tile(int64_t M, int r) { return lora_few(M) ? 16 : r <= 16 ? 128 : r <= 32 ? 64 : 32; }
-static inline int lora_ranks(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : 64; }
+static inline int lora_tile(int64_t M, int r) { return lora_few(M) ? 16 : r <= 32 ? 128 : 64; }
 static inline int lora_parts(int64_t M, int K, int r)
 {
     const int64_t tiles = (M + lora_tile(M, r) - 1) / lora_tile(M, r), want = (kLoraFill + tiles - 1) / tiles;

@@ -31,6 +31,7 @@ __device__ __forceinline__ v4f mfma16x16(v4i w, v4i x, v4f c)
 }
 
 constexpr int kLoraWaves = 4, kLoraThreads = 64 * kLoraWaves;
+constexpr int kOneWaves = 8;              // of the launch that makes s itself
 
 // The adapter of row m, -1: none, or no such row.
 __device__ __forceinline__ int adapter_of(const LoraAdd& l, int64_t m)
@@ -134,21 +135,22 @@ __global__ __launch_bounds__(kLoraThreads) void k_lora_down_few(LoraAdd l, int p
 // What a chunk past the end of K is loaded from.
 __device__ const uint4 kZeros = {0, 0, 0, 0};
 
-// Many rows.  A workgroup: 32 WR rows by 16 WC ranks, a wave 32 by 16 of them; one part of K in stages
-// of 64 values (128 bytes a row, a cache line) through four LDS slots, three stages' loads out at a
-// time.  What bounds it is x, read once (and again for each further adapter of a tile's rows).
-template <int WR, int WC>
+// Many rows.  A workgroup: 32 WR rows by 16 WC TC ranks, a wave 32 by 16 TC of them; one part of K in
+// stages of 64 values (128 bytes a row, a cache line) through four LDS slots, three stages' loads out at a
+// time.  What bounds it is x, read once (and again for each further adapter of a tile's rows), and A, read
+// from the L2 for each tile: 8192 rows of rank 64, K = 4096 30 us in tiles of 32 rows, 27 in tiles of 64.
+template <int WR, int WC, int TC>
 struct DownShape {
     static_assert(WR * WC == kLoraWaves, "waves");
-    static constexpr int BM = 32 * WR, BN = 16 * WC, NS = 4, kStage = (BM + BN) * 128, kLds = NS * kStage;
-    // 1 KiB loads per wave and stage: of x's rows, of A's (WC = 1: two loads, by two waves each)
-    static constexpr int NLA = WR, NLB = WC > 1 ? WC / 2 : 1, NL = NLA + NLB;
+    static constexpr int BM = 32 * WR, BN = 16 * WC * TC, NS = 4, kStage = (BM + BN) * 128, kLds = NS * kStage;
+    // 1 KiB loads per wave and stage: of x's rows, of A's (16 ranks: two loads, by two waves each)
+    static constexpr int NLA = WR, NLB = BN > 16 ? BN / 32 : 1, NL = NLA + NLB;
 };
 
-template <int kIn, int WR, int WC>
+template <int kIn, int WR, int WC, int TC>
 __global__ __launch_bounds__(kLoraThreads) void k_lora_down(LoraAdd l, int parts)
 {
-    using S = DownShape<WR, WC>;
+    using S = DownShape<WR, WC, TC>;
     constexpr int kI = (S::BM + 63) / 64;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4;
@@ -172,7 +174,7 @@ __global__ __launch_bounds__(kLoraThreads) void k_lora_down(LoraAdd l, int parts
         cx[k] = c0 + ((lane & 7) ^ swz(q));
         x[k] = l.x + (m0 + q < l.M ? m0 + q : l.M - 1) * l.x_stride + (int64_t)cx[k] * 16;
     }
-    auto load_of = [&](int k) { return WC > 1 ? wave * S::NLB + k : wave & 1; };
+    auto load_of = [&](int k) { return S::BN > 16 ? wave * S::NLB + k : wave & 1; };
     each_adapter(id, 0, 1, [&](int cur) {
         const uint8_t* a[S::NLB];
 #pragma unroll
@@ -191,7 +193,9 @@ __global__ __launch_bounds__(kLoraThreads) void k_lora_down(LoraAdd l, int parts
             for (int k = 0; k < S::NLB; ++k)
                 g2lds16(ca[k] + 8 * s < c1 ? a[k] + s * 128 : reinterpret_cast<const uint8_t*>(&kZeros), to + S::BM * 128 + load_of(k) * 1024);
         };
-        v4f acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+        v4f acc[TC][2];
+#pragma unroll
+        for (int t = 0; t < TC; ++t) acc[t][0] = acc[t][1] = v4f{0, 0, 0, 0};
         __syncthreads();                                  // the last adapter's stages are read
 #pragma unroll
         for (int s = 0; s < S::NS - 1; ++s)
@@ -206,17 +210,25 @@ __global__ __launch_bounds__(kLoraThreads) void k_lora_down(LoraAdd l, int parts
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int c = ((2 * g + h) ^ swz(i)) << 4;
-                const v4i va = *reinterpret_cast<const v4i*>(at + (S::BM + 16 * wc + i) * 128 + c);
+                v4i vx[2];
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    acc[q] = mfma16x16<kIn>(va, *reinterpret_cast<const v4i*>(at + (32 * wr + 16 * q + i) * 128 + c), acc[q]);
+                for (int q = 0; q < 2; ++q) vx[q] = *reinterpret_cast<const v4i*>(at + (32 * wr + 16 * q + i) * 128 + c);
+#pragma unroll
+                for (int t = 0; t < TC; ++t) {
+                    const v4i va = *reinterpret_cast<const v4i*>(at + (S::BM + 16 * (TC * wc + t) + i) * 128 + c);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) acc[t][q] = mfma16x16<kIn>(va, vx[q], acc[t][q]);
+                }
             }
         }
-        const int q0 = r0 + 16 * wc + 4 * g;
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-            if (mine[q] == cur && q0 < l.r)
-                *reinterpret_cast<v4f*>(l.ws + ((int64_t)part * l.M + m0 + 32 * wr + 16 * q + i) * l.r + q0) = acc[q];
+        for (int t = 0; t < TC; ++t) {
+            const int q0 = r0 + 16 * (TC * wc + t) + 4 * g;
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                if (mine[q] == cur && q0 < l.r)
+                    *reinterpret_cast<v4f*>(l.ws + ((int64_t)part * l.M + m0 + 32 * wr + 16 * q + i) * l.r + q0) = acc[t][q];
+        }
     });
 }
 
@@ -336,24 +348,28 @@ __device__ __forceinline__ void store1(void* p, int64_t at, int type, float v)
         static_cast<_Float16*>(p)[at] = (_Float16)v;
 }
 
-// Few rows, or rows that are not aligned vectors.  A workgroup: 16 rows by cols columns (a multiple of 256), its
-// waves 64 columns at a time, as products of 16.  The parts are summed once, in LDS.  A wave's results go through
-// LDS, so that base and out are read and written a whole line at a time: kV values a lane (4 where one of the two
-// is fp32, else 8; 1: rows that are not aligned vectors).
-template <int kIn, int kP, int kKS, int kV>
-__global__ __launch_bounds__(kLoraThreads) void k_lora_up_few(LoraAdd l, int parts, int cols)
+// Few rows, or rows that are not aligned vectors.  A workgroup: 16 rows by cols columns, its waves 64 columns at a
+// time, as products of 16.  s is summed once, in LDS: of the parts (kRT = 0), or it is made here from all of K, in
+// kRT tiles of 16 ranks -- one launch and each workgroup reads A again, for a few rows (8.9 us against 11.1 of one
+// row, rank 16, 4096 x 4096).  A wave's results go through LDS, so that base and out are read and written a whole
+// line at a time: kV values a lane (8: both of x's type; 4: one is fp32; 1: rows that are not aligned vectors).
+template <int kIn, int kP, int kKS, int kV, int kRT, int kWaves>
+__global__ __launch_bounds__(64 * kWaves) void k_lora_up_few(LoraAdd l, int parts, int cols)
 {
     constexpr int kRanks = 32 * kKS, kRows = 16;
     constexpr int kB = kKS <= 2 ? 4 : kKS == 4 ? 2 : 1;   // products of 16 columns whose B is in registers at once
     __shared__ float sum[kRows][kRanks + 4];
-    __shared__ float tile[kLoraWaves][kRows][68];
+    __shared__ float tile[kWaves][kRows][68];
     const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4, wave = tid >> 6;
     const int64_t m0 = (int64_t)blockIdx.x * kRows;
     const int first = (int)blockIdx.y * cols + wave * 64, end = ((int)blockIdx.y + 1) * cols < l.N ? ((int)blockIdx.y + 1) * cols : l.N;
-    constexpr int kStep = 64 * kLoraWaves;
+    constexpr int kStep = 64 * kWaves;
     const int id[1] = {lane < kRows ? adapter_of(l, m0 + lane) : -1};
     const bool there = lane < kRows && m0 + lane < l.M;
-    const int base_size = dtype_bytes(l.base_type);
+    // of 16-bit types there is x's, where the rows are vectors: no branch between a block's loads
+    const int base_type = kV == 8 ? kIn : kV == 4 && l.base_type != kF32 ? kIn : l.base_type;
+    const int out_type = kV == 8 ? kIn : kV == 4 && l.out_type != kF32 ? kIn : l.out_type;
+    const int base_size = dtype_bytes(base_type);
     // out = base + z (null: 0) of the rows in `rows` in columns n0 .. n0 + 63: lane's columns from `col` on, of every
     // kPer-th row
     constexpr int kLanes = 64 / kV, kPer = kV, kIt = kV > 1 ? kRows / kPer : 1;
@@ -387,7 +403,7 @@ __global__ __launch_bounds__(kLoraThreads) void k_lora_up_few(LoraAdd l, int par
                 const int row = kPer * t + row0;
                 if (!(rows >> row & 1)) continue;
                 float v[kV] = {};
-                if (l.base) unpack<kV>(raw.v[t], l.base_type, v);
+                if (l.base) unpack<kV>(raw.v[t], base_type, v);
                 if (z) {
 #pragma unroll
                     for (int e = 0; e < kV; e += 4) {
@@ -396,7 +412,7 @@ __global__ __launch_bounds__(kLoraThreads) void k_lora_up_few(LoraAdd l, int par
                         for (int x = 0; x < 4; ++x) v[e + x] += add[x];
                     }
                 }
-                store_row<kV>(l.out, (m0 + row) * l.out_stride + n0 + col, l.out_type, v);
+                store_row<kV>(l.out, (m0 + row) * l.out_stride + n0 + col, out_type, v);
             }
         } else {
             const int n = n0 + lane;
@@ -430,27 +446,89 @@ __global__ __launch_bounds__(kLoraThreads) void k_lora_up_few(LoraAdd l, int par
             load_b(first);
             load_base(rows, first, raw);
         }
-        __syncthreads();                                  // the last adapter's sums are read
-        for (int e = tid * 4; e < kRows * kRanks; e += 4 * kLoraThreads) {
-            const int row = e / kRanks, q = e % kRanks;
-            v4f s = {0, 0, 0, 0};
-            if (q < l.r && (rows >> row & 1)) {
-                const float* w = l.ws + (m0 + row) * l.r + q;
-                const int64_t step = l.M * l.r;
-                int part = 0;
-                for (; part + 4 <= parts; part += 4, w += 4 * step) {
-                    const v4f w0 = *reinterpret_cast<const v4f*>(w), w1 = *reinterpret_cast<const v4f*>(w + step),
-                              w2 = *reinterpret_cast<const v4f*>(w + 2 * step), w3 = *reinterpret_cast<const v4f*>(w + 3 * step);
-                    s += w0;
-                    s += w1;
-                    s += w2;
-                    s += w3;
-                }
-                for (; part < parts; ++part, w += step) s += *reinterpret_cast<const v4f*>(w);
+        const float scale = l.scales ? l.scales[cur] : 1.0f;
+        if constexpr (kRT > 0) {
+            // the waves share K 64 values at a time: two of them a buffer, lane group g has chunks u + 2 g, + 1
+            const int chunks = l.K / 8;
+            constexpr int kUnit = 8 * kWaves;
+            const uint8_t* x = l.x + (m0 + i < l.M ? m0 + i : l.M - 1) * l.x_stride + 32 * g;
+            const uint8_t* a[kRT];
+            v4f acc[kRT];
+#pragma unroll
+            for (int t = 0; t < kRT; ++t) {
+                a[t] = l.a + ((int64_t)cur * l.r + (16 * t + i < l.r ? 16 * t + i : l.r - 1)) * l.K * 2 + 32 * g;
+                acc[t] = v4f{0, 0, 0, 0};
             }
-            *reinterpret_cast<v4f*>(&sum[row][q]) = s;
+            struct Frag {
+                v4i x[4], a[4][kRT];
+            };
+            auto load = [&](Frag& f, int u0) {
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const int u = u0 + (s >> 1) * kUnit;
+                    const bool in = u + 8 <= chunks || u + 2 * g + (s & 1) < chunks;
+                    const int64_t at = (int64_t)(u + (s & 1)) * 16;
+                    f.x[s] = in ? *reinterpret_cast<const v4i*>(x + at) : v4i{0, 0, 0, 0};
+#pragma unroll
+                    for (int t = 0; t < kRT; ++t) f.a[s][t] = in ? *reinterpret_cast<const v4i*>(a[t] + at) : v4i{0, 0, 0, 0};
+                }
+            };
+            auto multiply = [&](const Frag& f) {
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+#pragma unroll
+                    for (int t = 0; t < kRT; ++t) acc[t] = mfma16x16<kIn>(f.a[s][t], f.x[s], acc[t]);
+            };
+            Frag f0, f1;
+            const int u0 = wave * 8;
+            if (u0 < chunks) load(f0, u0);
+            if (u0 + 2 * kUnit < chunks) load(f1, u0 + 2 * kUnit);
+            for (int u = u0; u < chunks; u += 4 * kUnit) {
+                multiply(f0);
+                if (u + 4 * kUnit < chunks) load(f0, u + 4 * kUnit);
+                if (u + 2 * kUnit >= chunks) break;
+                multiply(f1);
+                if (u + 6 * kUnit < chunks) load(f1, u + 6 * kUnit);
+            }
+            __syncthreads();                              // the last adapter's results are out of the tiles
+            constexpr int kLine = 16 * kRT + 4;
+            float* red = &tile[0][0][0];                  // [waves][16][kLine]
+            static_assert(kLine <= 68, "inside the tiles");
+#pragma unroll
+            for (int t = 0; t < kRT; ++t) *reinterpret_cast<v4f*>(red + (wave * 16 + i) * kLine + 16 * t + 4 * g) = acc[t];
+            __syncthreads();
+            for (int e = tid; e < kRows * kRanks; e += 64 * kWaves) {
+                const int row = e / kRanks, q = e % kRanks;
+                float s = 0.0f;
+                if (q < l.r)
+#pragma unroll
+                    for (int w = 0; w < kWaves; ++w) s += red[(w * 16 + row) * kLine + q];
+                sum[row][q] = s;
+            }
+            __syncthreads();
+        } else {
+            __syncthreads();                              // the last adapter's sums are read
+            for (int e = tid * 4; e < kRows * kRanks; e += 4 * 64 * kWaves) {
+                const int row = e / kRanks, q = e % kRanks;
+                v4f s = {0, 0, 0, 0};
+                if (q < l.r && (rows >> row & 1)) {
+                    const float* w = l.ws + (m0 + row) * l.r + q;
+                    const int64_t step = l.M * l.r;
+                    int part = 0;
+                    for (; part + 4 <= parts; part += 4, w += 4 * step) {
+                        const v4f w0 = *reinterpret_cast<const v4f*>(w), w1 = *reinterpret_cast<const v4f*>(w + step),
+                                  w2 = *reinterpret_cast<const v4f*>(w + 2 * step), w3 = *reinterpret_cast<const v4f*>(w + 3 * step);
+                        s += w0;
+                        s += w1;
+                        s += w2;
+                        s += w3;
+                    }
+                    for (; part < parts; ++part, w += step) s += *reinterpret_cast<const v4f*>(w);
+                }
+                *reinterpret_cast<v4f*>(&sum[row][q]) = s;
+            }
+            __syncthreads();
         }
-        __syncthreads();
         float s[kKS][8];
 #pragma unroll
         for (int k = 0; k < kKS; ++k)
@@ -461,7 +539,6 @@ __global__ __launch_bounds__(kLoraThreads) void k_lora_up_few(LoraAdd l, int par
                 for (int z = 0; z < 4; ++z) s[k][e + z] = v[z];
             }
         const Parts<kIn, kP, kKS> p = split<kIn, kP, kKS>(s);
-        const float scale = l.scales ? l.scales[cur] : 1.0f;
         for (int n0 = first; n0 < end; n0 += kStep) {
 #pragma unroll
             for (int t0 = 0; t0 < 4; t0 += kB) {
@@ -710,17 +787,23 @@ hipError_t launch_up_ranks(const LoraAdd& l, int parts, int ways, hipStream_t st
             return base == 0 ? launch_up_ring<kIn, kP, kKS, 0, 2>(l, parts, st) : base == 2 ? launch_up_ring<kIn, kP, kKS, 2, 2>(l, parts, st)
                                                                                            : launch_up_ring<kIn, kP, kKS, 4, 2>(l, parts, st);
     }
+    const int v = !wide || (out == 2 && l.out_type != kIn) || (base == 2 && l.base_type != kIn) ? 1 : base == 4 || out == 4 ? 4 : 8;
     const unsigned tiles = nblk(l.M, 16);
     const int64_t blocks = nblk(l.N, 64 * kLoraWaves), want = (1024 + tiles - 1) / tiles;
-    const int cols = (int)((blocks + want - 1) / want) * 64 * kLoraWaves;
-    const dim3 grid(tiles, nblk(l.N, cols), ways);
-    auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kLoraThreads), 0, st, l, parts, cols); };
-    if (!wide)
-        launch(k_lora_up_few<kIn, kP, kKS, 1>);
-    else if (base == 4 || out == 4)
-        launch(k_lora_up_few<kIn, kP, kKS, 4>);
-    else
-        launch(k_lora_up_few<kIn, kP, kKS, 8>);
+    int cols = (int)((blocks + want - 1) / want) * 64 * kLoraWaves, threads = kLoraThreads;
+    auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(tiles, nblk(l.N, cols), ways), dim3(threads), 0, st, l, parts, cols); };
+    auto launch_v = [&](auto k1, auto k4, auto k8) { v == 1 ? launch(k1) : v == 4 ? launch(k4) : launch(k8); };
+    if (parts == 0) {
+        cols = threads = 64 * kOneWaves;
+        if constexpr (kKS == 1) {
+            if (l.r <= 16)
+                launch_v(k_lora_up_few<kIn, kP, 1, 1, 1, kOneWaves>, k_lora_up_few<kIn, kP, 1, 4, 1, kOneWaves>, k_lora_up_few<kIn, kP, 1, 8, 1, kOneWaves>);
+            else
+                launch_v(k_lora_up_few<kIn, kP, 1, 1, 2, kOneWaves>, k_lora_up_few<kIn, kP, 1, 4, 2, kOneWaves>, k_lora_up_few<kIn, kP, 1, 8, 2, kOneWaves>);
+        }
+        return hipSuccess;
+    }
+    launch_v(k_lora_up_few<kIn, kP, kKS, 1, 0, kLoraWaves>, k_lora_up_few<kIn, kP, kKS, 4, 0, kLoraWaves>, k_lora_up_few<kIn, kP, kKS, 8, 0, kLoraWaves>);
     return hipSuccess;
 }
 
@@ -731,29 +814,35 @@ hipError_t launch_up(const LoraAdd& l, int parts, int ways, hipStream_t st)
            : l.r <= 128 ? launch_up_ranks<kIn, kP, 4>(l, parts, ways, st) : launch_up_ranks<kIn, kP, 8>(l, parts, ways, st);
 }
 
-template <int kIn, int WR, int WC>
+template <int kIn, int WR, int WC, int TC>
 hipError_t launch_down(const LoraAdd& l, int parts, int ways, hipStream_t st)
 {
-    using S = DownShape<WR, WC>;
+    using S = DownShape<WR, WC, TC>;
     const unsigned y = (unsigned)parts * nblk(l.r, S::BN);
     if (lora_few(l.M)) {
-        hipLaunchKernelGGL((k_lora_down_few<kIn, WC>), dim3(nblk(l.M, 16), y, ways), dim3(kLoraThreads), 0, st, l, parts);
+        hipLaunchKernelGGL((k_lora_down_few<kIn, S::BN / 16>), dim3(nblk(l.M, 16), y, ways), dim3(kLoraThreads), 0, st, l, parts);
         return hipSuccess;
     }
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_lora_down<kIn, WR, WC>), hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds);
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_lora_down<kIn, WR, WC, TC>), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                             S::kLds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_lora_down<kIn, WR, WC>), dim3(nblk(l.M, S::BM), y), dim3(kLoraThreads), S::kLds, st, l, parts);
+    hipLaunchKernelGGL((k_lora_down<kIn, WR, WC, TC>), dim3(nblk(l.M, S::BM), y), dim3(kLoraThreads), S::kLds, st, l, parts);
     return hipSuccess;
 }
 
 template <int kIn>
 hipError_t launch_typed(const LoraAdd& l, hipStream_t st)
 {
-    const int parts = lora_parts(l.M, l.K, l.r);
     // rows of a small batch mostly have an adapter each: its tiles' adapters go to workgroups of their own
     const int ways = l.M <= 512 ? (l.M < 16 ? (int)l.M : 16) : lora_few(l.M) ? 4 : 1;
-    const hipError_t e = lora_ranks(l.r) == 16 ? launch_down<kIn, 4, 1>(l, parts, ways, st) : lora_ranks(l.r) == 32 ? launch_down<kIn, 2, 2>(l, parts, ways, st)
-                                                                                                                    : launch_down<kIn, 1, 4>(l, parts, ways, st);
+    // One launch where its workgroups read A and x again for less than another launch takes (4096 x 4096, rank 16: 1 row
+    // 8.9 us against 11.1 of two, 16 rows of 16 adapters 13.0, 13.7, 64 rows 24, 17; 2048 x 2048: 64 rows 10.9, 13.3); its
+    // registers hold 32 ranks (of 64 31 us against 11 for one row).
+    const int64_t again = (int64_t)nblk(l.M, 16) * ways * nblk(l.N, 64 * kOneWaves) * (l.r + (l.M < 16 ? l.M : 16)) * l.K * 2;
+    const bool one = lora_few(l.M) && l.r <= 32 && again <= (int64_t)48 << 20;
+    const int parts = one ? 0 : lora_parts(l.M, l.K, l.r);
+    const hipError_t e = one ? hipSuccess : l.r <= 16 ? launch_down<kIn, 4, 1, 1>(l, parts, ways, st) : l.r <= 32 ? launch_down<kIn, 4, 1, 2>(l, parts, ways, st)
+                                                                                                               : launch_down<kIn, 2, 2, 2>(l, parts, ways, st);
     if (e != hipSuccess) return e;
     hipError_t e2;
     if constexpr (kIn == kBF16)
