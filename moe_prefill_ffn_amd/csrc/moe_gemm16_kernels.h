@@ -8,6 +8,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "moe_dtype.h"
@@ -557,7 +558,7 @@ int rounds_time(const Gemm16& g, int a_round)
 {
     // tiles as the groups have them on average: half a tile each is empty
     const int64_t some = g.M < g.G ? g.M : g.G, half = g.M / S::BM + g.G / 2;
-    const int64_t slots = g.bounds ? (half > some ? half : some) : (g.M + S::BM - 1) / S::BM;
+    const int64_t slots = g.bounds ? std::min(std::max(half, some), slots_of(g, S::BM)) : slots_of(g, S::BM);
     const int64_t tiles = slots * (int64_t)nblk(g.N, g.swiglu ? S::BN / 2 : S::BN), rest = tiles % kGrid<S>;
     const int64_t t = tiles / kGrid<S> * a_round + (rest == 0 ? 0 : rest <= kGrid<S> - 256 ? 43 : a_round);
     return (int)(t < INT32_MAX ? t : INT32_MAX);

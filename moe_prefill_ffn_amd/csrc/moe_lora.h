@@ -4,7 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "moe_layout.h"
+#include "moe_dtype.h"
 
 namespace moe {
 

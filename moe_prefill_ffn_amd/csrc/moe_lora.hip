@@ -595,7 +595,7 @@ struct UpShape {
     // which chunk of 16 bytes is in slot c of row n: 16 rows' same chunk lies in 16 distinct bank groups of 256 bytes
     static __device__ __forceinline__ int swap(int n) { return (kKS == 1 ? n >> 2 : kKS == 2 ? n >> 1 : n) & (kChunks < 16 ? kChunks - 1 : 15); }
 };
-constexpr int up_slots(int KS, int base_size) { return KS == 8 || (KS == 4 && base_size == 4) ? 3 : 4; }
+constexpr int up_slots(int KS, int base_size) { return KS == 8 && base_size == 4 ? 2 : KS == 8 || (KS == 4 && base_size == 4) ? 3 : 4; }
 // rows of the waves' results, padded against bank conflicts
 constexpr int up_out_row(int out_size) { return kUpCols * out_size + 16; }
 constexpr int up_lds(int KS, int base_size, int out_size)
@@ -757,6 +757,7 @@ template <int kIn, int kP, int kKS, int kBase, int kOut>
 hipError_t launch_up_ring(const LoraAdd& l, int parts, hipStream_t st)
 {
     constexpr int lds = up_lds(kKS, kBase, kOut);
+    static_assert(lds <= 163840, "a CU's LDS");
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_lora_up<kIn, kP, kKS, kBase, kOut>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;

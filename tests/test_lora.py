@@ -154,6 +154,36 @@ def test_lora(M, K, N, r, n, base_type, out_type, dtype):
 
 @gpu
 @pytest.mark.parametrize("dtype", HALF)
+@pytest.mark.parametrize("base_type,out_type", [("same", "same"), ("f32", "f32"), ("f32", "same"), (None, "f32"), (None, "same"), ("same", "f32"), ("other", "other")])
+@pytest.mark.parametrize("M,K,N,r,n", [(1025, 200, 136, 8, 4), (1300, 1000, 264, 16, 9), (1100, 72, 1000, 32, 30), (2050, 512, 72, 64, 5), (1200, 96, 400, 120, 3),
+                                       (1030, 264, 328, 200, 7), (1100, 1304, 136, 256, 2)])
+def test_many_rows(M, K, N, r, n, base_type, out_type, dtype):
+    """The kernels of more than 1024 rows, for each count of ranks that they hold at once and each size of base and out."""
+    g = gen(M + K + N + r)
+    other = torch.float16 if dtype == torch.bfloat16 else torch.bfloat16
+    types = {"same": dtype, "f32": torch.float32, "other": other}
+    x = torch.randn(M, K, generator=g).to(dtype)
+    a = (torch.randn(n, r, K, generator=g) / math.sqrt(K)).to(dtype).cuda()
+    b = (torch.randn(n, N, r, generator=g) / math.sqrt(r)).to(dtype).cuda()
+    scales = (0.5 + torch.rand(n, generator=g)).cuda()
+    base = torch.randn(M, N, generator=g).to(types[base_type]) if base_type else None
+    xd, _ = strided(x, 8)
+    bd = strided(base, 8)[0] if base_type else None
+    out, buf = strided(torch.zeros(M, N, dtype=types[out_type]), 8)
+    for kind in ("runs", "mixed", "wild", "none"):
+        ids = ids_of(kind, M, n, g).cuda()
+        out.fill_(77.0)
+        mp.moe_lora_add(xd, a, b, ids, bd, out, scales=scales)
+        check(out, xd, a, b, ids, bd, scales)
+        assert (buf[:, N:] == 77).all()
+        if base_type == out_type:                         # in place: the same bits
+            inner = bd.clone()
+            mp.moe_lora_add(xd, a, b, ids, inner, inner, scales=scales)
+            assert torch.equal(inner, out)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", HALF)
 @pytest.mark.parametrize("M", [1, 40, 1000])
 def test_in_place_and_by_default(M, dtype):
     g = gen(M)
