@@ -459,7 +459,7 @@ typedef struct moe_combine_args {
     const int32_t* pos;        /* device [n_tokens, top_k] */
     const void* base;          /* device [n_tokens, N], rows base_stride elements apart, or NULL; may be y */
     int64_t base_stride;       /* >= N */
-    void* y;                   /* device [n_tokens, N], rows y_stride elements apart */
+    void* y;                   /* device [n_tokens, N], rows y_stride elements apart; does not overlap d */
     int64_t y_stride;          /* >= N */
     int64_t n_tokens;          /* 0 (a no-op) .. 2^23 */
     int32_t N;                 /* 1..2^20 */
@@ -480,7 +480,8 @@ int moe_combine_rows(const moe_combine_args_t* a, void* stream);
  *   out[t, :] = base[t, :] + scales[i] * ((x[t, :] A_i^T) B_i^T),  i = adapters[t]
  *
  * A row whose adapter is outside [0, n_adapters) (-1: none) gets out = base.  Rows of an
- * adapter may stand anywhere.  x A_i^T is summed in fp32 and enters the second product with
+ * adapter may stand anywhere (above 1024 rows, runs of rows of one adapter are much the
+ * fastest).  x A_i^T is summed in fp32 and enters the second product with
  * 16 bits or more of it (22 or more for an fp32 out); the rest is fp32, rounded once.  An
  * infinity or a NaN in an adapter, or in a row of x, reaches the rows that use it only.
  * No handle, as the calls above; same bits for the same call.
@@ -496,7 +497,7 @@ typedef struct moe_lora_args {
     const float* scales;       /* device [n_adapters], NULL: 1 */
     const void* base;          /* device [M, N], rows base_stride elements apart, or NULL (0); may be out */
     int64_t base_stride;       /* >= N */
-    void* out;                 /* device [M, N], rows out_stride elements apart */
+    void* out;                 /* device [M, N], rows out_stride elements apart; overlaps neither x, a nor b */
     int64_t out_stride;        /* >= N */
     int64_t M;                 /* 0 (a no-op) .. 2^23 */
     int32_t N, K;              /* N in 1..2^20, K a multiple of 8 in 8..2^20 */

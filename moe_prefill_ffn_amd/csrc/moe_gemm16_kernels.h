@@ -121,9 +121,17 @@ struct Shape {
 __device__ const uint4 kZeros = {0, 0, 0, 0};
 
 // Persistent workgroups: each takes every so-many-th tile of its XCD's run (workgroups go
-// round-robin over the 8 XCDs), one after the other without a pause in its stages -- the last two
-// stages of a tile issue the first two of the next, whose pointers are made under the products,
-// and the epilogue's stores drain under them.  kTail: K ends inside a stage, or there is one alone.
+// round-robin over the 8 XCDs), one after the other without a pause in its stages -- the last NS
+// stages of a tile issue the first NS of the next, whose pointers are made under the products,
+// and the epilogue's stores drain under them.  kTail: K ends inside a stage, or has fewer than NS.
+//
+// What bounds it: large dense products the matrix cores and the loads' latency -- 8192 x 4096 x 4096, bf16, 217 to
+// 224 us or 1.25 PFLOP/s (a library product 217), the matrix cores busy 58% of the cycles: a fifth of a stage's
+// lines come from beyond the L2, and a 256 x 256 tile's two slots leave them one stage's time.  (Words a line read
+// ahead into the L2 cost 6 to 60%: more requests.)  Over groups memory -- gate/up of 1024 tokens over 128 experts
+// (805 MB of B) 159 to 170 us, 5 TB/s; down of 65536 rows in 256 groups (N = 4096, K = 1536; 4.0 GB, 4.9 by the L2's
+// misses) 1.2 ms, in 128 x 256 tiles through three slots (two slots of 256 x 256 1.38, and 1.36 with tiles numbered
+// across groups).
 template <class S, int kIn, int kT, bool kSwiglu, bool kTail>
 __global__ __launch_bounds__(64 * S::NW) void k_gemm16_tile(Gemm16 a, int n_tiles, int64_t n_slots)
 {
@@ -399,7 +407,8 @@ __global__ __launch_bounds__(64 * S::NW) void k_gemm16_tile(Gemm16 a, int n_tile
 // ----------------------------------------------------------- few-row kernel ---
 // Up to 16 kR rows of a group by 16 kN / NG columns (SwiGLU, NG = 2: 16 gate and 16 up rows of B) per
 // workgroup; its waves take every eighth 64 values of K, fed straight from memory, four such units' loads
-// out at a time, and add up through LDS in wave order.  What bounds it is B's bytes, read once.
+// out at a time, and add up through LDS in wave order.  What bounds it is B's bytes, read once: gate/up of one token,
+// 8 experts (N = 768, K = 2048, 50 MB) 13 us, 3.8 TB/s; one row of 4096 x 4096 7.7 us, 4.3 TB/s.
 constexpr int kFewWaves = 8;
 
 typedef float v4f __attribute__((ext_vector_type(4)));
@@ -568,8 +577,8 @@ template <int kIn, int kT, bool kSwiglu>
 hipError_t launch_shape(const Gemm16& g, hipStream_t st)
 {
     // the tiled kernel reaches a tile's rows, or all of A through the row table, by 32 bits of offset
-    const int64_t a_span = (g.rows || g.row_div > 1 ? g.a_rows : Tile256::BM) * g.a_stride, b_span = Tile256::BN * g.b_stride;
-    const bool far = a_span > (int64_t)UINT32_MAX || b_span > (int64_t)UINT32_MAX;
+    const int64_t a_span = g.rows || g.row_div > 1 ? g.a_rows : Tile256::BM;
+    const bool far = g.a_stride > (int64_t)UINT32_MAX / a_span || g.b_stride > (int64_t)UINT32_MAX / Tile256::BN;
     // Too few tiles to fill the chip, whose waves the few-row kernel has share K.  Groups of a row or two: gate/up of
     // 8 rows (N = 768, K = 2048) 13 us against 17 of 64 x 128 tiles, of 16 rows 20, 22, of 32 rows 43, 43; down of 16 rows
     // (N = 2048, K = 768) 13.5, 13.4.  One matrix 4096 x 4096: 1 row 7.7 us against 18 of 64 x 64, 16 rows 10, 18, 32
