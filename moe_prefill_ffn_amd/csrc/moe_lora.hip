@@ -583,13 +583,13 @@ __global__ __launch_bounds__(64 * kWaves) void k_lora_up_few(LoraAdd l, int part
 }
 
 // Many rows.  A workgroup: 64 rows, 16 of each of four waves, by cols columns (a multiple of 64), 64 at a time as a
-// stage in LDS: B's rows and base.  A fifth wave issues the stages' loads, NS - 1 ahead, straight into LDS, and alone
-// waits for them; the others' stores, which come back in order with a wave's loads, hold nothing up.  A wave adds its
+// stage in LDS: B's rows and base.  Four more waves issue the stages' loads, NS - 1 ahead, straight into LDS, and alone
+// wait for them (one wave for all loads took 20 to 80% longer); the others' stores, which come back in order with a wave's loads, hold nothing up.  A wave adds its
 // products to base, and writes 16 rows a line at a time through LDS.  8192 rows of rank 64 and 4096 columns, 128 MB of
 // base and out: 45 to 50 us, 2.7 TB/s, where a copy in the same pattern takes 27; what bounds it is a stage's chain
 // (barrier, LDS, products, LDS, stores), of which two workgroups a CU overlap two.  (Four waves that loaded for
 // themselves: 69 us with stores from the result registers, 59 a line at a time.)
-constexpr int kUpRows = 64, kUpCols = 64, kUpThreads = kLoraThreads + 64;
+constexpr int kUpRows = 64, kUpCols = 64, kUpLoaders = 4, kUpThreads = kLoraThreads + 64 * kUpLoaders;
 
 template <int kKS>
 struct UpShape {
@@ -613,7 +613,8 @@ __global__ __launch_bounds__(kUpThreads) void k_lora_up(LoraAdd l, int parts, in
 {
     using S = UpShape<kKS>;
     constexpr int NS = up_slots(kKS, kBase), kBaseRow = kUpCols * kBase, kStage = S::kB + kUpRows * kBaseRow;
-    constexpr int kLoadsB = S::kB / 1024, kLoadsBase = kUpRows * kBaseRow / 1024, NL = kLoadsB + kLoadsBase;
+    // 1 KiB loads a stage and loading wave
+    constexpr int kLoadsB = S::kB / 1024 / kUpLoaders, kLoadsBase = kUpRows * kBaseRow / 1024 / kUpLoaders, NL = kLoadsB + kLoadsBase;
     static_assert((NS - 2) * NL <= 63, "vmcnt");
     constexpr int kBaseChunks = kBaseRow / 16, kOutRow = up_out_row(kOut);
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -625,40 +626,36 @@ __global__ __launch_bounds__(kUpThreads) void k_lora_up(LoraAdd l, int parts, in
     auto base_swap = [](int row) { return kBase == 2 ? (row >> 1) & 7 : row & 15; };
     each_adapter(id, 0, 1, [&](int cur) {
         const uint64_t rows = __ballot(id[0] == cur);
-        if (wave == kLoraWaves) {
+        if (wave >= kLoraWaves) {
+            const int loader = wave - kLoraWaves;
             const uint32_t lds0 = lds_addr(lds);
             const uint8_t* b_at = l.b + ((int64_t)cur * l.N + first) * l.r * 2;
             const uint8_t* base_at = static_cast<const uint8_t*>(l.base) + (m0 * l.base_stride + first) * kBase;
             // What is not there (a column past the end, a rank past r, a row of another adapter) is read from what
             // is, and not used.  32 bits of offset: the host checked that 64 rows of base span less.
             const int one = __builtin_ctzll(rows);
-            uint32_t base_row[kLoadsBase > 0 ? kLoadsBase : 1];
-#pragma unroll
-            for (int k = 0; k < kLoadsBase; ++k) {
-                const int row = (k * 64 + lane) / (kBase ? kBaseChunks : 1);
-                base_row[k] = (uint32_t)((rows >> row & 1) ? row : one) * (uint32_t)(l.base_stride * kBase);
-            }
             auto issue = [&](int s) {
                 const uint32_t to = lds0 + s % NS * kStage;
                 const int last = end - 1 - first - s * kUpCols;          // the last column's place in the stage
                 const uint8_t* bs = b_at + (int64_t)s * kUpCols * l.r * 2;
-#pragma unroll 4                                          // all at once keeps too many addresses
-                for (int k = 0; k < kLoadsB; ++k) {
-                    const int at = k * 64 + lane, col = at / S::kChunks, c = at % S::kChunks ^ S::swap(col);
+#pragma unroll
+                for (int q = 0; q < kLoadsB; ++q) {
+                    const int k = loader * kLoadsB + q, at = k * 64 + lane, col = at / S::kChunks, c = at % S::kChunks ^ S::swap(col);
                     g2lds16_at(bs, (uint32_t)((col < last ? col : last) * l.r * 2 + (8 * c < l.r ? c : 0) * 16), to + k * 1024);
                 }
                 if constexpr (kBase) {
                     const uint8_t* from = base_at + s * kUpCols * kBase;
 #pragma unroll
-                    for (int k = 0; k < kLoadsBase; ++k) {
-                        const int at = k * 64 + lane, c = at % kBaseChunks ^ base_swap(at / kBaseChunks);
-                        g2lds16_at(from, base_row[k] + (c * (16 / kBase) <= last ? c : 0) * 16, to + S::kB + k * 1024);
+                    for (int q = 0; q < kLoadsBase; ++q) {
+                        const int k = loader * kLoadsBase + q, at = k * 64 + lane, row = at / kBaseChunks, c = at % kBaseChunks ^ base_swap(row);
+                        const uint32_t row_at = (uint32_t)((rows >> row & 1) ? row : one) * (uint32_t)(l.base_stride * kBase);
+                        g2lds16_at(from, row_at + (c * (16 / kBase) <= last ? c : 0) * 16, to + S::kB + k * 1024);
                     }
                 }
             };
-#pragma unroll
-            for (int s = 0; s < NS - 1; ++s)
-                if (s < n) issue(s);
+#pragma unroll 1
+            for (int s = 0; s < NS - 1 && s < n; ++s) issue(s);
+#pragma unroll 1
             for (int s = 0; s < n; ++s) {
                 if (s + NS - 1 <= n)                      // the loads of the NS - 2 stages behind it may be out
                     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((NS - 2) * NL) : "memory");
@@ -688,10 +685,10 @@ __global__ __launch_bounds__(kUpThreads) void k_lora_up(LoraAdd l, int parts, in
                 }
             }
             const Parts<kIn, kP, kKS> p = split<kIn, kP, kKS>(sums);
-            const float scale = l.scales ? l.scales[cur] : 1.0f;
+            const float factor = (l.scales ? l.scales[cur] : 1.0f) * p.back;     // p.back: a power of two
             uint8_t* out_rows = lds + NS * kStage + 16 * wave * kOutRow;
             for (int s = 0; s < n; ++s) {
-                // this wave's reads of the stage before are done; the fifth wave admits this one
+                // this wave's reads of the stage before are done; the loading waves admit this one
                 asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
                 const uint8_t* at = lds + s % NS * kStage;
 #pragma unroll
@@ -719,7 +716,7 @@ __global__ __launch_bounds__(kUpThreads) void k_lora_up(LoraAdd l, int parts, in
                         unpack<4>(raw, kBase == 4 ? (int)kF32 : kIn, v);
                     }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] += acc[e] * p.back * scale;
+                    for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(acc[e], factor, v[e]);
                     store_row<4>(out_rows + i * kOutRow, 16 * t + 4 * g, kOut == 4 ? (int)kF32 : kIn, v);
                 }
                 // within a wave LDS works in order; the compiler must not move across
@@ -737,7 +734,7 @@ __global__ __launch_bounds__(kUpThreads) void k_lora_up(LoraAdd l, int parts, in
         }
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // every wave has read the last stage
     });
-    if (l.out == l.base || wave == kLoraWaves) return;    // in place: rows of no adapter stay as they are
+    if (l.out == l.base || wave >= kLoraWaves) return;    // in place: rows of no adapter stay as they are
     const uint64_t none = __ballot(m0 + lane < l.M && id[0] < 0);
     constexpr int kV = 16 / (kOut > kBase ? kOut : kBase), kLanes = kUpCols / kV;
     for (int n0 = first; n0 < end; n0 += kUpCols) {
