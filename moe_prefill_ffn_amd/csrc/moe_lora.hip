@@ -586,7 +586,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_lora_up_few(LoraAdd l, int part
 // stage in LDS: B's rows and base.  Four more waves issue the stages' loads, NS - 1 ahead, straight into LDS, and alone
 // wait for them (one wave for all loads took 20 to 80% longer); the others' stores, which come back in order with a wave's loads, hold nothing up.  A wave adds its
 // products to base, and writes 16 rows a line at a time through LDS.  8192 rows of rank 64 and 4096 columns, 128 MB of
-// base and out: 45 to 50 us, 2.7 TB/s, where a copy in the same pattern takes 27; what bounds it is a stage's chain
+// base and out: 42 to 48 us, 2.8 TB/s, where a copy in the same pattern takes 27; what bounds it is a stage's chain
 // (barrier, LDS, products, LDS, stores), of which two workgroups a CU overlap two.  (Four waves that loaded for
 // themselves: 69 us with stores from the result registers, 59 a line at a time.)
 constexpr int kUpRows = 64, kUpCols = 64, kUpLoaders = 4, kUpThreads = kLoraThreads + 64 * kUpLoaders;
@@ -691,33 +691,47 @@ __global__ __launch_bounds__(kUpThreads) void k_lora_up(LoraAdd l, int parts, in
                 // this wave's reads of the stage before are done; the loading waves admit this one
                 asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
                 const uint8_t* at = lds + s % NS * kStage;
+                constexpr int kT = kKS <= 2 ? 4 : 1;      // products whose operands are read together
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const int col = 16 * t + i;
-                    v4f acc = {0, 0, 0, 0};
+                for (int t0 = 0; t0 < 4; t0 += kT) {
+                    v4i b[kT][kKS];
+                    uint4 raw[kT];
 #pragma unroll
-                    for (int k = 0; k < kKS; ++k) {
-                        v4i b = *reinterpret_cast<const v4i*>(at + col * S::kRow + (((4 * k + g) ^ S::swap(col)) << 4));
-                        if (32 * k + 8 * g >= l.r) b = v4i{0, 0, 0, 0};
+                    for (int t = 0; t < kT; ++t) {
+                        const int col = 16 * (t0 + t) + i;
 #pragma unroll
-                        for (int z = kP - 1; z >= 0; --z) acc = mfma16x16<kIn>(b, p.v[k][z], acc);
-                    }
-                    float v[4] = {};                      // columns 16 t + 4 g .. + 3 of the row
-                    if constexpr (kBase) {
-                        const int byte = (16 * t + 4 * g) * kBase;
-                        const uint8_t* from = at + S::kB + row * kBaseRow + (((byte >> 4) ^ base_swap(row)) << 4) + (byte & 15);
-                        uint4 raw;
-                        if constexpr (kBase == 4) {
-                            raw = *reinterpret_cast<const uint4*>(from);
-                        } else {
-                            const uint2 half = *reinterpret_cast<const uint2*>(from);
-                            raw = {half.x, half.y, 0, 0};
+                        for (int k = 0; k < kKS; ++k) {
+                            b[t][k] = *reinterpret_cast<const v4i*>(at + col * S::kRow + (((4 * k + g) ^ S::swap(col)) << 4));
+                            if (32 * k + 8 * g >= l.r) b[t][k] = v4i{0, 0, 0, 0};
                         }
-                        unpack<4>(raw, kBase == 4 ? (int)kF32 : kIn, v);
+                        if constexpr (kBase) {
+                            const int byte = (16 * (t0 + t) + 4 * g) * kBase;
+                            const uint8_t* from = at + S::kB + row * kBaseRow + (((byte >> 4) ^ base_swap(row)) << 4) + (byte & 15);
+                            if constexpr (kBase == 4) {
+                                raw[t] = *reinterpret_cast<const uint4*>(from);
+                            } else {
+                                const uint2 half = *reinterpret_cast<const uint2*>(from);
+                                raw[t] = {half.x, half.y, 0, 0};
+                            }
+                        }
                     }
+                    v4f acc[kT];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(acc[e], factor, v[e]);
-                    store_row<4>(out_rows + i * kOutRow, 16 * t + 4 * g, kOut == 4 ? (int)kF32 : kIn, v);
+                    for (int t = 0; t < kT; ++t) acc[t] = v4f{0, 0, 0, 0};
+#pragma unroll
+                    for (int k = 0; k < kKS; ++k)
+#pragma unroll
+                        for (int z = kP - 1; z >= 0; --z)
+#pragma unroll
+                            for (int t = 0; t < kT; ++t) acc[t] = mfma16x16<kIn>(b[t][k], p.v[k][z], acc[t]);
+#pragma unroll
+                    for (int t = 0; t < kT; ++t) {
+                        float v[4] = {};                  // columns 16 (t0 + t) + 4 g .. + 3 of the row
+                        if constexpr (kBase) unpack<4>(raw[t], kBase == 4 ? (int)kF32 : kIn, v);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(acc[t][e], factor, v[e]);
+                        store_row<4>(out_rows + i * kOutRow, 16 * (t0 + t) + 4 * g, kOut == 4 ? (int)kF32 : kIn, v);
+                    }
                 }
                 // within a wave LDS works in order; the compiler must not move across
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");

@@ -173,10 +173,10 @@ int main()
     return 0;
 }
 """
-# the kernels' threads: one launch of 512, or 256 and 256 (few rows), 256 and 320 (many)
+# the kernels' threads: one launch of 512, or 256 and 256 (few rows), 256 and 512 (many)
 LORA_RULE = [((1, 4096, 4096, 16, 0), [512]), ((1, 4096, 4096, 40, 0), [256, 256]), ((16, 4096, 4096, 16, 0), [512]), ((64, 4096, 4096, 16, 0), [256, 256]),
-             ((64, 2048, 2048, 16, 0), [512]), ((1024, 4096, 4096, 16, 0), [256, 256]), ((1025, 4096, 4096, 16, 0), [256, 320]), ((1025, 4096, 4095, 16, 0), [256, 256]),
-             ((8192, 4096, 4096, 64, 0), [256, 320]), ((8192, 4096, 4096, 256, 1), [256, 320]), ((8192, 64, 64, 8, 1), [256, 320])]
+             ((64, 2048, 2048, 16, 0), [512]), ((1024, 4096, 4096, 16, 0), [256, 256]), ((1025, 4096, 4096, 16, 0), [256, 512]), ((1025, 4096, 4095, 16, 0), [256, 256]),
+             ((8192, 4096, 4096, 64, 0), [256, 512]), ((8192, 4096, 4096, 256, 1), [256, 512]), ((8192, 64, 64, 8, 1), [256, 512])]
 
 
 def test_launches_of_the_adapters(tmp_path):
