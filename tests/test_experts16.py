@@ -176,6 +176,23 @@ def test_group_of_more_pairs_than_one_round_of_workgroups():
 
 
 @gpu
+@pytest.mark.parametrize("P", [100, 5000])
+def test_group_without_what_is_not_wanted(P):
+    """The C call with bounds alone, and with counts beside them."""
+    eidx = torch.randint(-1, 7, (P,), generator=gen(P)).int()
+    dev, bounds, counts = eidx.cuda(), torch.full((8,), -77, dtype=torch.int32, device="cuda"), torch.zeros(7, dtype=torch.int32, device="cuda")
+    ws = torch.empty(max(1, mp.moe_group_workspace_size(P, 7)), dtype=torch.uint8, device="cuda")
+    a = group_args(eidx=dev.data_ptr(), n_pairs=P, n_groups=7, bounds=bounds.data_ptr(), rows=None, pos=None, counts=counts.data_ptr(),
+                   workspace=ws.data_ptr(), workspace_bytes=ws.numel())
+    want = table(eidx, 7)
+    for c in (counts.data_ptr(), None):
+        a.counts = c
+        bounds.fill_(-77)
+        assert mp.lib().moe_group_rows(a, torch.cuda.current_stream().cuda_stream) == mp.MOE_OK
+        assert torch.equal(bounds.cpu(), want[0]) and torch.equal(counts.cpu(), want[3])
+
+
+@gpu
 @pytest.mark.parametrize("P", [300, 20000])
 def test_group_in_a_replayed_graph_and_on_two_streams(P):
     g, E = gen(P), 37

@@ -332,6 +332,50 @@ def test_beside_the_projections(M):
 
 
 @gpu
+@pytest.mark.parametrize("T", [3, 200, 1500])
+def test_a_captured_layer_with_adapters(T):
+    """Row table, gate/up, down, a shared expert whose second product carries adapters in place, the combine: one graph,
+    replayed on other inputs, routings and adapters between eager calls, against the eager run bit for bit."""
+    g = gen(T)
+    d, f, E, k, n, r = 128, 192, 9, 3, 5, 16
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    x, eidx, w = torch.empty(T, d, **bf), torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+    ids = torch.empty(T, dtype=torch.int32, device="cuda")
+    gu, dn = [(torch.randn(E + 1, *s, generator=g) / 16).to(**bf) for s in ((2 * f, d), (d, f))]
+    a, b = (torch.randn(n, r, f, generator=g) / 16).to(**bf), (torch.randn(n, d, r, generator=g) / 4).to(**bf)
+
+    def layer():
+        bounds, rows, pos = mp.moe_group_rows(eidx, E)
+        h = mp.moe_grouped_gemm(x, gu[:E], bounds=bounds, rows=rows, top_k=k, swiglu=True)
+        dm = mp.moe_grouped_gemm(h, dn[:E], bounds=bounds)
+        hs = mp.moe_grouped_gemm(x, gu[E], swiglu=True)
+        shared = mp.moe_grouped_gemm(hs, dn[E], dtype=torch.float32)
+        mp.moe_lora_add(hs, a, b, ids, shared, shared)
+        return mp.moe_combine_rows(dm, w, pos, base=shared)
+
+    def fill():
+        x.copy_(torch.randn(T, d, generator=g))
+        eidx.copy_(torch.rand(T, E, generator=g).topk(k, -1).indices.int())
+        eidx[T // 2] = -1
+        w.copy_(torch.rand(T, k, generator=g))
+        ids.copy_(torch.randint(-1, n, (T,), generator=g).int())
+
+    fill()
+    layer()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = layer()
+    for _ in range(4):
+        fill()
+        y.fill_(77.0)
+        graph.replay()
+        want = layer()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+
+
+@gpu
 def test_binding_refusals_on_the_device():
     x, a, b = [torch.zeros(*s, dtype=torch.bfloat16, device="cuda") for s in ((4, 64), (2, 16, 64), (2, 40, 16))]
     ids = torch.zeros(4, dtype=torch.int32, device="cuda")
