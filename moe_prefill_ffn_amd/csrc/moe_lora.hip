@@ -807,18 +807,19 @@ hipError_t launch_up_ranks(const LoraAdd& l, int parts, int ways, hipStream_t st
     const int64_t blocks = nblk(l.N, 64 * kLoraWaves), want = (1024 + tiles - 1) / tiles;
     int cols = (int)((blocks + want - 1) / want) * 64 * kLoraWaves, threads = kLoraThreads;
     auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(tiles, nblk(l.N, cols), ways), dim3(threads), 0, st, l, parts, cols); };
+    constexpr int k16 = kP == 3 ? 4 : 8;                  // three parts are of an fp32 out
     auto launch_v = [&](auto k1, auto k4, auto k8) { v == 1 ? launch(k1) : v == 4 ? launch(k4) : launch(k8); };
     if (parts == 0) {
         cols = threads = 64 * kOneWaves;
         if constexpr (kKS == 1) {
             if (l.r <= 16)
-                launch_v(k_lora_up_few<kIn, kP, 1, 1, 1, kOneWaves>, k_lora_up_few<kIn, kP, 1, 4, 1, kOneWaves>, k_lora_up_few<kIn, kP, 1, 8, 1, kOneWaves>);
+                launch_v(k_lora_up_few<kIn, kP, 1, 1, 1, kOneWaves>, k_lora_up_few<kIn, kP, 1, 4, 1, kOneWaves>, k_lora_up_few<kIn, kP, 1, k16, 1, kOneWaves>);
             else
-                launch_v(k_lora_up_few<kIn, kP, 1, 1, 2, kOneWaves>, k_lora_up_few<kIn, kP, 1, 4, 2, kOneWaves>, k_lora_up_few<kIn, kP, 1, 8, 2, kOneWaves>);
+                launch_v(k_lora_up_few<kIn, kP, 1, 1, 2, kOneWaves>, k_lora_up_few<kIn, kP, 1, 4, 2, kOneWaves>, k_lora_up_few<kIn, kP, 1, k16, 2, kOneWaves>);
         }
         return hipSuccess;
     }
-    launch_v(k_lora_up_few<kIn, kP, kKS, 1, 0, kLoraWaves>, k_lora_up_few<kIn, kP, kKS, 4, 0, kLoraWaves>, k_lora_up_few<kIn, kP, kKS, 8, 0, kLoraWaves>);
+    launch_v(k_lora_up_few<kIn, kP, kKS, 1, 0, kLoraWaves>, k_lora_up_few<kIn, kP, kKS, 4, 0, kLoraWaves>, k_lora_up_few<kIn, kP, kKS, k16, 0, kLoraWaves>);
     return hipSuccess;
 }
 
