@@ -457,7 +457,8 @@ typedef struct moe_combine_args {
     int64_t d_rows;            /* 0 .. 2^31 - 1 */
     const float* weights;      /* device [n_tokens, top_k] */
     const int32_t* pos;        /* device [n_tokens, top_k] */
-    const void* base;          /* device [n_tokens, N], rows base_stride elements apart, or NULL; may be y */
+    const void* base;          /* device [n_tokens, N], rows base_stride elements apart, or NULL; may be y with
+                                  y's type and stride, else does not overlap y */
     int64_t base_stride;       /* >= N */
     void* y;                   /* device [n_tokens, N], rows y_stride elements apart; does not overlap d */
     int64_t y_stride;          /* >= N */
@@ -495,7 +496,8 @@ typedef struct moe_lora_args {
     const void* b;             /* device [n_adapters, N, rank], 16-byte aligned */
     const int32_t* adapters;   /* device [M] */
     const float* scales;       /* device [n_adapters], NULL: 1 */
-    const void* base;          /* device [M, N], rows base_stride elements apart, or NULL (0); may be out */
+    const void* base;          /* device [M, N], rows base_stride elements apart, or NULL (0); may be out
+                                  with out's type and stride, else does not overlap out */
     int64_t base_stride;       /* >= N */
     void* out;                 /* device [M, N], rows out_stride elements apart; overlaps neither x, a nor b */
     int64_t out_stride;        /* >= N */

@@ -772,7 +772,7 @@ def moe_combine_rows(d: torch.Tensor, weights: torch.Tensor, pos: torch.Tensor, 
                      stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """y[t] = base[t] + sum_j weights[t, j] * d[pos[t, j]], summed in slot order in fp32, rounded once.
 
-    d [R, N], base [T, N] (None: 0; may be y) and y (or a new tensor of ``dtype``, by default d's type): fp32, bf16
+    d [R, N], base [T, N] (None: 0; may be y itself) and y (or a new tensor of ``dtype``, by default d's type): fp32, bf16
     or fp16 each, rows may be strided.  weights fp32, pos int32, [T, k]; a slot whose pos is outside [0, R)
     is left out."""
     index = _mx_device(d, "d")
@@ -816,7 +816,7 @@ def moe_lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapters: to
     [0, n) (-1) gets base[t].  Returns out.
 
     x [M, K], a [n, rank, K] and b [n, N, rank]: the same of bf16, fp16 (K and rank multiples of 8, rank up to
-    256); adapters int32 [M]; scales fp32 [n] (None: 1); base [M, N] (None: 0; may be out) and out (or a new
+    256); adapters int32 [M]; scales fp32 [n] (None: 1); base [M, N] (None: 0; may be out itself) and out (or a new
     tensor of ``dtype``, by default x's type): fp32, bf16 or fp16 each.  Rows of x, base and out may be
     strided.  workspace: device uint8 scratch of moe_lora_workspace_size() bytes that no other call in flight
     uses; without one the call takes it from torch's allocator, on ``stream``."""

@@ -706,6 +706,11 @@ void queue_prefetches(moe_prefill_t* h, int layer)
 bool dtype_ok(int t) { return t == MOE_F32 || t == MOE_BF16 || t == MOE_F16; }
 bool stride_ok(int64_t s, int64_t least) { return s >= least && s <= ((int64_t)1 << 40); }
 uint64_t addr(const void* p) { return reinterpret_cast<uintptr_t>(p); }
+// In place, a row's results lie where its own base was, and nowhere else: the same type, and the same stride.
+bool in_place_ok(const void* base, int base_type, int64_t base_stride, const void* out, int out_type, int64_t out_stride, int64_t rows)
+{
+    return base != out || !base || (base_type == out_type && (base_stride == out_stride || rows == 1));
+}
 static_assert(MOE_F32 == kF32 && MOE_BF16 == kBF16 && MOE_F16 == kF16, "one numbering");
 static_assert(MOE_DECODE_MAX_PAIRS == kDecodeMaxPairs, "one limit");
 
@@ -1348,6 +1353,8 @@ int moe_combine_rows(const moe_combine_args_t* in, void* stream)
             return fail(nullptr, MOE_EINVAL, "combine: d, weights, pos and y are required");
         if (!stride_ok(a.d_stride, a.N) || !stride_ok(a.y_stride, a.N) || (a.base && !stride_ok(a.base_stride, a.N)))
             return fail(nullptr, MOE_EINVAL, "combine: a row stride below N, or above 2^40");
+        if (!in_place_ok(a.base, a.base_dtype, a.base_stride, a.y, a.y_dtype, a.y_stride, a.n_tokens))
+            return fail(nullptr, MOE_EINVAL, "combine: base is y with another type or row stride");
         if (addr(a.d) % dtype_bytes(a.d_dtype) || addr(a.y) % dtype_bytes(a.y_dtype) ||
             (a.base && addr(a.base) % dtype_bytes(a.base_dtype)) || (addr(a.weights) | addr(a.pos)) % 4)
             return fail(nullptr, MOE_EINVAL, "combine: d, base, y, weights and pos must be aligned to their elements");
@@ -1425,6 +1432,8 @@ int moe_lora_add(const moe_lora_args_t* in, void* stream)
             return fail(nullptr, MOE_EINVAL, "lora: x, a, b, adapters, out and workspace are required");
         if (!stride_ok(a.x_stride, a.K) || !stride_ok(a.out_stride, a.N) || (a.base && !stride_ok(a.base_stride, a.N)))
             return fail(nullptr, MOE_EINVAL, "lora: a row stride below the row's length, or above 2^40");
+        if (!in_place_ok(a.base, a.base_dtype, a.base_stride, a.out, a.out_dtype, a.out_stride, a.M))
+            return fail(nullptr, MOE_EINVAL, "lora: base is out with another type or row stride");
         if ((addr(a.x) | addr(a.a) | addr(a.b) | (uint64_t)(a.x_stride * 2)) % 16)
             return fail(nullptr, MOE_EINVAL, "lora: the rows of x, and a and b, must be 16-byte aligned");
         if (addr(a.out) % dtype_bytes(a.out_dtype) || (a.base && addr(a.base) % dtype_bytes(a.base_dtype)) ||
