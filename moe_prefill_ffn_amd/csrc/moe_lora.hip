@@ -203,10 +203,11 @@ __global__ __launch_bounds__(kLoraThreads) void k_lora_down(LoraAdd l, int parts
         for (int s = 0; s < S::NS - 1; ++s)
             if (s < n) issue(s);
         for (int s = 0; s < n; ++s) {
+            // this wave's reads of the stage before are done, by its own wait and not by where the compiler put one
             if (s + S::NS - 1 <= n)                       // the loads of the NS - 2 stages behind it may be out
-                asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((S::NS - 2) * S::NL) : "memory");
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S::NS - 2) * S::NL) : "memory");
             else
-                asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
             if (s + S::NS - 1 < n) issue(s + S::NS - 1);  // into the slot that every wave has read
             const uint8_t* at = lds + (s & 3) * S::kStage;
 #pragma unroll
@@ -658,9 +659,9 @@ __global__ __launch_bounds__(kUpThreads) void k_lora_up(LoraAdd l, int parts, in
 #pragma unroll 1
             for (int s = 0; s < n; ++s) {
                 if (s + NS - 1 <= n)                      // the loads of the NS - 2 stages behind it may be out
-                    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((NS - 2) * NL) : "memory");
+                    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NS - 2) * NL) : "memory");
                 else
-                    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+                    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
                 if (s + NS - 1 < n) issue(s + NS - 1);    // into the slot that every wave has read
             }
         } else {
