@@ -424,17 +424,17 @@ __device__ __forceinline__ v4f mfma16x16(v4i w, v4i x, v4f c)
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, w), __builtin_bit_cast(v8h, x), c, 0, 0, 0);
 }
 
-// kR row tiles; kN tiles of 16 rows of B (SwiGLU: half of them gate, half up)
+// kR row tiles; kN tiles of 16 rows of B (SwiGLU: half of them gate, half up); from tile x0 and column tile y0 on
 template <int kIn, int kT, bool kSwiglu, int kR, int kN>
-__global__ __launch_bounds__(64 * kFewWaves) void k_gemm16_few(Gemm16 a)
+__global__ __launch_bounds__(64 * kFewWaves) void k_gemm16_few(Gemm16 a, int64_t x0, int y0)
 {
     constexpr int BM = 16 * kR, kCols = kSwiglu ? 8 * kN : 16 * kN;
     __shared__ float red[kFewWaves][BM][16 * kN + 4];
-    const Rows t = rows_of_tile<BM>(a, blockIdx.x);
+    const Rows t = rows_of_tile<BM>(a, x0 + blockIdx.x);
     if (t.m0 >= t.m1) return;                             // uniform
     const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int chunks = a.K / 8, n0 = (int)blockIdx.y * kCols;
+    const int chunks = a.K / 8, n0 = (y0 + (int)blockIdx.y) * kCols;
     const uint8_t* x[kR];
     const uint8_t* w[kN];
 #pragma unroll
@@ -554,8 +554,13 @@ hipError_t launch_tile(const Gemm16& g, hipStream_t st)
 template <int kIn, int kT, bool kSwiglu, int kR, int kN>
 hipError_t launch_few(const Gemm16& g, hipStream_t st)
 {
-    hipLaunchKernelGGL((k_gemm16_few<kIn, kT, kSwiglu, kR, kN>), dim3((unsigned)slots_of(g, 16 * kR), nblk(g.N, (kSwiglu ? 8 : 16) * kN)),
-                       dim3(64 * kFewWaves), 0, st, g);
+    // A launch takes less than 2^32 threads along x and 65536 workgroups along y: more rows or columns take several.
+    constexpr int64_t kMostX = 1 << 22, kMostY = 32768;
+    const int64_t xs = slots_of(g, 16 * kR), ys = nblk(g.N, (kSwiglu ? 8 : 16) * kN);
+    for (int64_t x0 = 0; x0 < xs; x0 += kMostX)
+        for (int64_t y0 = 0; y0 < ys; y0 += kMostY)
+            hipLaunchKernelGGL((k_gemm16_few<kIn, kT, kSwiglu, kR, kN>), dim3((unsigned)std::min(xs - x0, kMostX), (unsigned)std::min(ys - y0, kMostY)),
+                               dim3(64 * kFewWaves), 0, st, g, x0, (int)y0);
     return hipGetLastError();
 }
 
