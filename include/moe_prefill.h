@@ -417,6 +417,8 @@ int moe_group_rows(const moe_group_args_t* a, void* stream);
  * values of them included; rows in no group are left as they were.  Infinities and
  * NaN go the way of the sum that they enter and reach no other element.  Another row
  * count may take another order of the sum over K.
+ * Slow for many rows (about ten times): rows of B, or of A without a table, more than 16 MB
+ * apart, and a table over 64 GiB of A or more.
  */
 typedef struct moe_grouped_gemm_args {
     uint32_t struct_size;

@@ -123,7 +123,8 @@ __device__ const uint4 kZeros = {0, 0, 0, 0};
 // Persistent workgroups: each takes every so-many-th tile of its XCD's run (workgroups go
 // round-robin over the 8 XCDs), one after the other without a pause in its stages -- the last NS
 // stages of a tile issue the first NS of the next, whose pointers are made under the products,
-// and the epilogue's stores drain under them.  kTail: K ends inside a stage, or has fewer than NS.
+// and the epilogue's stores drain under them.  kTail: K ends inside a stage, or has fewer than NS; also for a table over
+// 4 GiB of A or more.
 //
 // What bounds it: large dense products the matrix cores and the loads' latency -- 8192 x 4096 x 4096, bf16, 217 to
 // 224 us or 1.25 PFLOP/s (a library product 217), the matrix cores busy 58% of the cycles: a fifth of a stage's
@@ -149,8 +150,9 @@ __global__ __launch_bounds__(64 * S::NW) void k_gemm16_tile(Gemm16 a, int n_tile
     ListedTile* s_list = reinterpret_cast<ListedTile*>(lds + S::kListOff);
     const uint32_t lds0 = lds_addr(lds);
 
-    // A base per operand and tile, an offset per lane and load.  32 bits of offset: the host checked
-    // that a tile's rows, or all of A where a table names them, span less.
+    // A base per operand and tile, an offset per lane and load, 32 bits of bytes, or of 16 bytes with kTail: the
+    // host checked that a tile's rows, or all of A where a table names them, span less.
+    constexpr int kUnit = kTail ? 16 : 1;
     const uint8_t* a_at;
     const uint8_t* b_at;
     uint32_t dofs[S::NL];
@@ -160,13 +162,14 @@ __global__ __launch_bounds__(64 * S::NW) void k_gemm16_tile(Gemm16 a, int n_tile
 
     // row q of tile t's rows of A, relative to a_at's row: from the row table (indices in
     // s_rows[buf]) relative to A, else to the tile's first
-    const bool by_table = a.rows != nullptr || a.row_div > 1;
+    const bool in_order = !a.rows && a.row_div == 1;
+    auto first_of = [&](const ListedTile& t) { return a.rows ? 0 : in_order ? t.m0 : t.m0 / a.row_div; };
     auto a_ofs = [&](const ListedTile& t, int buf, int q) -> uint32_t {
         const int last = t.m1 - 1 - t.m0, at = q < last ? q : last;
-        if (!by_table) return (uint32_t)at;
+        if (in_order) return (uint32_t)at;
         int r = a.rows ? s_rows[buf * S::BM + at] : t.m0 + at;
         if (a.row_div > 1) r /= a.row_div;
-        return (uint32_t)(r < 0 ? 0 : (r >= a.a_rows ? (int)(a.a_rows - 1) : r));
+        return (uint32_t)((r < 0 ? 0 : (r >= a.a_rows ? (int)(a.a_rows - 1) : r)) - first_of(t));
     };
     // row q of its rows of B, relative to the tile's first (SwiGLU: 32 gate rows and their 32 up
     // rows in turn, the up rows relative to the first up row)
@@ -176,14 +179,14 @@ __global__ __launch_bounds__(64 * S::NW) void k_gemm16_tile(Gemm16 a, int n_tile
     };
     const int64_t up = kSwiglu ? (int64_t)a.N * a.b_stride : 0;     // bytes from a gate row to its up row
     auto point_data = [&](const ListedTile& t, int buf) {
-        a_at = a.a + (by_table ? 0 : t.m0) * a.a_stride;
+        a_at = a.a + first_of(t) * a.a_stride;
         b_at = a.b + t.g * a.b_group + (int64_t)(t.nt * kOutCols) * a.b_stride;
 #pragma unroll
         for (int l = 0; l < S::NL; ++l) {
             const bool is_a = l < S::NLA;
             const int q = (is_a ? wave * S::NLA + l : wave * S::NLB + l - S::NLA) * 8 + (lane >> 3);
-            dofs[l] = is_a ? a_ofs(t, buf, q) * (uint32_t)a.a_stride : b_ofs(t, q) * (uint32_t)a.b_stride;
-            dofs[l] += ((lane & 7) ^ swz(q)) * 16;
+            dofs[l] = is_a ? a_ofs(t, buf, q) * (uint32_t)(a.a_stride / kUnit) : b_ofs(t, q) * (uint32_t)(a.b_stride / kUnit);
+            dofs[l] += ((lane & 7) ^ swz(q)) * (16 / kUnit);
         }
     };
     // Stages go through the slots in turn, through a list's tiles.
@@ -196,7 +199,7 @@ __global__ __launch_bounds__(64 * S::NW) void k_gemm16_tile(Gemm16 a, int n_tile
             g2lds16_at(base, dofs[l], to);
         } else {
             const int c = (lane & 7) ^ swz(ql * 8 + (lane >> 3));
-            g2lds16(c < chunks - s * 8 ? base + dofs[l] : reinterpret_cast<const uint8_t*>(&kZeros), to);
+            g2lds16(c < chunks - s * 8 ? base + (uint64_t)dofs[l] * kUnit : reinterpret_cast<const uint8_t*>(&kZeros), to);
         }
     };
     // the row indices of tile t into s_rows[buf] (past its end: the last one again)
@@ -548,7 +551,9 @@ hipError_t launch_kernel(const Gemm16& g, hipStream_t st)
 template <class S, int kIn, int kT, bool kSwiglu>
 hipError_t launch_tile(const Gemm16& g, hipStream_t st)
 {
-    return g.K % 64 || g.K < 64 * S::NS ? launch_kernel<S, kIn, kT, kSwiglu, true>(g, st) : launch_kernel<S, kIn, kT, kSwiglu, false>(g, st);
+    // a table over 4 GiB of A or more: offsets in 16 bytes, up to 64 GiB
+    const bool wide = g.rows && g.a_stride > (int64_t)UINT32_MAX / g.a_rows;
+    return wide || g.K % 64 || g.K < 64 * S::NS ? launch_kernel<S, kIn, kT, kSwiglu, true>(g, st) : launch_kernel<S, kIn, kT, kSwiglu, false>(g, st);
 }
 
 template <int kIn, int kT, bool kSwiglu, int kR, int kN>
@@ -581,9 +586,11 @@ int rounds_time(const Gemm16& g, int a_round)
 template <int kIn, int kT, bool kSwiglu>
 hipError_t launch_shape(const Gemm16& g, hipStream_t st)
 {
-    // the tiled kernel reaches a tile's rows, or all of A through the row table, by 32 bits of offset
-    const int64_t a_span = g.rows || g.row_div > 1 ? g.a_rows : Tile256::BM;
-    const bool far = g.a_stride > (int64_t)UINT32_MAX / a_span || g.b_stride > (int64_t)UINT32_MAX / Tile256::BN;
+    // The tiled kernel reaches a tile's rows by 32 bits of offset (of bytes: 256 rows at most 16 MB apart), all of A through the
+    // row table by 32 bits of 16 bytes (64 GiB; 8192 of 524,400 rows by 4096 x 4096, 260 us).  Beyond that the few-row kernel
+    // takes any number of rows, and B again for every 16 of them (8192 x 4096 x 4096: 2.7 ms against 0.25).
+    const bool far_a = g.rows ? g.a_stride / 16 > (int64_t)UINT32_MAX / g.a_rows : g.a_stride > (int64_t)UINT32_MAX / Tile256::BM;
+    const bool far = far_a || g.b_stride > (int64_t)UINT32_MAX / Tile256::BN;
     // Too few tiles to fill the chip, whose waves the few-row kernel has share K.  Groups of a row or two: gate/up of
     // 8 rows (N = 768, K = 2048) 13 us against 17 of 64 x 128 tiles, of 16 rows 20, 22, of 32 rows 43, 43; down of 16 rows
     // (N = 2048, K = 768) 13.5, 13.4.  One matrix 4096 x 4096: 1 row 7.7 us against 18 of 64 x 64, 16 rows 10, 18, 32
