@@ -8,6 +8,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "moe_dtype.h"
 #include "moe_lora.h"
 #include "moe_tile.h"
@@ -307,6 +309,50 @@ __device__ __forceinline__ Parts<kIn, kP, kKS> split(const float (&s)[kKS][8])
     return p;
 }
 
+// The same product where B holds infinities or NaN, of which the sum of parts would make NaN (hi inf + lo inf, lo being 0 or
+// of the other sign): sign(s) times B's infinities and NaN, 0 in place of its numbers, plus the parts times B with a 1 of
+// the same sign in the place of those.  What the ones add is finite, and lost beside an infinity.  Taken where a
+// result of the short way is not finite; then the short way's order, so that finite results are its.
+template <int kIn, int kP, int kKS, class F>
+__device__ __forceinline__ v4f product_long(const Parts<kIn, kP, kKS>& p, F read)   // read(k): b[k]
+{
+    constexpr uint32_t two = 0x10001u, inf = kIn == kBF16 ? 0x7f80u : 0x7c00u, one = (kIn == kBF16 ? 0x3f80u : 0x3c00u) * two;
+    // all bits of a half where its magnitude and `add` reach 2^15
+    auto reach = [](uint32_t w, uint32_t add) {
+        const uint32_t m = (((w & 0x7fff7fffu) + add * 0x10001u) >> 15) & 0x10001u;
+        return (m << 16) - m;
+    };
+    v4f special = {0, 0, 0, 0}, z = {0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < kKS; ++k) {
+        const v4i b = read(k);
+        v4i alone, rest, sign;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint32_t w = (uint32_t)b[q], s = (uint32_t)p.v[k][0][q];
+            asm volatile("" : "+v"(w), "+v"(s));          // made here, not ahead of the loops in registers of their own
+            const uint32_t m = reach(w, 0x8000u - inf);
+            alone[q] = (int)(w & m);
+            rest[q] = (int)((w & ~m) | (m & ((w & 0x80008000u) | one)));
+            sign[q] = (int)((reach(s, 0x7fffu) & ((s & 0x80008000u) | one)) | (reach(s, 0x7fffu - inf) & 0x7fff7fffu));
+        }
+        special = mfma16x16<kIn>(alone, sign, special);
+#pragma unroll
+        for (int y = kP - 1; y >= 0; --y) z = mfma16x16<kIn>(rest, p.v[k][y], z);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z[e] += special[e];
+    return z;
+}
+// The larger of `most` and z's magnitudes; NaN stays.
+__device__ __forceinline__ float most_of(float most, const v4f& z)
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) most = __builtin_elementwise_maximum(most, __builtin_fabsf(z[e]));
+    return most;
+}
+
 // n consecutive values, n * size <= 16 bytes, of a vector of that type; and to aligned memory.
 template <int n>
 __device__ __forceinline__ void unpack(const uint4& raw, int type, float (&v)[n])
@@ -435,13 +481,16 @@ __global__ __launch_bounds__(64 * kWaves) void k_lora_up_few(LoraAdd l, int part
     each_adapter(id, blockIdx.z, gridDim.z, [&](int cur) {
         const uint64_t rows = __ballot(id[0] == cur);
         v4i b[kB][kKS];
-        auto load_b = [&](int n0) {                       // of kB products' columns from n0 on
+        auto b_at = [&](int n0) {                         // of a product's columns from n0 on
+            return l.b + ((int64_t)cur * l.N + (n0 + i < l.N ? n0 + i : l.N - 1)) * l.r * 2 + 16 * g;
+        };
+        auto load_one = [&](const uint8_t* p, int k) { return 32 * k + 8 * g < l.r ? *reinterpret_cast<const v4i*>(p + 64 * k) : v4i{0, 0, 0, 0}; };
+        auto load_b = [&](int n0) {                       // of kB products
 #pragma unroll
             for (int t = 0; t < kB; ++t) {
-                const int n = n0 + 16 * t + i < l.N ? n0 + 16 * t + i : l.N - 1;
-                const uint8_t* p = l.b + ((int64_t)cur * l.N + n) * l.r * 2 + 16 * g;
+                const uint8_t* p = b_at(n0 + 16 * t);
 #pragma unroll
-                for (int k = 0; k < kKS; ++k) b[t][k] = 32 * k + 8 * g < l.r ? *reinterpret_cast<const v4i*>(p + 64 * k) : v4i{0, 0, 0, 0};
+                for (int k = 0; k < kKS; ++k) b[t][k] = load_one(p, k);
             }
         };
         Base raw;
@@ -542,7 +591,14 @@ __global__ __launch_bounds__(64 * kWaves) void k_lora_up_few(LoraAdd l, int part
                 for (int z = 0; z < 4; ++z) s[k][e + z] = v[z];
             }
         const Parts<kIn, kP, kKS> p = split<kIn, kP, kKS>(s);
+        auto put = [&](int t, const v4f& z) {
+            v4f v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = z[e] * p.back * scale;
+            *reinterpret_cast<v4f*>(&tile[wave][i][16 * t + 4 * g]) = v;
+        };
         for (int n0 = first; n0 < end; n0 += kStep) {
+            float most = 0.0f;
 #pragma unroll
             for (int t0 = 0; t0 < 4; t0 += kB) {
                 v4f acc[kB];
@@ -560,10 +616,15 @@ __global__ __launch_bounds__(64 * kWaves) void k_lora_up_few(LoraAdd l, int part
                     load_b(n0 + kStep);
 #pragma unroll
                 for (int t = 0; t < kB; ++t) {
-                    v4f v;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = acc[t][e] * p.back * scale;
-                    *reinterpret_cast<v4f*>(&tile[wave][i][16 * (t0 + t) + 4 * g]) = v;
+                    put(t0 + t, acc[t]);
+                    most = most_of(most, acc[t]);
+                }
+            }
+            if (__ballot(!(most < __builtin_inff()))) {   // seldom: B is read again
+#pragma unroll 1
+                for (int t = 0; t < 4; ++t) {
+                    const uint8_t* from = b_at(n0 + 16 * t);
+                    put(t, product_long(p, [&](int k) { return load_one(from, k); }));
                 }
             }
             // within a wave LDS works in order; the compiler must not move across
@@ -692,20 +753,18 @@ __global__ __launch_bounds__(kUpThreads) void k_lora_up(LoraAdd l, int parts, in
                 // this wave's reads of the stage before are done; the loading waves admit this one
                 asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
                 const uint8_t* at = lds + s % NS * kStage;
-                constexpr int kT = kKS <= 2 ? 4 : 1;      // products whose operands are read together
-#pragma unroll
-                for (int t0 = 0; t0 < 4; t0 += kT) {
-                    v4i b[kT][kKS];
+                auto read_b = [&](int t, int k) {         // of product t's 16 columns
+                    const int col = 16 * t + i;
+                    const v4i b = *reinterpret_cast<const v4i*>(at + col * S::kRow + (((4 * k + g) ^ S::swap(col)) << 4));
+                    return 32 * k + 8 * g < l.r ? b : v4i{0, 0, 0, 0};
+                };
+                // products t0 .. t0 + kT - 1 onto base, into the waves' rows
+                auto columns = [&](int t0, auto n_c, auto product) {
+                    constexpr int kT = decltype(n_c)::value;
                     uint4 raw[kT];
+                    if constexpr (kBase) {
 #pragma unroll
-                    for (int t = 0; t < kT; ++t) {
-                        const int col = 16 * (t0 + t) + i;
-#pragma unroll
-                        for (int k = 0; k < kKS; ++k) {
-                            b[t][k] = *reinterpret_cast<const v4i*>(at + col * S::kRow + (((4 * k + g) ^ S::swap(col)) << 4));
-                            if (32 * k + 8 * g >= l.r) b[t][k] = v4i{0, 0, 0, 0};
-                        }
-                        if constexpr (kBase) {
+                        for (int t = 0; t < kT; ++t) {
                             const int byte = (16 * (t0 + t) + 4 * g) * kBase;
                             const uint8_t* from = at + S::kB + row * kBaseRow + (((byte >> 4) ^ base_swap(row)) << 4) + (byte & 15);
                             if constexpr (kBase == 4) {
@@ -717,14 +776,7 @@ __global__ __launch_bounds__(kUpThreads) void k_lora_up(LoraAdd l, int parts, in
                         }
                     }
                     v4f acc[kT];
-#pragma unroll
-                    for (int t = 0; t < kT; ++t) acc[t] = v4f{0, 0, 0, 0};
-#pragma unroll
-                    for (int k = 0; k < kKS; ++k)
-#pragma unroll
-                        for (int z = kP - 1; z >= 0; --z)
-#pragma unroll
-                            for (int t = 0; t < kT; ++t) acc[t] = mfma16x16<kIn>(b[t][k], p.v[k][z], acc[t]);
+                    product(acc);
 #pragma unroll
                     for (int t = 0; t < kT; ++t) {
                         float v[4] = {};                  // columns 16 (t0 + t) + 4 g .. + 3 of the row
@@ -733,6 +785,33 @@ __global__ __launch_bounds__(kUpThreads) void k_lora_up(LoraAdd l, int parts, in
                         for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(acc[t][e], factor, v[e]);
                         store_row<4>(out_rows + i * kOutRow, 16 * (t0 + t) + 4 * g, kOut == 4 ? (int)kF32 : kIn, v);
                     }
+                };
+                constexpr int kT = kKS <= 2 ? 4 : 1;      // products whose operands are read together
+                float most = 0.0f;
+#pragma unroll
+                for (int t0 = 0; t0 < 4; t0 += kT) {
+                    v4i b[kT][kKS];
+#pragma unroll
+                    for (int t = 0; t < kT; ++t)
+#pragma unroll
+                        for (int k = 0; k < kKS; ++k) b[t][k] = read_b(t0 + t, k);
+                    columns(t0, std::integral_constant<int, kT>{}, [&](v4f(&acc)[kT]) {
+#pragma unroll
+                        for (int t = 0; t < kT; ++t) acc[t] = v4f{0, 0, 0, 0};
+#pragma unroll
+                        for (int k = 0; k < kKS; ++k)
+#pragma unroll
+                            for (int z = kP - 1; z >= 0; --z)
+#pragma unroll
+                                for (int t = 0; t < kT; ++t) acc[t] = mfma16x16<kIn>(b[t][k], p.v[k][z], acc[t]);
+#pragma unroll
+                        for (int t = 0; t < kT; ++t) most = most_of(most, acc[t]);
+                    });
+                }
+                if (__ballot(!(most < __builtin_inff()))) {          // seldom
+#pragma unroll 1
+                    for (int t = 0; t < 4; ++t)
+                        columns(t, std::integral_constant<int, 1>{}, [&](v4f(&acc)[1]) { acc[0] = product_long(p, [&](int k) { return read_b(t, k); }); });
                 }
                 // within a wave LDS works in order; the compiler must not move across
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
