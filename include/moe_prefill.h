@@ -484,10 +484,11 @@ int moe_combine_rows(const moe_combine_args_t* a, void* stream);
  *
  * A row whose adapter is outside [0, n_adapters) (-1: none) gets out = base.  Rows of an
  * adapter may stand anywhere (above 1024 rows, runs of rows of one adapter are much the
- * fastest).  x A_i^T is summed in fp32 and enters the second product with
- * 16 bits or more of it (22 or more for an fp32 out); the rest is fp32, rounded once.  An
- * infinity or a NaN in an adapter, or in a row of x, reaches the rows that use it only, with
- * the value that the formula gives (a call whose adapters hold some takes longer).
+ * fastest).  x A_i^T is summed in fp32 and enters the second product with 16 bits or more of it
+ * (22 or more for an fp32 out), however small it is beside the row's other sums; the rest is
+ * fp32, rounded once.  An infinity or a NaN in an adapter, or in a row of x, reaches the rows
+ * that use it only, with the value that the formula gives (a call whose adapters hold some
+ * takes longer).
  * No handle, as the calls above; same bits for the same call.
  */
 typedef struct moe_lora_args {

@@ -241,19 +241,31 @@ __global__ __launch_bounds__(kLoraThreads) void k_lora_down(LoraAdd l, int parts
 // s enters the matrix instruction as a sum of 16-bit parts, so that little of its 24 bits is lost: bf16
 // two parts, each the nearest to what the parts before it left (2^-16 of s lost at most), for fp32
 // results three (2^-24).  fp16: the row of s times the power of two that brings its largest value to
-// [2^14, 2^15), as two parts: 2^-22 of a value lost, or 2^-39 of the row's largest.
+// [2^14, 2^15), as two parts, the second, what the first left, times 2^12 and its products' sum times 2^-12: 2^-22 of a
+// value lost, or 2^-16 where the output has 16 bits anyway, if the value is within `width` (29, or 35) powers of two of the
+// largest.  A smaller one is multiplied by 2^width until it is, and belongs to the window of that number, whose product
+// product_long makes apart (of normal values some 2^-28, or 2^-34).  Sums of products of fp16 numbers span 100 powers of
+// two, which four windows hold.
+constexpr int fp16_width(bool out32) { return out32 ? 29 : 35; }
+constexpr float kSecond = 0x1p12f;                        // fp16: what the second part is multiplied by
+
 template <int kIn, int kP, int kKS>
 struct Parts {
     v4i v[kKS][kP];
     float back;               // what the results are multiplied by
+    uint32_t windows = 1;     // a bit for each that holds something in the wave (fp16), and the first
+    uint32_t window[kKS];     // 4 bits a value
+    int width;
 };
 
 template <int kIn, int kP, int kKS>
-__device__ __forceinline__ Parts<kIn, kP, kKS> split(const float (&s)[kKS][8])
+__device__ __forceinline__ Parts<kIn, kP, kKS> split(float (&s)[kKS][8], int width)
 {
     Parts<kIn, kP, kKS> p;
-    float to = 1.0f;
     p.back = 1.0f;
+    p.width = width;
+#pragma unroll
+    for (int k = 0; k < kKS; ++k) p.window[k] = 0;
     if constexpr (kIn == kF16) {
         float most = 0.0f;
 #pragma unroll
@@ -270,14 +282,39 @@ __device__ __forceinline__ Parts<kIn, kP, kKS> split(const float (&s)[kKS][8])
         }
         int e = (int)(__float_as_uint(most) >> 23) - 127; // floor(log2 most)
         e = e < -100 ? -100 : e;
-        to = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+        const float to = __uint_as_float((uint32_t)(127 + 14 - e) << 23), least = __uint_as_float((uint32_t)(127 + 15 - width) << 23);
         p.back = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+        bool small = false;
+#pragma unroll
+        for (int k = 0; k < kKS; ++k)
+#pragma unroll
+            for (int z = 0; z < 8; ++z) {
+                s[k][z] *= to;
+                small |= __builtin_fabsf(s[k][z]) < least && s[k][z] != 0.0f;
+            }
+        if (__ballot(small)) {
+            uint32_t mine = 1;
+#pragma unroll
+            for (int k = 0; k < kKS; ++k)
+#pragma unroll
+                for (int z = 0; z < 8; ++z) {
+                    const int down = 14 + 127 - (int)(__float_as_uint(s[k][z]) >> 23 & 255);      // below 0: infinity, NaN
+                    const int w = s[k][z] == 0.0f || down < width ? 0 : min(down / width, 112 / width);
+                    s[k][z] *= __uint_as_float((uint32_t)(127 + width * w) << 23);
+                    p.window[k] |= (uint32_t)w << (4 * z);
+                    mine |= 1u << w;
+                    asm volatile("" : "+v"(s[k][z]), "+v"(mine));    // one value after the other, not all in registers at once
+                }
+            p.windows = 0;
+#pragma unroll 1
+            for (int w = 0; w < 4; ++w) p.windows |= __ballot(mine >> w & 1) ? 1u << w : 0u;
+        }
     }
 #pragma unroll
     for (int k = 0; k < kKS; ++k) {
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
-            float rest[2] = {s[k][e] * to, s[k][e + 1] * to};
+            float rest[2] = {s[k][e], s[k][e + 1]};
 #pragma unroll
             for (int q = 0; q < kP; ++q) {
                 uint32_t w;
@@ -302,19 +339,48 @@ __device__ __forceinline__ Parts<kIn, kP, kKS> split(const float (&s)[kKS][8])
                 p.v[k][q][e / 2] = (int)w;
 #pragma unroll
                 for (int z = 0; z < 2; ++z)               // an infinity or a NaN is in the first part alone
-                    rest[z] = __builtin_fabsf(at[z]) < __builtin_inff() ? rest[z] - at[z] : 0.0f;
+                    rest[z] = __builtin_fabsf(at[z]) < __builtin_inff() ? (rest[z] - at[z]) * (kIn == kF16 ? kSecond : 1.0f) : 0.0f;
             }
         }
     }
     return p;
 }
 
-// The same product where B holds infinities or NaN, of which the sum of parts would make NaN (hi inf + lo inf, lo being 0 or
-// of the other sign): sign(s) times B's infinities and NaN, 0 in place of its numbers, plus the parts times B with a 1 of
-// the same sign in the place of those.  What the ones add is finite, and lost beside an infinity.  Taken where a
-// result of the short way is not finite; then the short way's order, so that finite results are its.
+// acc = B s of kT tiles, the smaller parts first: of each step of ranks (bf16), or of all ranks (fp16).
+template <int kIn, int kP, int kKS, int kT>
+__device__ __forceinline__ void product(const v4i (*b)[kKS], const Parts<kIn, kP, kKS>& p, v4f* acc)
+{
+#pragma unroll
+    for (int t = 0; t < kT; ++t) acc[t] = v4f{0, 0, 0, 0};
+    if constexpr (kIn == kBF16) {
+#pragma unroll
+        for (int k = 0; k < kKS; ++k)
+#pragma unroll
+            for (int z = kP - 1; z >= 0; --z)
+#pragma unroll
+                for (int t = 0; t < kT; ++t) acc[t] = mfma16x16<kIn>(b[t][k], p.v[k][z], acc[t]);
+    } else {
+        static_assert(kP == 2, "parts of fp16");
+#pragma unroll
+        for (int z = 1; z >= 0; --z) {
+#pragma unroll
+            for (int k = 0; k < kKS; ++k)
+#pragma unroll
+                for (int t = 0; t < kT; ++t) acc[t] = mfma16x16<kIn>(b[t][k], p.v[k][z], acc[t]);
+#pragma unroll
+            for (int t = 0; t < (z ? kT : 0); ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[t][e] *= 1.0f / kSecond;
+        }
+    }
+}
+
+// The same product the long way, taken where a sum of the short way is not finite or s has several windows: each window's
+// product by itself, the smallest first.  Where B holds infinities or NaN the sum of parts would make NaN (hi inf + lo inf,
+// lo being 0 or of the other sign), so: sign(s) times those, 0 in place of B's numbers, plus the parts times B with a 1 of the
+// same sign in their place.  What the ones add is finite, and lost beside an infinity.  read(k): b[k]; odd: B may hold some.
 template <int kIn, int kP, int kKS, class F>
-__device__ __forceinline__ v4f product_long(const Parts<kIn, kP, kKS>& p, F read)   // read(k): b[k]
+__device__ __forceinline__ v4f product_long(const Parts<kIn, kP, kKS>& p, bool odd, F read)
 {
     constexpr uint32_t two = 0x10001u, inf = kIn == kBF16 ? 0x7f80u : 0x7c00u, one = (kIn == kBF16 ? 0x3f80u : 0x3c00u) * two;
     // all bits of a half where its magnitude and `add` reach 2^15
@@ -322,27 +388,56 @@ __device__ __forceinline__ v4f product_long(const Parts<kIn, kP, kKS>& p, F read
         const uint32_t m = (((w & 0x7fff7fffu) + add * 0x10001u) >> 15) & 0x10001u;
         return (m << 16) - m;
     };
-    v4f special = {0, 0, 0, 0}, z = {0, 0, 0, 0};
+    // what is made of a value is made here, not ahead of the loops in registers of its own
+    auto here = [](uint32_t w) {
+        asm volatile("" : "+v"(w));
+        return w;
+    };
+    v4f z = {0, 0, 0, 0};
 #pragma unroll
     for (int k = 0; k < kKS; ++k) {
+        if (!odd) break;                                  // uniform
         const v4i b = read(k);
-        v4i alone, rest, sign;
+        v4i alone, sign;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            uint32_t w = (uint32_t)b[q], s = (uint32_t)p.v[k][0][q];
-            asm volatile("" : "+v"(w), "+v"(s));          // made here, not ahead of the loops in registers of their own
-            const uint32_t m = reach(w, 0x8000u - inf);
-            alone[q] = (int)(w & m);
-            rest[q] = (int)((w & ~m) | (m & ((w & 0x80008000u) | one)));
+            const uint32_t w = here((uint32_t)b[q]), s = here((uint32_t)p.v[k][0][q]);
+            alone[q] = (int)(w & reach(w, 0x8000u - inf));
             sign[q] = (int)((reach(s, 0x7fffu) & ((s & 0x80008000u) | one)) | (reach(s, 0x7fffu - inf) & 0x7fff7fffu));
         }
-        special = mfma16x16<kIn>(alone, sign, special);
-#pragma unroll
-        for (int y = kP - 1; y >= 0; --y) z = mfma16x16<kIn>(rest, p.v[k][y], z);
+        z = mfma16x16<kIn>(alone, sign, z);
         __builtin_amdgcn_sched_barrier(0);
     }
+#pragma unroll 1
+    for (uint32_t left = p.windows; left;) {
+        const int win = 31 - __builtin_clz(left);
+        left &= ~(1u << win);
+        v4f sum[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};        // of fp16's second parts, of the rest
 #pragma unroll
-    for (int e = 0; e < 4; ++e) z[e] += special[e];
+        for (int k = 0; k < kKS; ++k) {
+            asm volatile("" ::: "memory");                // b[k] is read here, for each window again
+            const v4i b = read(k);
+            v4i rest, part[kP];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t w = here((uint32_t)b[q]), m = reach(w, 0x8000u - inf);
+                rest[q] = (int)((w & ~m) | (m & ((w & 0x80008000u) | one)));
+                uint32_t in = ~0u;
+                if constexpr (kIn == kF16) {
+                    const uint32_t of = here(p.window[k]) >> (8 * q);
+                    in = ((of & 15) == (uint32_t)win ? 0xffffu : 0u) | ((of >> 4 & 15) == (uint32_t)win ? 0xffff0000u : 0u);
+                }
+#pragma unroll
+                for (int y = 0; y < kP; ++y) part[y][q] = (int)((uint32_t)p.v[k][y][q] & in);
+            }
+#pragma unroll
+            for (int y = kP - 1; y >= 0; --y) sum[kIn == kBF16 || !y] = mfma16x16<kIn>(rest, part[y], sum[kIn == kBF16 || !y]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        const float back = __uint_as_float((uint32_t)(127 - p.width * win) << 23);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[e] = __builtin_fmaf(__builtin_fmaf(sum[0][e], 1.0f / kSecond, sum[1][e]), back, z[e]);
+    }
     return z;
 }
 // The larger of `most` and z's magnitudes; NaN stays.
@@ -402,8 +497,12 @@ __device__ __forceinline__ void store1(void* p, int64_t at, int type, float v)
 // kRT tiles of 16 ranks -- one launch and each workgroup reads A again, for a few rows (8.9 us against 11.1 of one
 // row, rank 16, 4096 x 4096).  A wave's results go through LDS, so that base and out are read and written a whole
 // line at a time: kV values a lane (8: both of x's type; 4: one is fp32; 1: rows that are not aligned vectors).
+// Waves a SIMD that the registers leave, where the compiler would go a little past them: 48 rows of rank 64, fp16, 19 us with
+// three and 23 with two; 1000 rows of rank 256 onto fp32 98 with two and 118 with one.
+constexpr int up_few_waves(int in, int KS, int V, int RT) { return in != kF16 || RT ? 1 : KS == 8 ? 2 : V == 8 ? 3 : 1; }
+
 template <int kIn, int kP, int kKS, int kV, int kRT, int kWaves>
-__global__ __launch_bounds__(64 * kWaves) void k_lora_up_few(LoraAdd l, int parts, int cols)
+__global__ __launch_bounds__(64 * kWaves, up_few_waves(kIn, kKS, kV, kRT)) void k_lora_up_few(LoraAdd l, int parts, int cols)
 {
     constexpr int kRanks = 32 * kKS, kRows = 16;
     constexpr int kB = kKS <= 2 ? 4 : kKS == 4 ? 2 : 1;   // products of 16 columns whose B is in registers at once
@@ -552,7 +651,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_lora_up_few(LoraAdd l, int part
             for (int e = tid; e < kRows * kRanks; e += 64 * kWaves) {
                 const int row = e / kRanks, q = e % kRanks;
                 float s = 0.0f;
-                if (q < l.r)
+                if (q < l.r && (rows >> row & 1))
 #pragma unroll
                     for (int w = 0; w < kWaves; ++w) s += red[(w * 16 + row) * kLine + q];
                 sum[row][q] = s;
@@ -590,7 +689,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_lora_up_few(LoraAdd l, int part
 #pragma unroll
                 for (int z = 0; z < 4; ++z) s[k][e + z] = v[z];
             }
-        const Parts<kIn, kP, kKS> p = split<kIn, kP, kKS>(s);
+        const Parts<kIn, kP, kKS> p = split<kIn, kP, kKS>(s, fp16_width(l.out_type == kF32));
         auto put = [&](int t, const v4f& z) {
             v4f v;
 #pragma unroll
@@ -604,11 +703,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_lora_up_few(LoraAdd l, int part
                 v4f acc[kB];
 #pragma unroll
                 for (int t = 0; t < kB; ++t) {
-                    acc[t] = v4f{0, 0, 0, 0};
-#pragma unroll
-                    for (int k = 0; k < kKS; ++k)
-#pragma unroll
-                        for (int z = kP - 1; z >= 0; --z) acc[t] = mfma16x16<kIn>(b[t][k], p.v[k][z], acc[t]);
+                    product<kIn, kP, kKS, 1>(&b[t], p, &acc[t]);
                 }
                 if (t0 + kB < 4)
                     load_b(n0 + 16 * (t0 + kB));
@@ -620,11 +715,12 @@ __global__ __launch_bounds__(64 * kWaves) void k_lora_up_few(LoraAdd l, int part
                     most = most_of(most, acc[t]);
                 }
             }
-            if (__ballot(!(most < __builtin_inff()))) {   // seldom: B is read again
+            const bool odd = __ballot(!(most < __builtin_inff())) != 0;
+            if (odd || p.windows > 1) {                   // seldom: B is read again
 #pragma unroll 1
                 for (int t = 0; t < 4; ++t) {
                     const uint8_t* from = b_at(n0 + 16 * t);
-                    put(t, product_long(p, [&](int k) { return load_one(from, k); }));
+                    put(t, product_long(p, odd, [&](int k) { return load_one(from, k); }));
                 }
             }
             // within a wave LDS works in order; the compiler must not move across
@@ -746,7 +842,7 @@ __global__ __launch_bounds__(kUpThreads) void k_lora_up(LoraAdd l, int parts, in
                     }
                 }
             }
-            const Parts<kIn, kP, kKS> p = split<kIn, kP, kKS>(sums);
+            const Parts<kIn, kP, kKS> p = split<kIn, kP, kKS>(sums, fp16_width(kOut == 4));
             const float factor = (l.scales ? l.scales[cur] : 1.0f) * p.back;     // p.back: a power of two
             uint8_t* out_rows = lds + NS * kStage + 16 * wave * kOutRow;
             for (int s = 0; s < n; ++s) {
@@ -796,22 +892,16 @@ __global__ __launch_bounds__(kUpThreads) void k_lora_up(LoraAdd l, int parts, in
 #pragma unroll
                         for (int k = 0; k < kKS; ++k) b[t][k] = read_b(t0 + t, k);
                     columns(t0, std::integral_constant<int, kT>{}, [&](v4f(&acc)[kT]) {
-#pragma unroll
-                        for (int t = 0; t < kT; ++t) acc[t] = v4f{0, 0, 0, 0};
-#pragma unroll
-                        for (int k = 0; k < kKS; ++k)
-#pragma unroll
-                            for (int z = kP - 1; z >= 0; --z)
-#pragma unroll
-                                for (int t = 0; t < kT; ++t) acc[t] = mfma16x16<kIn>(b[t][k], p.v[k][z], acc[t]);
+                        product<kIn, kP, kKS, kT>(b, p, acc);
 #pragma unroll
                         for (int t = 0; t < kT; ++t) most = most_of(most, acc[t]);
                     });
                 }
-                if (__ballot(!(most < __builtin_inff()))) {          // seldom
+                const bool odd = __ballot(!(most < __builtin_inff())) != 0;
+                if (odd || p.windows > 1) {               // seldom
 #pragma unroll 1
                     for (int t = 0; t < 4; ++t)
-                        columns(t, std::integral_constant<int, 1>{}, [&](v4f(&acc)[1]) { acc[0] = product_long(p, [&](int k) { return read_b(t, k); }); });
+                        columns(t, std::integral_constant<int, 1>{}, [&](v4f(&acc)[1]) { acc[0] = product_long(p, odd, [&](int k) { return read_b(t, k); }); });
                 }
                 // within a wave LDS works in order; the compiler must not move across
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
