@@ -13,15 +13,13 @@
 
 #include "moe_dtype.h"
 #include "moe_gemm16.h"
+#include "moe_mfma16.h"
 #include "moe_tile.h"
 #include "moe_tile_numbers.h"
 
 namespace moe {
 
 namespace {
-
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
 // The matrix instruction takes 8 values of K per lane half and operand.  Its first operand is the
 // weights, the second the activations, so a lane holds four consecutive output columns of one row
@@ -117,18 +115,17 @@ struct Shape {
     static constexpr int kLds = kListOff + kListMost * (int)sizeof(ListedTile);
 };
 
-// What a chunk past the end of K is loaded from.
-__device__ const uint4 kZeros = {0, 0, 0, 0};
-
 // Persistent workgroups: each takes every so-many-th tile of its XCD's run (workgroups go
 // round-robin over the 8 XCDs), one after the other without a pause in its stages -- the last NS
 // stages of a tile issue the first NS of the next, whose pointers are made under the products,
-// and the epilogue's stores drain under them.  kTail: K ends inside a stage, or has fewer than NS; also for a table over
-// 4 GiB of A or more.
+// and the epilogue's stores drain under them.  Not so 256 x 256 tiles, whose 512 registers a wave do not hold all that: 16 to
+// 27 are spilled, by type, and a tile's end reloads them behind everything that is out, the stores just made and the
+// next tile's loads too, some eight times.  kTail: K ends inside a stage, or has fewer than NS; also for a table over 4 GiB of
+// A or more.
 //
-// What bounds it: large dense products the matrix cores and the loads' latency -- 8192 x 4096 x 4096, bf16, 217 to
+// What bounds it: large dense products the matrix cores and the loads' latency -- 8192 x 4096 x 4096, bf16, 215 to
 // 224 us or 1.25 PFLOP/s (a library product 217), the matrix cores busy 58% of the cycles: a fifth of a stage's
-// lines come from beyond the L2, and a 256 x 256 tile's two slots leave them one stage's time.  (Words a line read
+// lines come from beyond the L2, a 256 x 256 tile's two slots leave them one stage's time, and its end waits as said.  (Words a line read
 // ahead into the L2 cost 6 to 60%: more requests.)  Over groups memory -- gate/up of 1024 tokens over 128 experts
 // (805 MB of B) 159 to 170 us, 5 TB/s; down of 65536 rows in 256 groups (N = 4096, K = 1536; 4.0 GB, 4.9 by the L2's
 // misses) 1.2 ms, in 128 x 256 tiles through three slots (two slots of 256 x 256 1.38, and 1.36 with tiles numbered
@@ -205,9 +202,8 @@ __global__ __launch_bounds__(64 * S::NW) void k_gemm16_tile(Gemm16 a, int n_tile
     // the row indices of tile t into s_rows[buf] (past its end: the last one again)
     auto issue_rows = [&](const ListedTile& t, int buf) {
         if (!a.rows || wave * 64 >= S::BM) return;
-        static_assert(S::BM <= 64 * S::NW, "one index a thread");
+        static_assert(S::BM % 64 == 0 && S::BM <= 64 * S::NW, "one index a thread, whole waves");
         const int at = wave * 64 + lane, last = t.m1 - 1 - t.m0;
-        if (S::BM < 64 && lane >= S::BM) return;
         g2lds4(a.rows + t.m0 + (at < last ? at : last), lds0 + S::kRowsOff + (buf * S::BM + wave * 64) * 4);
     };
 
@@ -413,19 +409,6 @@ __global__ __launch_bounds__(64 * S::NW) void k_gemm16_tile(Gemm16 a, int n_tile
 // out at a time, and add up through LDS in wave order.  What bounds it is B's bytes, read once: gate/up of one token,
 // 8 experts (N = 768, K = 2048, 50 MB) 13 us, 3.8 TB/s; one row of 4096 x 4096 7.7 us, 4.3 TB/s.
 constexpr int kFewWaves = 8;
-
-typedef float v4f __attribute__((ext_vector_type(4)));
-
-// The operands as in mfma16, 16 rows of each: lane group g = lane / 16 takes 8 values of K and gets four
-// consecutive columns of row lane % 16.
-template <int kIn>
-__device__ __forceinline__ v4f mfma16x16(v4i w, v4i x, v4f c)
-{
-    if constexpr (kIn == kBF16)
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, w), __builtin_bit_cast(v8bf, x), c, 0, 0, 0);
-    else
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, w), __builtin_bit_cast(v8h, x), c, 0, 0, 0);
-}
 
 // kR row tiles; kN tiles of 16 rows of B (SwiGLU: half of them gate, half up); from tile x0 and column tile y0 on
 template <int kIn, int kT, bool kSwiglu, int kR, int kN>

@@ -12,27 +12,12 @@
 
 #include "moe_dtype.h"
 #include "moe_lora.h"
+#include "moe_mfma16.h"
 #include "moe_tile.h"
 
 namespace moe {
 
 namespace {
-
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-typedef _Float16 v8h __attribute__((ext_vector_type(8)));
-typedef float v4f __attribute__((ext_vector_type(4)));
-
-// First operand: adapter rows, lane i = lane % 16 holds one; second: rows of x (or of s).  Lane
-// group g = lane / 16 takes 8 values of the summed dimension and gets four consecutive results of
-// row i of the second operand.
-template <int kIn>
-__device__ __forceinline__ v4f mfma16x16(v4i w, v4i x, v4f c)
-{
-    if constexpr (kIn == kBF16)
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, w), __builtin_bit_cast(v8bf, x), c, 0, 0, 0);
-    else
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, w), __builtin_bit_cast(v8h, x), c, 0, 0, 0);
-}
 
 constexpr int kLoraWaves = 4, kLoraThreads = 64 * kLoraWaves;
 constexpr int kOneWaves = 8;              // of the launch that makes s itself
@@ -135,9 +120,6 @@ __global__ __launch_bounds__(kLoraThreads) void k_lora_down_few(LoraAdd l, int p
         }
     });
 }
-
-// What a chunk past the end of K is loaded from.
-__device__ const uint4 kZeros = {0, 0, 0, 0};
 
 // Many rows.  A workgroup: 32 WR rows by 16 WC TC ranks, a wave 32 by 16 TC of them; one part of K in
 // stages of 64 values (128 bytes a row, a cache line) through four LDS slots, three stages' loads out at a
