@@ -935,14 +935,25 @@ hipError_t launch_up_ring(const LoraAdd& l, int parts, hipStream_t st)
     return hipSuccess;
 }
 
-template <int kIn, int kP, int kKS>
-hipError_t launch_up_ranks(const LoraAdd& l, int parts, int ways, hipStream_t st)
+// whole vectors of 8 columns at aligned addresses
+bool wide_rows(const LoraAdd& l)
 {
-    // whole vectors of 8 columns at aligned addresses
     auto even = [&](const void* p, int64_t stride, int type) {
         return (reinterpret_cast<uintptr_t>(p) | (uint64_t)(stride * dtype_bytes(type))) % 16 == 0;
     };
-    const bool wide = l.N % 8 == 0 && even(l.out, l.out_stride, l.out_type) && (!l.base || even(l.base, l.base_stride, l.base_type));
+    return l.N % 8 == 0 && even(l.out, l.out_stride, l.out_type) && (!l.base || even(l.base, l.base_stride, l.base_type));
+}
+// values a lane of k_lora_up_few
+int few_vector(const LoraAdd& l)
+{
+    const int base = l.base ? dtype_bytes(l.base_type) : 0, out = dtype_bytes(l.out_type);
+    return !wide_rows(l) || (out == 2 && l.out_type != l.in_type) || (base == 2 && l.base_type != l.in_type) ? 1 : base == 4 || out == 4 ? 4 : 8;
+}
+
+template <int kIn, int kP, int kKS>
+hipError_t launch_up_ranks(const LoraAdd& l, int parts, int ways, hipStream_t st)
+{
+    const bool wide = wide_rows(l);
     const int base = l.base ? dtype_bytes(l.base_type) : 0, out = dtype_bytes(l.out_type);
     const bool types = (out == 4 || l.out_type == kIn) && (base != 2 || l.base_type == kIn);
     if (!lora_few(l.M) && wide && types && (!l.base || l.base_stride * base <= 1 << 25)) {
@@ -954,7 +965,7 @@ hipError_t launch_up_ranks(const LoraAdd& l, int parts, int ways, hipStream_t st
             return base == 0 ? launch_up_ring<kIn, kP, kKS, 0, 2>(l, parts, st) : base == 2 ? launch_up_ring<kIn, kP, kKS, 2, 2>(l, parts, st)
                                                                                            : launch_up_ring<kIn, kP, kKS, 4, 2>(l, parts, st);
     }
-    const int v = !wide || (out == 2 && l.out_type != kIn) || (base == 2 && l.base_type != kIn) ? 1 : base == 4 || out == 4 ? 4 : 8;
+    const int v = few_vector(l);
     const unsigned tiles = nblk(l.M, 16);
     const int64_t blocks = nblk(l.N, 64 * kLoraWaves), want = (1024 + tiles - 1) / tiles;
     int cols = (int)((blocks + want - 1) / want) * 64 * kLoraWaves, threads = kLoraThreads;
@@ -1005,9 +1016,11 @@ hipError_t launch_typed(const LoraAdd& l, hipStream_t st)
     const int ways = l.M <= 512 ? (l.M < 16 ? (int)l.M : 16) : lora_few(l.M) ? 4 : 1;
     // One launch where its workgroups read A and x again for less than another launch takes (4096 x 4096, rank 16: 1 row
     // 8.9 us against 11.1 of two, 16 rows of 16 adapters 13.0, 13.7, 64 rows 24, 17; 2048 x 2048: 64 rows 10.9, 13.3); its
-    // registers hold 32 ranks (of 64 31 us against 11 for one row).
-    const int64_t again = (int64_t)nblk(l.M, 16) * ways * nblk(l.N, 64 * kOneWaves) * (l.r + (l.M < 16 ? l.M : 16)) * l.K * 2;
-    const bool one = lora_few(l.M) && l.r <= 32 && again <= (int64_t)48 << 20;
+    // registers hold 32 ranks (of 64 31 us against 11 for one row).  Beside rows in fp32 vectors more than 16 ranks spill 10
+    // to 20, and are worth one launch of short reads alone (rank 32, 1, 16 and 48 rows: K = 512 8.0, 8.5, 9.1 us against 10.7 of two,
+    // 1184 8.0, 9.3, 10.9, 2048 10.6, 13.1, 14.4, 4096 14.6, 19.0, -; rank 24, 1 row, 2048 9.6).
+    const int64_t reads = (l.r + (l.M < 16 ? l.M : 16)) * l.K * 2, again = (int64_t)nblk(l.M, 16) * ways * nblk(l.N, 64 * kOneWaves) * reads;
+    const bool one = lora_few(l.M) && l.r <= 32 && again <= (int64_t)48 << 20 && (l.r <= 16 || few_vector(l) != 4 || reads <= 1 << 17);
     const int parts = one ? 0 : lora_parts(l.M, l.K, l.r);
     const hipError_t e = one ? hipSuccess : l.r <= 16 ? launch_down<kIn, 4, 1, 1>(l, parts, ways, st) : l.r <= 32 ? launch_down<kIn, 4, 1, 2>(l, parts, ways, st)
                                                                                                                : launch_down<kIn, 2, 2, 2>(l, parts, ways, st);
