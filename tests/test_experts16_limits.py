@@ -19,6 +19,7 @@ int main()
     std::printf("[");
     const long long sizes[][6] = {SIZES};                 // M, N, K, groups (0: dense), swiglu, bytes from a row of B to the next
     for (auto& s : sizes) {
+        std::printf("%s[\"case\"]", sep), sep = ", ";
         moe::Gemm16 g{};
         g.a = g.b = none, g.out = none;
         g.a_rows = g.M = s[0], g.N = (int)s[1], g.K = (int)s[2], g.row_div = 1, g.swiglu = (int)s[4], g.out_stride = s[1];
@@ -30,19 +31,29 @@ int main()
     return 0;
 }
 """
+LARGEST = [(1 << 27, 2, 8, 0, 0, 1 << 25), (1 << 27, 256, 8, 0, 0, 1 << 25), (1 << 27, 100, 8, 65535, 1, 1 << 25), (1 << 27, 256, 8, 0, 0, 0),
+           (1 << 27, 32, 8, 65535, 0, 0), (1, 1 << 20, 8, 0, 1, 0), (24, 1 << 20, 64, 300, 1, 0), (4, 1 << 20, 8, 0, 0, 0), (1000, 1 << 20, 64, 0, 0, 1 << 25)]
 
 
-@pytest.mark.parametrize("M,N,K,G,swiglu,b_stride", [
-    (1 << 27, 2, 8, 0, 0, 1 << 25), (1 << 27, 256, 8, 0, 0, 1 << 25), (1 << 27, 100, 8, 65535, 1, 1 << 25), (1 << 27, 256, 8, 0, 0, 0), (1 << 27, 32, 8, 65535, 0, 0),
-    (1, 1 << 20, 8, 0, 1, 0), (24, 1 << 20, 64, 300, 1, 0), (4, 1 << 20, 8, 0, 0, 0), (1000, 1 << 20, 64, 0, 0, 1 << 25)])
-def test_launches_hold_the_largest_calls(tmp_path, M, N, K, G, swiglu, b_stride):
+def launches_of(at, sizes):
+    """The launches of each of the sizes, in their order."""
+    out = []
+    for e in record(at, "moe_gemm16.h", "moe_gemm16_bf16.hip", LAUNCHES.replace("SIZES", ", ".join("{%d, %d, %d, %d, %d, %d}" % s for s in sizes))):
+        if e[0] == "case":
+            out.append([])
+        elif e[0] == "launch":
+            out[-1].append(e)
+    assert len(out) == len(sizes)
+    return out
+
+
+def test_launches_hold_the_largest_calls(tmp_path):
     """Fewer than 2^32 threads along x and 65536 workgroups along y in every launch; few-row launches cover all tiles."""
-    events = record(tmp_path, "moe_gemm16.h", "moe_gemm16_bf16.hip", LAUNCHES.replace("SIZES", "{%d, %d, %d, %d, %d, %d}" % (M, N, K, G, swiglu, b_stride)))
-    launches = [e for e in events if e[0] == "launch"]
-    assert launches and all(gx * threads < 1 << 32 and gy < 65536 for _, _, _, gx, gy, threads in launches)
-    if launches[0][2] == 0:                               # no dynamic LDS: the few-row kernel
-        tiles = {(rows, cols): min(M, M // rows + G if G else -(-M // rows)) * -(-N // cols) for rows in (16, 32) for cols in (16, 32)}
-        assert sum(gx * gy for _, _, _, gx, gy, _ in launches) in tiles.values()
+    for (M, N, K, G, swiglu, b_stride), launches in zip(LARGEST, launches_of(tmp_path, LARGEST)):
+        assert launches and all(gx * threads < 1 << 32 and gy < 65536 for _, _, _, gx, gy, threads in launches), (M, N, G)
+        if launches[0][2] == 0:                           # no dynamic LDS: the few-row kernel
+            tiles = [min(M, M // rows + G if G else -(-M // rows)) * -(-N // cols) for rows in (16, 32) for cols in (16, 32)]
+            assert sum(gx * gy for _, _, _, gx, gy, _ in launches) in tiles, (M, N, G)
 
 
 @gpu
@@ -71,8 +82,13 @@ def test_the_most_rows_by_the_few_row_kernel():
         assert ((out[i:i + (1 << 24)].double() - want).abs() <= err + 2.0 ** -8 * (want.abs() + err)).all()
 
 
-TABLES = LAUNCHES.replace("{SIZES};                 // M, N, K, groups (0: dense), swiglu, bytes from a row of B to the next",
-                          "{SIZES};  // M, N, K, rows of A, by a table, top_k").split("moe::Gemm16 g{};")[0] + r"""
+TABLES = r"""
+int main()
+{
+    static uint8_t none[256];
+    std::printf("[");
+    const long long sizes[][6] = {SIZES};                 // M, N, K, rows of A, by a table, top_k
+    for (auto& s : sizes) {
         moe::Gemm16 g{};
         g.a = g.b = none, g.out = none;
         g.M = s[0], g.N = (int)s[1], g.K = (int)s[2], g.a_rows = s[3], g.rows = s[4] ? reinterpret_cast<const int32_t*>(none) : nullptr, g.row_div = (int)s[5];

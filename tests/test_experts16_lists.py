@@ -6,8 +6,7 @@ import pytest
 import torch
 
 import moe_prefill_ffn_amd as mp
-from launch_recorder import record
-from test_experts16_limits import LAUNCHES
+from test_experts16_limits import launches_of
 
 gpu = pytest.mark.gpu
 # M, N, K, groups (0: dense), rows of a tile
@@ -15,9 +14,7 @@ CASES = [(17_200_011, 32, 8, 0, 128), (16_900_000, 24, 128, 0, 128), (16_900_123
 
 
 def test_these_sizes_take_several_lists(tmp_path):
-    main = LAUNCHES.replace("SIZES", ", ".join("{%d, %d, %d, %d, 0, 0}" % c[:4] for c in CASES))
-    launches = [e for e in record(tmp_path, "moe_gemm16.h", "moe_gemm16_bf16.hip", main) if e[0] == "launch"]
-    for (M, N, K, G, rows), (_, _, lds, grid, _, threads) in zip(CASES, launches):
+    for (M, N, K, G, rows), [(_, _, lds, grid, _, threads)] in zip(CASES, launches_of(tmp_path, [c[:4] + (0, 0) for c in CASES])):
         assert threads == 256 and M // rows > 256 * grid, (M, N, K, G, grid, lds)
 
 
