@@ -226,7 +226,7 @@ __global__ __launch_bounds__(kLoraThreads) void k_lora_down(LoraAdd l, int parts
 // [2^14, 2^15), as two parts, the second, what the first left, times 2^12 and its products' sum times 2^-12: 2^-22 of a
 // value lost, or 2^-16 where the output has 16 bits anyway, if the value is within `width` (29, or 35) powers of two of the
 // largest.  A smaller one is multiplied by 2^width until it is, and belongs to the window of that number, whose product
-// product_long makes apart (of normal values some 2^-28, or 2^-34).  Sums of products of fp16 numbers span 100 powers of
+// product_long makes apart (of normally distributed values some 2^-28, or 2^-34).  Sums of products of fp16 numbers span 100 powers of
 // two, which four windows hold.
 constexpr int fp16_width(bool out32) { return out32 ? 29 : 35; }
 constexpr float kSecond = 0x1p12f;                        // fp16: what the second part is multiplied by
